@@ -10,6 +10,7 @@ Importing this package raises if ``libpq2.so`` has not been built
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -21,7 +22,7 @@ LIB_PATH = os.path.join(_HERE, "libpq2.so")
 
 GROUP = 128
 PATH_AUTO, PATH_GEMV, PATH_SMALL, PATH_PREFILL, PATH_PANEL = 0, 1, 2, 3, 4
-ACT_BF16, ACT_F16 = 1, 2
+ACT_F32, ACT_BF16, ACT_F16 = 0, 1, 2
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python gemm_pq2_w2a8_amd/build.py`")
@@ -38,6 +39,10 @@ lib.pq2_quantize_act.restype = ctypes.c_int
 lib.pq2_quantize_act.argtypes = [_P, _P, _P, _P, _I64, _I64, _P]
 lib.pq2_quantize_act_16.restype = ctypes.c_int
 lib.pq2_quantize_act_16.argtypes = [_P, ctypes.c_int, _P, _P, _P, _I64, _I64, _P]
+_F32 = ctypes.c_float
+lib.pq2_norm_quantize.restype = ctypes.c_int
+lib.pq2_norm_quantize.argtypes = [_P, ctypes.c_int, _P, _P, _P, _I64, _F32, _P, _F32, _P, _P, _P,
+                                  _P, _P, _I64, _I64, _P]
 _SZ = ctypes.c_size_t
 lib.pq2_gemm_workspace_bytes.restype = _SZ
 lib.pq2_gemm_workspace_bytes.argtypes = [_I64, _I64, _I64]
@@ -65,6 +70,7 @@ LINEAR_MAX_M = 16   # PQ2_LINEAR_MAX_M
 
 # Every extern "C" symbol declared in include/pq2.h.
 ABI_SYMBOLS = ("pq2_abi_version", "pq2_status_str", "pq2_quantize_act", "pq2_quantize_act_16",
+               "pq2_norm_quantize",
                "pq2_gemm_workspace_bytes", "pq2_gemm", "pq2_gemm_noalloc", "pq2_gemm_bf16",
                "pq2_gemm_kernel_path", "pq2_gemm_path", "pq2_linear", "pq2_linear_workspace_bytes",
                "pq2_linear_kernel_path", "pq2_gemm_group_dots")
@@ -139,6 +145,41 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape: Tuple[int, ...]
         raise ValueError(f"{name} must be contiguous")
 
 
+def _ptr(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: Tuple[int, ...],
+         device: torch.device) -> int:
+    """Address of a contiguous tensor of this type and shape on `device` (0 for
+    None); raises what _need raises, and ValueError for another device."""
+    if t is None:
+        return 0
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda
+            and t.is_contiguous()):
+        _need(t, name, dtype, shape)
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t.data_ptr()
+
+
+def _launch_on(device: torch.device):
+    """Context in which a launch goes to `device` (a kernel runs on the current
+    device, which need not be the tensors')."""
+    if torch.cuda.current_device() == device.index:
+        return _HERE_ALREADY
+    return torch.cuda.device(device)
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+_ACT_FORMAT = {torch.float32: ACT_F32, torch.bfloat16: ACT_BF16, torch.float16: ACT_F16}
+
+
+def _format(x: torch.Tensor, name: str) -> int:
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    fmt = _ACT_FORMAT.get(x.dtype)
+    if fmt is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {x.dtype}")
+    return fmt
+
+
 def _mk(x: torch.Tensor) -> Tuple[int, int]:
     if x.dim() != 2:
         raise ValueError("expected a 2-D tensor")
@@ -163,6 +204,45 @@ def pq2_quantize_act(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, t: torch
     _need(x, "x", torch.float32, (M, K))
     _check(lib.pq2_quantize_act(x.data_ptr(), q.data_ptr(), s.data_ptr(), t.data_ptr(), M, K,
                                 _stream(x, stream)))
+
+
+def pq2_norm_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None,
+                      s: Optional[torch.Tensor] = None, t: Optional[torch.Tensor] = None, *,
+                      residual: Optional[torch.Tensor] = None,
+                      w_post: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                      alpha: float = 1.0, w_pre: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                      h: Optional[torch.Tensor] = None, n: Optional[torch.Tensor] = None,
+                      stream=None) -> None:
+    """The norms after and before a block with its gate and residual scale,
+    ending in the quantiser:
+
+        h = residual + alpha * gate * (rms(x) * w_post),   n = rms(h) * w_pre,
+        q, s, t = pq2_quantize_act's of n
+
+    x, residual, h, n [M][K] and gate [rows][K] (rows dividing M; [K] is one
+    row) share x's type (float32, bfloat16 or float16); w_post, w_pre float32
+    [K]; q, s, t as for pq2_quantize_act, all or none. Whatever is None is left
+    out; h may be residual or x."""
+    fmt = _format(x, "x")
+    M, K = _mk(x)
+    G = K // GROUP
+    ty, dev = x.dtype, x.device
+    xp = _ptr(x, "x", ty, (M, K), dev)
+    gate_rows = 0
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor) or gate.dim() not in (1, 2):
+            raise ValueError("gate must be a 1-D or 2-D tensor")
+        gate_rows = 1 if gate.dim() == 1 else int(gate.shape[0])
+        gate = gate.view(1, -1) if gate.dim() == 1 else gate
+    args = (xp, fmt, _ptr(residual, "residual", ty, (M, K), dev),
+            _ptr(w_post, "w_post", torch.float32, (K,), dev),
+            _ptr(gate, "gate", ty, (gate_rows, K), dev), gate_rows, alpha,
+            _ptr(w_pre, "w_pre", torch.float32, (K,), dev), eps, _ptr(h, "h", ty, (M, K), dev),
+            _ptr(n, "n", ty, (M, K), dev), _ptr(q, "q", torch.int8, (M, K), dev),
+            _ptr(s, "s", torch.float32, (M, G), dev), _ptr(t, "t", torch.int32, (M, G), dev), M, K,
+            _stream(x, stream))
+    with _launch_on(dev):
+        _check(lib.pq2_norm_quantize(*args))
 
 
 def _workspace(workspace, M: int, N: int, K: int, device, stream,
@@ -304,6 +384,23 @@ def quantize_act(x: torch.Tensor, stream=None):
     t = torch.empty((M, G), dtype=torch.int32, device=x.device)
     pq2_quantize_act(x, q, s, t, stream)
     return q, s, t
+
+
+def norm_quantize(x: torch.Tensor, *, residual: Optional[torch.Tensor] = None,
+                  w_post: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                  alpha: float = 1.0, w_pre: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                  stream=None):
+    """Allocate h and q/s/t with torch and run pq2_norm_quantize: (h, q, s, t)."""
+    _format(x, "x")
+    M, K = _mk(x)
+    G = K // GROUP
+    h = torch.empty_like(x)
+    q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    s = torch.empty((M, G), dtype=torch.float32, device=x.device)
+    t = torch.empty((M, G), dtype=torch.int32, device=x.device)
+    pq2_norm_quantize(x, q, s, t, residual=residual, w_post=w_post, gate=gate, alpha=alpha,
+                      w_pre=w_pre, eps=eps, h=h, stream=stream)
+    return h, q, s, t
 
 
 def linear(x: torch.Tensor, codes: torch.Tensor, wscale: torch.Tensor,

@@ -22,6 +22,8 @@ pq2_status check_mnk(int64_t M, int64_t N, int64_t K) {
     return PQ2_OK;
 }
 
+bool finite32(float v) { return v - v == 0.0f; }
+
 pq2_status from_hip(hipError_t e) { return e == hipSuccess ? PQ2_OK : PQ2_ERR_HIP; }
 
 // K chunks the caller's workspace allows the panel kernel: S chunks need
@@ -171,6 +173,26 @@ pq2_status pq2_quantize_act_16(const uint16_t *x, int x_format, int8_t *q, float
     if (x_format != PQ2_ACT_BF16 && x_format != PQ2_ACT_F16) return PQ2_ERR_ARG;
     return from_hip(pq2::launch_quantize(x, x_format, q, s, t, M, K,
                                          static_cast<hipStream_t>(hip_stream)));
+}
+
+pq2_status pq2_norm_quantize(const void *x, int x_format, const void *residual,
+                             const float *w_post, const void *gate, int64_t gate_rows, float alpha,
+                             const float *w_pre, float eps, void *h, void *n, int8_t *q, float *s,
+                             int32_t *t, int64_t M, int64_t K, void *hip_stream) {
+    if (!x || (!h && !n && !q) || !q != !s || !q != !t) return PQ2_ERR_NULL;
+    pq2_status st = check_mnk(M, 1, K);
+    if (st != PQ2_OK) return st;
+    if (gate ? (gate_rows < 1 || M % gate_rows != 0) : gate_rows != 0) return PQ2_ERR_SHAPE;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(w_post, 16) || !aligned(gate, 16) ||
+        !aligned(w_pre, 16) || !aligned(h, 16) || !aligned(n, 16) || !aligned(q, 16) ||
+        !aligned(s, 4) || !aligned(t, 4))
+        return PQ2_ERR_ALIGN;
+    if (x_format != PQ2_ACT_F32 && x_format != PQ2_ACT_BF16 && x_format != PQ2_ACT_F16)
+        return PQ2_ERR_ARG;
+    if (!(eps > 0.0f) || !finite32(eps) || !finite32(alpha)) return PQ2_ERR_ARG;
+    const pq2::NormArgs a{x, residual, w_post, gate, gate ? M / gate_rows : 1, alpha, w_pre, eps,
+                          h, n, q, s, t, M, K};
+    return from_hip(pq2::launch_norm_quantize(a, x_format, static_cast<hipStream_t>(hip_stream)));
 }
 
 size_t pq2_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {

@@ -24,6 +24,24 @@ int device_cus();
 hipError_t launch_quantize(const void *x, int format, int8_t *q, float *s, int32_t *t,
                            int64_t M, int64_t K, hipStream_t stream);
 
+// pq2_norm_quantize (arguments as in the header; gate row of row m:
+// m / rows_per_gate). h may be x or residual itself.
+struct NormArgs {
+    const void *x, *residual;    // [M][K]
+    const float *w_post;         // [K] or nullptr
+    const void *gate;            // [M / rows_per_gate][K] or nullptr
+    int64_t rows_per_gate;
+    float alpha;
+    const float *w_pre;          // [K] or nullptr
+    float eps;
+    void *h, *n;                 // [M][K] or nullptr
+    int8_t *q;                   // [M][K] or nullptr (then s and t too)
+    float *s;
+    int32_t *t;
+    int64_t M, K;
+};
+hipError_t launch_norm_quantize(const NormArgs &a, int format, hipStream_t stream);
+
 // The dot4 GEMV runs 1 to kGemvMaxM token rows.
 constexpr int64_t kGemvMaxM = 4;
 

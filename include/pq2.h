@@ -129,6 +129,42 @@ pq2_status pq2_quantize_act_16(const uint16_t *x, int x_format, int8_t *q, float
                                int64_t M, int64_t K, void *hip_stream);
 
 /*
+ * The norms after and before a block, with the block's gate and residual
+ * scale, ending in the quantiser -- the step between one block's output and
+ * the next projection's activations in one launch. With
+ * rms(v) = v / sqrt(mean(v^2) + eps) over a row, per row m:
+ *   p = w_post ? rms(x) * w_post : x
+ *   h = residual + alpha * gate * p     (without residual: alpha * gate * p;
+ *                                        without gate: alpha * p)
+ *   n = w_pre ? rms(h) * w_pre : h
+ *   q, s, t = pq2_quantize_act's rule on n
+ * All of it in float32 (16-bit inputs are widened exactly): h and n are
+ * rounded, to nearest even, only where they are stored, n is formed from the
+ * unrounded h and quantised unrounded. Weights that are kept as offsets from
+ * one are passed with the one added. |x| and |h| must be finite and small
+ * enough for their squares to sum in float32.
+ *   x_format  PQ2_ACT_F32, PQ2_ACT_BF16 or PQ2_ACT_F16: the type of x,
+ *             residual, gate, h and n (else PQ2_ERR_ARG);
+ *   x         [M][K]; residual [M][K] or NULL;
+ *   w_post, w_pre  float32 [K] or NULL (that norm is left out);
+ *   gate      [gate_rows][K] or NULL (then gate_rows must be 0). gate_rows
+ *             divides M (else PQ2_ERR_SHAPE) and row m takes gate row
+ *             m / (M / gate_rows): 1 is one gate for every row, M one each;
+ *   alpha     finite; eps > 0 and finite (else PQ2_ERR_ARG);
+ *   h, n      [M][K] or NULL (not stored). h may be residual or x itself
+ *             (updated in place); any other overlap is not allowed;
+ *   q, s, t   as for pq2_quantize_act, all three or none.
+ * At least one of h, n and q must be given (else PQ2_ERR_NULL). Every base
+ * is 16-byte aligned, s and t 4-byte. Results depend on the row alone, bit
+ * for bit, whatever M is.
+ */
+#define PQ2_ACT_F32 0
+pq2_status pq2_norm_quantize(const void *x, int x_format, const void *residual,
+                             const float *w_post, const void *gate, int64_t gate_rows, float alpha,
+                             const float *w_pre, float eps, void *h, void *n, int8_t *q, float *s,
+                             int32_t *t, int64_t M, int64_t K, void *hip_stream);
+
+/*
  * Device workspace, in bytes, that pq2_gemm (and pq2_gemm_bf16) needs to run
  * its fastest plan for this shape: the persistent small-batch kernel splits
  * K into S chunks for some shapes (K = 17408 at 3..16 token rows: S = 3;
