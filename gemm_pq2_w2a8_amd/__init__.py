@@ -59,6 +59,9 @@ lib.pq2_gemm_path.argtypes = [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, ctypes.c
                               _P]
 lib.pq2_gemm_group_dots.restype = ctypes.c_int
 lib.pq2_gemm_group_dots.argtypes = [_P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int, _P]
+lib.pq2_gemm_grouped.restype = ctypes.c_int
+lib.pq2_gemm_grouped.argtypes = [_P, _P, _P, _I64, _P, _P, _P, _I64, _P, _P, _P, ctypes.c_int,
+                                 _I64, _I64, _I64, _P]
 lib.pq2_linear.restype = ctypes.c_int
 lib.pq2_linear.argtypes = [_P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]
 lib.pq2_linear_workspace_bytes.restype = _SZ
@@ -70,7 +73,7 @@ LINEAR_MAX_M = 16   # PQ2_LINEAR_MAX_M
 
 # Every extern "C" symbol declared in include/pq2.h.
 ABI_SYMBOLS = ("pq2_abi_version", "pq2_status_str", "pq2_quantize_act", "pq2_quantize_act_16",
-               "pq2_norm_quantize",
+               "pq2_norm_quantize", "pq2_gemm_grouped",
                "pq2_gemm_workspace_bytes", "pq2_gemm", "pq2_gemm_noalloc", "pq2_gemm_bf16",
                "pq2_gemm_kernel_path", "pq2_gemm_path", "pq2_linear", "pq2_linear_workspace_bytes",
                "pq2_linear_kernel_path", "pq2_gemm_group_dots")
@@ -338,6 +341,39 @@ def pq2_gemm_path(q: torch.Tensor, s: torch.Tensor, t: torch.Tensor, codes: torc
     _check(lib.pq2_gemm_path(q.data_ptr(), s.data_ptr(), t.data_ptr(), codes.data_ptr(),
                              wscale.data_ptr(), y.data_ptr(), M, N, K, int(path), wp, wn,
                              _stream(q, stream)))
+
+
+def pq2_gemm_grouped(q: torch.Tensor, s: torch.Tensor, t: torch.Tensor, codes: torch.Tensor,
+                     wscale: torch.Tensor, offsets: torch.Tensor, y: torch.Tensor,
+                     rows: Optional[torch.Tensor] = None,
+                     row_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """y [T][N] (float32 or bfloat16): slot i of expert e (offsets[e] <= i <
+    offsets[e + 1]) = row_scale[i] * the PQ2_0 product of activation row rows[i]
+    of plane-order q/s/t [R] and codes[e], wscale[e].
+
+    codes uint8 [E][N][K/4], wscale [E][N][G], offsets int32 [E + 1] on the
+    device, rows int32 [T] (None: row i; a row outside [0, R) gives zeros),
+    row_scale float32 [T] or None. Slots behind offsets[E] are left alone."""
+    R, K = _mk(q)
+    G = K // GROUP
+    if codes.dim() != 3 or y.dim() != 2:
+        raise ValueError("expected 3-D codes and 2-D y")
+    E, N, T = int(codes.shape[0]), int(codes.shape[1]), int(y.shape[0])
+    dev = q.device
+    if y.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"y must be float32 or bfloat16, got {y.dtype}")
+    if wscale.dtype == torch.float16:
+        wscale = wscale.view(torch.int16)
+    args = (_ptr(q, "q", torch.int8, (R, K), dev), _ptr(s, "s", torch.float32, (R, G), dev),
+            _ptr(t, "t", torch.int32, (R, G), dev), R,
+            _ptr(codes, "codes", torch.uint8, (E, N, K // 4), dev),
+            _ptr(wscale, "wscale", torch.int16, (E, N, G), dev),
+            _ptr(offsets, "offsets", torch.int32, (E + 1,), dev), E,
+            _ptr(rows, "rows", torch.int32, (T,), dev),
+            _ptr(row_scale, "row_scale", torch.float32, (T,), dev),
+            _ptr(y, "y", y.dtype, (T, N), dev), _ACT_FORMAT[y.dtype], T, N, K, _stream(q, stream))
+    with _launch_on(dev):
+        _check(lib.pq2_gemm_grouped(*args))
 
 
 def pq2_linear(x: torch.Tensor, codes: torch.Tensor, wscale: torch.Tensor, y: torch.Tensor,

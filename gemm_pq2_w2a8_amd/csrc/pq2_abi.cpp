@@ -308,6 +308,31 @@ pq2_status pq2_linear(const float *x, const uint8_t *codes, const uint16_t *wsca
     }
 }
 
+pq2_status pq2_gemm_grouped(const int8_t *q, const float *s, const int32_t *t, int64_t R,
+                            const uint8_t *codes, const uint16_t *wscale, const int32_t *offsets,
+                            int64_t E, const int32_t *rows, const float *row_scale, void *y,
+                            int y_format, int64_t T, int64_t N, int64_t K, void *hip_stream) {
+    if (T == 0) return PQ2_OK;
+    if (!q || !s || !t || !codes || !wscale || !offsets || !y) return PQ2_ERR_NULL;
+    if (E < 1 || E > PQ2_GROUPED_MAX_E || T < 0 || T > PQ2_GROUPED_MAX_T || N > PQ2_GROUPED_MAX_N)
+        return PQ2_ERR_SHAPE;
+    pq2_status st = check_mnk(R, N, K);
+    if (st == PQ2_OK) st = check_mnk(T, N, K);
+    if (st == PQ2_OK) st = check_mnk(1, E * N, K);
+    if (st != PQ2_OK) return st;
+    if (!rows && R < T) return PQ2_ERR_SHAPE;
+    if (y_format != PQ2_ACT_F32 && y_format != PQ2_ACT_BF16) return PQ2_ERR_ARG;
+    if (!aligned(q, 16) || !aligned(codes, 16) || !aligned(s, 4) || !aligned(t, 4) ||
+        !aligned(wscale, 2) || !aligned(offsets, 4) || !aligned(rows, 4) ||
+        !aligned(row_scale, 4) || !aligned(y, y_format == PQ2_ACT_F32 ? 4 : 2))
+        return PQ2_ERR_ALIGN;
+    const bool f32 = y_format == PQ2_ACT_F32;
+    const pq2::GroupedArgs a{q, s, t, R, codes, wscale, offsets, E, rows, row_scale,
+                             f32 ? static_cast<float *>(y) : nullptr,
+                             f32 ? nullptr : static_cast<uint16_t *>(y), T, N, K};
+    return from_hip(pq2::launch_grouped(a, static_cast<hipStream_t>(hip_stream)));
+}
+
 pq2_status pq2_gemm_group_dots(const int8_t *q, const int32_t *t, const uint8_t *codes,
                                int32_t *d, int64_t M, int64_t N, int64_t K, int path,
                                void *hip_stream) {

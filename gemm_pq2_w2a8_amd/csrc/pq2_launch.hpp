@@ -42,6 +42,24 @@ struct NormArgs {
 };
 hipError_t launch_norm_quantize(const NormArgs &a, int format, hipStream_t stream);
 
+// pq2_gemm_grouped (arguments as in the header; y or y16, the other nullptr).
+struct GroupedArgs {
+    const int8_t *q;             // [R][K]
+    const float *s;              // [R][G]
+    const int32_t *t;            // [R][G]
+    int64_t R;
+    const uint8_t *codes;        // [E][N][K / 4]
+    const uint16_t *ws;          // [E][N][G]
+    const int32_t *offsets;      // [E + 1]
+    int64_t E;
+    const int32_t *rows;         // [T] or nullptr
+    const float *row_scale;      // [T] or nullptr
+    float *y;                    // [T][N]
+    uint16_t *y16;
+    int64_t T, N, K;
+};
+hipError_t launch_grouped(const GroupedArgs &a, hipStream_t stream);
+
 // The dot4 GEMV runs 1 to kGemvMaxM token rows.
 constexpr int64_t kGemvMaxM = 4;
 

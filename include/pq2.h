@@ -261,6 +261,41 @@ pq2_status pq2_gemm_bf16(const int8_t *q, const float *s, const int32_t *t,
                          void *workspace, size_t workspace_bytes, void *hip_stream);
 
 /*
+ * Products grouped by expert with ragged sizes: E weight matrices of one
+ * shape, each multiplying its own run of the T slots. Slot i belongs to the
+ * expert e with offsets[e] <= i < offsets[e + 1] and takes activation row
+ * rows[i] (row i without rows), so activations are quantised once per token
+ * and read by every expert the token goes to:
+ *   y[i][n] = row_scale[i] * sum_g s[row][g] * wscale[e][n][g] * D
+ * with D the exact group dot of pq2_gemm (int32) and the same float32 epilogue;
+ * without row_scale no factor. The sizes are read on the device: nothing has to
+ * be known on the host, and a captured graph may be replayed with others.
+ *   q, s, t    as for pq2_gemm, R rows;
+ *   codes      uint8 [E][N][K/4], wscale [E][N][G], as for pq2_gemm;
+ *   offsets    int32 [E + 1], non-decreasing, within [0, T]. Experts may have
+ *              no slots. Slots before offsets[0] or from offsets[E] on are left
+ *              as they were. Other contents are clamped into range: y is
+ *              unspecified then, but nothing outside [0, T) is touched;
+ *   rows       int32 [T], or NULL (then R >= T). A row outside [0, R) marks a
+ *              slot without activations: its y is zero;
+ *   row_scale  float32 [T] (a router's weights), or NULL;
+ *   y          [T][N], PQ2_ACT_F32 (4-byte aligned) or PQ2_ACT_BF16 bit patterns
+ *              (2-byte; the float32 result rounded to nearest even), by
+ *              y_format (else PQ2_ERR_ARG).
+ * T = 0 returns PQ2_OK and does nothing. PQ2_ERR_SHAPE: E outside 1 ..
+ * PQ2_GROUPED_MAX_E, T above PQ2_GROUPED_MAX_T, N above PQ2_GROUPED_MAX_N, the
+ * limits of pq2_gemm for R, T, N, K, or E*N above PQ2_MAX_DIM or E*N*K/4 above
+ * PQ2_MAX_ELEMS. No workspace; repeated calls give identical y.
+ */
+#define PQ2_GROUPED_MAX_E 4096
+#define PQ2_GROUPED_MAX_T (1LL << 24)
+#define PQ2_GROUPED_MAX_N (1LL << 20)
+pq2_status pq2_gemm_grouped(const int8_t *q, const float *s, const int32_t *t, int64_t R,
+                            const uint8_t *codes, const uint16_t *wscale, const int32_t *offsets,
+                            int64_t E, const int32_t *rows, const float *row_scale, void *y,
+                            int y_format, int64_t T, int64_t N, int64_t K, void *hip_stream);
+
+/*
  * Quantise and multiply without the separate quantiser launch, for decode
  * batches of 1 to 16 token rows (PQ2_LINEAR_MAX_M): y = the PQ2_0 product of
  * x quantised exactly as pq2_quantize_act would (page "Making a ternary
