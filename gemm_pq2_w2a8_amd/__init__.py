@@ -62,6 +62,11 @@ lib.pq2_gemm_group_dots.argtypes = [_P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_i
 lib.pq2_gemm_grouped.restype = ctypes.c_int
 lib.pq2_gemm_grouped.argtypes = [_P, _P, _P, _I64, _P, _P, _P, _I64, _P, _P, _P, ctypes.c_int,
                                  _I64, _I64, _I64, _P]
+lib.pq2_lora_add.restype = ctypes.c_int
+lib.pq2_lora_add.argtypes = [_P, ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, _P, _P, _P,
+                             ctypes.c_int, _I64, _I64, _I64, _I64, _I64, _P, _SZ, _P]
+lib.pq2_lora_workspace_bytes.restype = _SZ
+lib.pq2_lora_workspace_bytes.argtypes = [_I64, _I64, _I64]
 lib.pq2_linear.restype = ctypes.c_int
 lib.pq2_linear.argtypes = [_P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]
 lib.pq2_linear_workspace_bytes.restype = _SZ
@@ -73,7 +78,7 @@ LINEAR_MAX_M = 16   # PQ2_LINEAR_MAX_M
 
 # Every extern "C" symbol declared in include/pq2.h.
 ABI_SYMBOLS = ("pq2_abi_version", "pq2_status_str", "pq2_quantize_act", "pq2_quantize_act_16",
-               "pq2_norm_quantize", "pq2_gemm_grouped",
+               "pq2_norm_quantize", "pq2_gemm_grouped", "pq2_lora_add", "pq2_lora_workspace_bytes",
                "pq2_gemm_workspace_bytes", "pq2_gemm", "pq2_gemm_noalloc", "pq2_gemm_bf16",
                "pq2_gemm_kernel_path", "pq2_gemm_path", "pq2_linear", "pq2_linear_workspace_bytes",
                "pq2_linear_kernel_path", "pq2_gemm_group_dots")
@@ -92,6 +97,11 @@ def gemm_workspace_bytes(M: int, N: int, K: int) -> int:
 def linear_workspace_bytes(M: int, N: int, K: int) -> int:
     """Workspace bytes of pq2_linear's plan for this shape (0: none needed)."""
     return int(lib.pq2_linear_workspace_bytes(M, N, K))
+
+
+def lora_workspace_bytes(M: int, K: int, R: int) -> int:
+    """Workspace bytes of pq2_lora_add's fastest plan for this shape."""
+    return int(lib.pq2_lora_workspace_bytes(M, K, R))
 
 
 def linear_kernel_path(M: int, N: int, K: int, workspace_bytes: Optional[int] = None) -> int:
@@ -374,6 +384,42 @@ def pq2_gemm_grouped(q: torch.Tensor, s: torch.Tensor, t: torch.Tensor, codes: t
             _ptr(y, "y", y.dtype, (T, N), dev), _ACT_FORMAT[y.dtype], T, N, K, _stream(q, stream))
     with _launch_on(dev):
         _check(lib.pq2_gemm_grouped(*args))
+
+
+def pq2_lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter: torch.Tensor,
+                 y: torch.Tensor, base: Optional[torch.Tensor] = None,
+                 ranks: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                 workspace="auto", stream=None) -> None:
+    """y[m] = base[m] + scale[l] * b[l] @ (a[l] @ x[m]) with l = adapter[m]; rows
+    whose adapter is outside [0, L) copy their base.
+
+    x [M][K] float32, bfloat16 or float16; a [L][R][K], b [L][N][R] bfloat16 or
+    float16; adapter int32 [M]; ranks int32 [L] (None: R), scale float32 [L]
+    (None: 1); y and base [M][N] float32 or bfloat16, base None or y itself for
+    an addition in place. workspace: "auto" (torch allocates) or a device
+    tensor of lora_workspace_bytes(M, K, R) bytes (at least M * R floats)."""
+    fmt = _format(x, "x")
+    M, K = _mk(x)
+    dev = x.device
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError("expected 3-D a and b")
+    if a.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"a must be bfloat16 or float16, got {a.dtype}")
+    if y.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"y must be float32 or bfloat16, got {y.dtype}")
+    L, R, N = int(a.shape[0]), int(a.shape[1]), int(b.shape[1])
+    args = (_ptr(x, "x", x.dtype, (M, K), dev), fmt, _ptr(a, "a", a.dtype, (L, R, K), dev),
+            _ptr(b, "b", a.dtype, (L, N, R), dev), _ACT_FORMAT[a.dtype],
+            _ptr(adapter, "adapter", torch.int32, (M,), dev),
+            _ptr(ranks, "ranks", torch.int32, (L,), dev),
+            _ptr(scale, "scale", torch.float32, (L,), dev),
+            _ptr(base, "base", y.dtype, (M, N), dev), _ptr(y, "y", y.dtype, (M, N), dev),
+            _ACT_FORMAT[y.dtype], M, N, K, R, L)
+    wp, wn, _keep = _workspace(workspace, M, K, R, dev, stream, lora_workspace_bytes)
+    if _keep is not None and _keep.device != dev:
+        raise ValueError(f"workspace must be on {dev}, got {_keep.device}")
+    with _launch_on(dev):
+        _check(lib.pq2_lora_add(*args, wp, wn, _stream(x, stream)))
 
 
 def pq2_linear(x: torch.Tensor, codes: torch.Tensor, wscale: torch.Tensor, y: torch.Tensor,

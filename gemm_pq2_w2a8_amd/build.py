@@ -22,7 +22,7 @@ PROBE_LIB = os.path.join(HERE, "libpq2_probe.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["pq2_abi.cpp", "quantize.hip", "norm_quantize.hip", "gemv_dot4.hip", "small_mfma.hip",
-           "small_panel.hip", "prefill_mfma.hip", "grouped.hip"]
+           "small_panel.hip", "prefill_mfma.hip", "grouped.hip", "lora.hip"]
 PROBE_SOURCES = ["probe.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

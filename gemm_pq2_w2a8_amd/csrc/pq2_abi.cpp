@@ -120,6 +120,16 @@ pq2_status check_gemm(const int8_t *q, const float *s, const int32_t *t, const u
     return PQ2_OK;
 }
 
+// Shapes of pq2_lora_add.
+pq2_status check_lora(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
+    if (M > PQ2_LORA_MAX_M || N > PQ2_LORA_MAX_N || L < 1 || L > PQ2_LORA_MAX_L || R < 8 ||
+        R > PQ2_LORA_MAX_R || R % 8 != 0)
+        return PQ2_ERR_SHAPE;
+    const pq2_status st = check_mnk(M, N, K);
+    if (st != PQ2_OK) return st;
+    return L * R * K > PQ2_MAX_ELEMS || L * R * N > PQ2_MAX_ELEMS ? PQ2_ERR_SHAPE : PQ2_OK;
+}
+
 // Kernel of pq2_linear: the fused dot4 GEMV for one or two token rows (it
 // reads only the real rows) and, without a ring plan, for three or four;
 // the fused ring variant of the panel kernel for 3 to 16 rows where it has
@@ -148,7 +158,7 @@ const char *pq2_status_str(int status) {
         case PQ2_ERR_ALIGN: return "PQ2_ERR_ALIGN: a base pointer is misaligned";
         case PQ2_ERR_HIP: return "PQ2_ERR_HIP: the HIP runtime rejected a launch";
         case PQ2_ERR_ARG: return "PQ2_ERR_ARG: invalid path selector for this shape and workspace, no fused kernel of pq2_linear for this shape and workspace, or unknown activation format";
-        case PQ2_ERR_SCRATCH: return "PQ2_ERR_SCRATCH: the shape needs more split-K scratch than pq2_gemm_noalloc holds (PQ2_NOALLOC_SCRATCH_BYTES)";
+        case PQ2_ERR_SCRATCH: return "PQ2_ERR_SCRATCH: the shape needs more split-K scratch than pq2_gemm_noalloc holds (PQ2_NOALLOC_SCRATCH_BYTES), or pq2_lora_add more workspace than it was given";
         default: return "PQ2 unknown status";
     }
 }
@@ -331,6 +341,36 @@ pq2_status pq2_gemm_grouped(const int8_t *q, const float *s, const int32_t *t, i
                              f32 ? static_cast<float *>(y) : nullptr,
                              f32 ? nullptr : static_cast<uint16_t *>(y), T, N, K};
     return from_hip(pq2::launch_grouped(a, static_cast<hipStream_t>(hip_stream)));
+}
+
+size_t pq2_lora_workspace_bytes(int64_t M, int64_t K, int64_t R) {
+    if (check_lora(M, 1, K, R, 1) != PQ2_OK) return 0;
+    return pq2::lora_workspace_bytes(M, K, R);
+}
+
+pq2_status pq2_lora_add(const void *x, int x_format, const void *a, const void *b, int w_format,
+                        const int32_t *adapter, const int32_t *ranks, const float *scale,
+                        const void *base, void *y, int y_format, int64_t M, int64_t N, int64_t K,
+                        int64_t R, int64_t L, void *workspace, size_t workspace_bytes,
+                        void *hip_stream) {
+    if (!x || !a || !b || !adapter || !y) return PQ2_ERR_NULL;
+    const pq2_status st = check_lora(M, N, K, R, L);
+    if (st != PQ2_OK) return st;
+    if ((x_format != PQ2_ACT_F32 && x_format != PQ2_ACT_BF16 && x_format != PQ2_ACT_F16) ||
+        (w_format != PQ2_ACT_BF16 && w_format != PQ2_ACT_F16) ||
+        (y_format != PQ2_ACT_F32 && y_format != PQ2_ACT_BF16))
+        return PQ2_ERR_ARG;
+    const uintptr_t ya = y_format == PQ2_ACT_F32 ? 4 : 2;
+    if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(adapter, 4) ||
+        !aligned(ranks, 4) || !aligned(scale, 4) || !aligned(base, ya) || !aligned(y, ya) ||
+        !aligned(workspace, 16))
+        return PQ2_ERR_ALIGN;
+    if (!workspace || workspace_bytes / sizeof(float) < (uint64_t)M * (uint64_t)R)
+        return PQ2_ERR_SCRATCH;
+    const pq2::LoraArgs args{x, a, b, adapter, ranks, scale, base ? base : y, y, M, N, K, R, L};
+    return from_hip(pq2::launch_lora(args, x_format, w_format, y_format,
+                                     static_cast<float *>(workspace), workspace_bytes,
+                                     static_cast<hipStream_t>(hip_stream)));
 }
 
 pq2_status pq2_gemm_group_dots(const int8_t *q, const int32_t *t, const uint8_t *codes,

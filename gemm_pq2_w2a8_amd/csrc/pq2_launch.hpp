@@ -60,6 +60,23 @@ struct GroupedArgs {
 };
 hipError_t launch_grouped(const GroupedArgs &a, hipStream_t stream);
 
+// pq2_lora_add (arguments as in the header; base is never nullptr here).
+struct LoraArgs {
+    const void *x;               // [M][K]
+    const void *a, *b;           // [L][R][K], [L][N][R]
+    const int32_t *adapter;      // [M]
+    const int32_t *ranks;        // [L] or nullptr
+    const float *scale;          // [L] or nullptr
+    const void *base;            // [M][N], may be y
+    void *y;                     // [M][N]
+    int64_t M, N, K, R, L;
+};
+// Bytes of the shrink's sums for the K chunks the plan takes; work holds them
+// (work_bytes of at least M * R floats: fewer chunks where it is smaller).
+size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t R);
+hipError_t launch_lora(const LoraArgs &a, int x_format, int w_format, int y_format, float *work,
+                       size_t work_bytes, hipStream_t stream);
+
 // The dot4 GEMV runs 1 to kGemvMaxM token rows.
 constexpr int64_t kGemvMaxM = 4;
 

@@ -50,7 +50,8 @@
  *                and workspace no fused kernel of pq2_linear runs, or an
  *                unknown activation format (pq2_quantize_act_16);
  *  PQ2_ERR_SCRATCH (pq2_gemm_noalloc) the small-batch plan's split-K partial
- *                sums need more than PQ2_NOALLOC_SCRATCH_BYTES;
+ *                sums need more than PQ2_NOALLOC_SCRATCH_BYTES; (pq2_lora_add)
+ *                the workspace holds fewer than M * R floats;
  *  PQ2_ERR_HIP   a kernel launch was rejected by the HIP runtime.
  * Nothing is enqueued when a status other than PQ2_OK is returned, except for
  * PQ2_ERR_HIP. A fault during execution surfaces at the caller's next
@@ -294,6 +295,52 @@ pq2_status pq2_gemm_grouped(const int8_t *q, const float *s, const int32_t *t, i
                             const uint8_t *codes, const uint16_t *wscale, const int32_t *offsets,
                             int64_t E, const int32_t *rows, const float *row_scale, void *y,
                             int y_format, int64_t T, int64_t N, int64_t K, void *hip_stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection: row m of a
+ * batch adds the product of its own adapter l = adapter[m] to the projection's
+ * output,
+ *   y[m] = base[m] + scale[l] * B[l] (A[l] x[m]),
+ * where A and B are 16-bit matrices of rank ranks[l] and x the projection's
+ * unquantised input. Both products are accumulated in float32 and A x stays
+ * float32 between them; y is rounded once. Rows may have any adapters in any
+ * order; rows with the same one next to each other share its reads.
+ *   x        [M][K] of x_format (PQ2_ACT_F32, PQ2_ACT_BF16, PQ2_ACT_F16);
+ *   a, b     [L][R][K] and [L][N][R] of w_format (PQ2_ACT_BF16, PQ2_ACT_F16);
+ *            R a multiple of 8, the room of the largest rank;
+ *   adapter  int32 [M]; a row whose adapter is outside [0, L) has none: its
+ *            base is copied to y, bit for bit;
+ *   ranks    int32 [L], clamped into [0, R], or NULL (all R): rows of A and
+ *            columns of B from ranks[l] on have no influence whatever they hold;
+ *   scale    float32 [L], or NULL (1);
+ *   base, y  [M][N] of y_format (PQ2_ACT_F32, 4-byte aligned, or PQ2_ACT_BF16
+ *            bit patterns, 2-byte); base NULL or the same as y adds in place;
+ *   x, a, b  are 16-byte aligned, x finite (a row that is not affects itself
+ *            alone, and so does an adapter that is not);
+ *   workspace, workspace_bytes  device memory for A x, 16-byte aligned: at
+ *            least M * R floats (else PQ2_ERR_SCRATCH), in
+ *            pq2_lora_workspace_bytes(M, K, R) bytes the fastest plan runs.
+ *            Calls that may overlap need workspaces of their own.
+ * PQ2_ERR_SHAPE: the limits of pq2_gemm for M, N, K, M above PQ2_LORA_MAX_M, N
+ * above PQ2_LORA_MAX_N, L outside 1 .. PQ2_LORA_MAX_L, R not a multiple of 8 in
+ * 8 .. PQ2_LORA_MAX_R, or A or B above PQ2_MAX_ELEMS elements. PQ2_ERR_ARG: an
+ * unknown format. Repeated calls give identical y.
+ */
+#define PQ2_LORA_MAX_M (1LL << 24)
+#define PQ2_LORA_MAX_N (1LL << 20)
+#define PQ2_LORA_MAX_L (1LL << 20)
+#define PQ2_LORA_MAX_R 256
+pq2_status pq2_lora_add(const void *x, int x_format, const void *a, const void *b, int w_format,
+                        const int32_t *adapter, const int32_t *ranks, const float *scale,
+                        const void *base, void *y, int y_format, int64_t M, int64_t N, int64_t K,
+                        int64_t R, int64_t L, void *workspace, size_t workspace_bytes,
+                        void *hip_stream);
+
+/*
+ * Workspace bytes of pq2_lora_add's fastest plan for this shape (0 for a bad
+ * one). Pure host query.
+ */
+size_t pq2_lora_workspace_bytes(int64_t M, int64_t K, int64_t R);
 
 /*
  * Quantise and multiply without the separate quantiser launch, for decode
