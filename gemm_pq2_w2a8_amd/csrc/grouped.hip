@@ -7,77 +7,12 @@
 // number of row tiles any offsets can give and every wave finds its own tile
 // (find_tile); blocks past the last tile end at once.
 #include "pq2_device.hpp"
+#include "pq2_grouped.hpp"
 #include "pq2_launch.hpp"
 
 namespace pq2 {
 
 namespace {
-
-// Row tile of a block: slots [first, first + count) of expert e.
-struct RowTile {
-    int e, first, count;
-};
-
-// The b-th tile of bm slots over all experts, in expert order; false when
-// there are fewer. Every lane of the wave takes a run of experts, counts its
-// tiles and scans the counts over the wave. Offsets are clamped into [0, T]
-// and to be non-decreasing pairwise, so no slot outside [0, T) is ever named;
-// a lane's count is capped (2^24, above any count valid offsets give) so that
-// the scan of any input stays in 32 bits.
-__device__ __forceinline__ bool find_tile(const int32_t *__restrict__ offsets, int E, int T, int bm,
-                                          int b, RowTile &tile) {
-    const int lane = threadIdx.x & (kWave - 1);
-    const int per = (E + kWave - 1) / kWave;
-    const int e0 = lane * per;
-    auto range = [&](int e, int &lo, int &hi) __attribute__((always_inline)) {
-        lo = min(max(offsets[e], 0), T);
-        hi = min(max(offsets[e + 1], lo), T);
-    };
-    int sum = 0;
-    for (int k = 0; k < per; ++k) {
-        if (e0 + k >= E) break;
-        int lo, hi;
-        range(e0 + k, lo, hi);
-        sum = min(sum + (hi - lo + bm - 1) / bm, 1 << 24);
-    }
-    int incl = sum;
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-        const int v = __shfl_up(incl, d, kWave);
-        if (lane >= d) incl += v;
-    }
-    int rest = b - (incl - sum);
-    const uint64_t mine = __ballot(rest >= 0 && rest < sum);
-    if (mine == 0) return false;
-    const int src = __builtin_ctzll(mine);
-    RowTile t{0, 0, 0};
-    if (lane == src) {
-        for (int k = 0; k < per; ++k) {
-            if (e0 + k >= E) break;
-            int lo, hi;
-            range(e0 + k, lo, hi);
-            const int tiles = (hi - lo + bm - 1) / bm;
-            if (rest < tiles) {
-                t.e = e0 + k;
-                t.first = lo + rest * bm;
-                t.count = min(hi - t.first, bm);
-                break;
-            }
-            rest -= tiles;
-        }
-    }
-    tile.e = __builtin_amdgcn_readlane(t.e, src);
-    tile.first = __builtin_amdgcn_readlane(t.first, src);
-    tile.count = __builtin_amdgcn_readlane(t.count, src);
-    return tile.count > 0;
-}
-
-// Tiles of bm slots that T slots of E experts can form at most: every expert
-// with slots has one partly filled tile, the others are full.
-int64_t max_tiles(int64_t T, int64_t E, int64_t bm) {
-    const int64_t some = T < E ? T : E;
-    return some + (T - some) / bm;
-}
 
 // 16 slots x 64 columns, one wave per 16 columns, both operands from global
 // memory. Operand A of v_mfma_i32_16x16x64_i8 is the activations (slots =
@@ -87,24 +22,17 @@ int64_t max_tiles(int64_t T, int64_t E, int64_t bm) {
 // which plane order keeps together.
 __global__ __launch_bounds__(256) void grouped_small_kernel(GroupedArgs p) {
     RowTile tile;
-    if (!find_tile(p.offsets, (int)p.E, (int)p.T, 16, blockIdx.x, tile)) return;
+    if (!TileScan(p.offsets, (int)p.E, (int)p.T, 16).find(blockIdx.x, tile)) return;
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int r = lane & 15, c = lane >> 4;
     const int64_t n0 = ((int64_t)blockIdx.y * 4 + wave) * 16;
     if (n0 >= p.N) return;
     const int G = (int)(p.K / kGroup);
     const int64_t KB = p.K / 4;
-    // activation row of a slot of the tile, or -1: no activations
-    auto source = [&](int slot) __attribute__((always_inline)) -> int64_t {
-        if (slot >= tile.count) return -1;
-        const int64_t i = tile.first + slot;
-        const int64_t row = p.rows ? (int64_t)p.rows[i] : i;
-        return row >= 0 && row < p.R ? row : -1;
-    };
-    const int64_t row_a = source(r);
+    const int64_t row_a = source_row(p, tile, r);
     int64_t row_d[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) row_d[i] = source(4 * c + i);
+    for (int i = 0; i < 4; ++i) row_d[i] = source_row(p, tile, 4 * c + i);
     const int64_t n = n0 + r < p.N ? n0 + r : p.N - 1;
     const uint8_t *codes = p.codes + (tile.e * p.N + n) * KB + 16 * (c & 1);
     const uint16_t *ws = p.ws + (tile.e * p.N + n) * G;
@@ -151,6 +79,7 @@ __global__ __launch_bounds__(256) void grouped_small_kernel(GroupedArgs p) {
 }  // namespace
 
 hipError_t launch_grouped(const GroupedArgs &a, hipStream_t stream) {
+    if (grouped_wide_fits(a)) return launch_grouped_wide(a, stream);
     const dim3 grid((unsigned)max_tiles(a.T, a.E, 16), (unsigned)((a.N + 63) / 64));
     hipLaunchKernelGGL(grouped_small_kernel, grid, dim3(256), 0, stream, a);
     return hipGetLastError();

@@ -59,6 +59,9 @@ struct GroupedArgs {
     int64_t T, N, K;
 };
 hipError_t launch_grouped(const GroupedArgs &a, hipStream_t stream);
+// The wide prefill tiles over the experts' slots, and whether they pay there.
+bool grouped_wide_fits(const GroupedArgs &a);
+hipError_t launch_grouped_wide(const GroupedArgs &a, hipStream_t stream);
 
 // pq2_lora_add (arguments as in the header; base is never nullptr here).
 struct LoraArgs {

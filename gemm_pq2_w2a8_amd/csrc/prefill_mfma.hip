@@ -38,7 +38,10 @@
 //    the 8 XCDs) gets a contiguous run of tiles along N for the same token
 //    panel, which then stays in that XCD's L2.
 #include "pq2_device.hpp"
+#include "pq2_grouped.hpp"
 #include "pq2_launch.hpp"
+
+#include <type_traits>
 
 namespace pq2 {
 
@@ -758,13 +761,20 @@ __global__ __launch_bounds__(256) void wide_tail_sum_kernel(const float *__restr
     store_y(y, y16, m * N + n, acc);
 }
 
-template <bool DOTS, int WM_>
+// GROUPED: the rows are the slots of experts (pq2_gemm_grouped). A block finds
+// its expert and slots from the offsets, each slot's activation row is gathered
+// through the copies' per-lane offsets (rows that do not exist read zeros), and
+// the row scale is applied at the store; M is the number of slots then and sp
+// unused. The blocks past the last tile end at once, the others are numbered
+// over the XCDs as below by the number of tiles there really are.
+template <bool DOTS, int WM_, bool GROUPED = false>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
 void prefill_wide_kernel(const int8_t *__restrict__ q, const float *__restrict__ s,
                          const int32_t *__restrict__ t, const uint8_t *__restrict__ codes,
                          const uint16_t *__restrict__ ws, float *__restrict__ y,
                          uint16_t *__restrict__ y16, int32_t *__restrict__ d, int64_t M,
-                         int64_t N, int64_t K, WideSplit sp) {
+                         int64_t N, int64_t K, WideSplit sp,
+                         std::conditional_t<GROUPED, GroupedArgs, int> grp) {
     using L = PfWide<DOTS, WM_>;
     constexpr int T = L::T, WN = L::WN, WM = L::WM;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -785,28 +795,54 @@ void prefill_wide_kernel(const int8_t *__restrict__ q, const float *__restrict__
     // order); slot sp.full + u runs K chunk u % sp.chunks (groups
     // chunk * sp.chunk_groups onward) of tile sp.full + u / sp.chunks and
     // leaves its partial sums in sp.part[u] ([BM][BN] float32).
-    int64_t tile;
+    int64_t n0, m0;
+    int toks;
     int g0 = 0, g1 = G;
     float *partial = nullptr;
-    if ((int64_t)blockIdx.x < sp.full) {
-        tile = xcd_tile(blockIdx.x, sp.full);
+    RowTile slots{0, 0, 0};
+    if constexpr (GROUPED) {
+        const TileScan scan(grp.offsets, (int)grp.E, (int)M, L::BM);
+        const int64_t blocks = scan.total * tiles_n;
+        if ((int64_t)blockIdx.x >= blocks) return;
+        const int64_t tile = xcd_tile(blockIdx.x, blocks);
+        if (!scan.find((int)(tile / tiles_n), slots)) return;
+        n0 = (tile % tiles_n) * L::BN;
+        m0 = slots.first;
+        toks = slots.count;
+        codes += slots.e * N * KB;
+        ws += slots.e * N * G;
     } else {
-        const int64_t u = (int64_t)blockIdx.x - sp.full;
-        tile = sp.full + u / sp.chunks;
-        g0 = (int)(u % sp.chunks) * sp.chunk_groups;
-        g1 = g0 + sp.chunk_groups < G ? g0 + sp.chunk_groups : G;
-        partial = sp.part + u * (L::BM * L::BN);
+        int64_t tile;
+        if ((int64_t)blockIdx.x < sp.full) {
+            tile = xcd_tile(blockIdx.x, sp.full);
+        } else {
+            const int64_t u = (int64_t)blockIdx.x - sp.full;
+            tile = sp.full + u / sp.chunks;
+            g0 = (int)(u % sp.chunks) * sp.chunk_groups;
+            g1 = g0 + sp.chunk_groups < G ? g0 + sp.chunk_groups : G;
+            partial = sp.part + u * (L::BM * L::BN);
+        }
+        n0 = (tile % tiles_n) * L::BN;
+        m0 = (tile / tiles_n) * L::BM;
+        toks = M - m0 < L::BM ? (int)(M - m0) : L::BM;
     }
-    const int64_t n0 = (tile % tiles_n) * L::BN;
-    const int64_t m0 = (tile / tiles_n) * L::BM;
     const int rows = N - n0 < L::BN ? (int)(N - n0) : L::BN;
-    const int toks = M - m0 < L::BM ? (int)(M - m0) : L::BM;
+    // activation rows of the tile, relative to the resources' base; -1: none
+    const int64_t first = GROUPED ? 0 : m0;
+    int64_t span = toks;
+    if constexpr (GROUPED) span = grp.R;
+    auto row_of = [&](int tok) __attribute__((always_inline)) -> int {
+        if constexpr (GROUPED)
+            return (int)source_row(grp, slots, tok);
+        else
+            return tok < toks ? tok : -1;
+    };
 
     const __amdgpu_buffer_rsrc_t rs_codes = make_rsrc(codes + n0 * KB, (int64_t)rows * KB);
-    const __amdgpu_buffer_rsrc_t rs_q = make_rsrc(q + m0 * K, (int64_t)toks * K);
-    const __amdgpu_buffer_rsrc_t rs_t = make_rsrc(t + m0 * G, (int64_t)toks * G * 4);
+    const __amdgpu_buffer_rsrc_t rs_q = make_rsrc(q + first * K, span * K);
+    const __amdgpu_buffer_rsrc_t rs_t = make_rsrc(t + first * G, span * G * 4);
     const __amdgpu_buffer_rsrc_t rs_ws = make_rsrc(DOTS ? nullptr : ws + n0 * G, DOTS ? 0 : (int64_t)rows * G * 2);
-    const __amdgpu_buffer_rsrc_t rs_s = make_rsrc(DOTS ? nullptr : s + m0 * G, DOTS ? 0 : (int64_t)toks * G * 4);
+    const __amdgpu_buffer_rsrc_t rs_s = make_rsrc(DOTS ? nullptr : s + first * G, DOTS ? 0 : span * G * 4);
 
     // Copy sources of group 0 (group g adds 32 g or 128 g through the SGPR
     // offset). Unit u of copy instruction i is i * T + tid; code unit
@@ -826,13 +862,15 @@ void prefill_wide_kernel(const int8_t *__restrict__ q, const float *__restrict__
         const int u = i * T + tid;
         const int tok = u >> 3;
         const int piece = (u & 7) ^ (tok & 7);
-        qoff[i] = tok < toks ? tok * (int)K + 16 * piece : kCopyOob;
+        const int row = row_of(tok);
+        qoff[i] = row >= 0 ? row * (int)K + 16 * piece : kCopyOob;
     }
     // scale chunk c: ws unit tid = row tid, groups 8c .. 8c + 7 (byte offset
     // 2 (row G + 8c)); s / t unit tid = token tid / 2, groups 8c + 4 (tid & 1)
     // .. + 3 (byte offset 4 (token G + 8c + 4 (tid & 1)))
     const int wsoff = tid < rows ? 2 * tid * G : kCopyOob;
-    const int tokoff = (tid >> 1) < toks ? 4 * ((tid >> 1) * G + 4 * (tid & 1)) : kCopyOob;
+    const int tokrow = (tid >> 1) < L::BM ? row_of(tid >> 1) : -1;
+    const int tokoff = tokrow >= 0 ? 4 * (tokrow * G + 4 * (tid & 1)) : kCopyOob;
 
     auto issue_stage = [&](int g, uint8_t *st) __attribute__((always_inline)) {
 #pragma unroll
@@ -1012,7 +1050,14 @@ void prefill_wide_kernel(const int8_t *__restrict__ q, const float *__restrict__
 #pragma unroll
         for (int b = 0; b < WM; ++b) {
             const int64_t m = m0 + 16 * b + r;
-            if (m >= M) continue;
+            if (16 * b + r >= toks) continue;
+            if constexpr (GROUPED) {
+                const float f = grp.row_scale ? grp.row_scale[m] : 1.0f;
+#pragma unroll
+                for (int a = 0; a < WN; ++a)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[a][b][i] *= f;
+            }
 #pragma unroll
             for (int a = 0; a < WN; ++a) {
                 const int64_t nb = n0 + row_base + 16 * a + 4 * lg;
@@ -1082,7 +1127,7 @@ hipError_t launch_wide_dots(const int8_t *q, const int32_t *t, const uint8_t *co
     hipLaunchKernelGGL((prefill_wide_kernel<DOTS, WM>), dim3((unsigned)blocks), dim3(L::T),
                        (size_t)L::kLdsBytes, stream, q, DOTS ? nullptr : out.s, t, codes,
                        DOTS ? nullptr : out.ws, DOTS ? nullptr : out.y,
-                       DOTS ? nullptr : out.y16, DOTS ? out.d : nullptr, M, N, K, sp);
+                       DOTS ? nullptr : out.y16, DOTS ? out.d : nullptr, M, N, K, sp, 0);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || DOTS || sp.chunks == 1) return e;
     hipLaunchKernelGGL(wide_tail_sum_kernel<L::BM>, dim3((unsigned)((T - sp.full) * L::BM)),
@@ -1206,6 +1251,34 @@ int prefill_cfg(int64_t M, int64_t N, int64_t K) {
 }
 
 }  // namespace
+
+bool grouped_wide_fits(const GroupedArgs &a) {
+    const int64_t G = a.K / kGroup, some = a.T < a.E ? a.T : a.E;
+    // scale chunks of eight groups; gathered rows within 31-bit offsets
+    if (G % 8 != 0 || a.R * a.K >= kCopyOob || a.R * G * 4 >= kCopyOob || a.K > 65536) return false;
+    if (max_tiles(a.T, a.E, 64) * ((a.N + kWideBN - 1) / kWideBN) >= (int64_t(1) << 24)) return false;
+    return a.T >= 32 * some;
+}
+
+namespace {
+
+template <int WM>
+hipError_t launch_grouped_wide_as(const GroupedArgs &a, hipStream_t stream) {
+    using L = PfWide<false, WM>;
+    const int64_t blocks = max_tiles(a.T, a.E, L::BM) * ((a.N + L::BN - 1) / L::BN);
+    hipLaunchKernelGGL((prefill_wide_kernel<false, WM, true>), dim3((unsigned)blocks), dim3(L::T),
+                       (size_t)L::kLdsBytes, stream, a.q, a.s, a.t, a.codes, a.ws, a.y, a.y16,
+                       nullptr, a.T, a.N, a.K, WideSplit{}, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_grouped_wide(const GroupedArgs &a, hipStream_t stream) {
+    const int64_t some = a.T < a.E ? a.T : a.E;
+    return a.T >= 192 * some ? launch_grouped_wide_as<8>(a, stream)
+                             : launch_grouped_wide_as<4>(a, stream);
+}
 
 size_t prefill_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     const int cfg = prefill_cfg(M, N, K);

@@ -164,6 +164,9 @@ SHAPES = {
     "odd_groups": ([4, 30, 70], 129, 128 * 41),
     "wide": ([5, 0, 17], 2050, 256),
     "large_tiles": ([600, 0, 513, 255], 515, 640),
+    "tiles_of_64": ([40, 70, 33, 0, 64, 129], 300, 2048),
+    "tiles_of_128": ([600, 0, 513, 255, 1], 515, 1024),
+    "one_long": ([391], 257, 5120),
     "many_experts": ([i % 4 for i in range(200)], 17, 256),
     "over_4_per_lane": ([(i * 7) % 3 for i in range(700)], 16, 128),
 }
@@ -209,7 +212,8 @@ def test_random_shapes(seed):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("counts,N,K", [([3, 9, 0, 1], 50, 384), ([40, 9, 130], 70, 1024)])
+@pytest.mark.parametrize("counts,N,K", [([3, 9, 0, 1], 50, 384), ([40, 9, 130], 70, 1024),
+                                        ([500, 1], 300, 1024)])
 def test_rows_out_of_range_give_zeros(counts, N, K):
     p = Problem(counts, N, K, R=6, seed=4, weighted=True, invalid=True)
     p.check(p.run())
@@ -217,8 +221,8 @@ def test_rows_out_of_range_give_zeros(counts, N, K):
 
 @pytest.mark.gpu
 def test_slots_before_and_behind_are_left_alone():
-    for counts in ([2, 0, 3], [70, 20, 90]):
-        p = Problem(counts, 33, 256, R=4, seed=5, lead=5, spare=21)
+    for counts, K in (([2, 0, 3], 256), ([70, 20, 90], 256), ([70, 20, 90], 1024)):
+        p = Problem(counts, 33, K, R=4, seed=5, lead=5, spare=21)
         p.check(p.run())
     p = Problem([0, 0], 8, 128, R=4, seed=5, spare=9)          # no expert has a slot
     assert (p.run() == 7.0).all()
@@ -227,11 +231,12 @@ def test_slots_before_and_behind_are_left_alone():
 @pytest.mark.gpu
 @pytest.mark.parametrize("off", [[-5, 3, 999], [6, 2, 4], [0, 2 ** 31 - 1, -2 ** 31],
                                  [2 ** 31 - 1] * 3, [-2 ** 31] * 3])
-def test_bad_offsets_stay_inside(off):
+@pytest.mark.parametrize("T,K", [(10, 256), (200, 1024)])
+def test_bad_offsets_stay_inside(off, T, K):
     """Contents that are no offsets: whatever y then is, its guard rows keep
-    their values and the slots named properly are right."""
-    T, N, K = 10, 20, 256
-    p = Problem([5, 5], N, K, R=3, seed=6)
+    their values."""
+    N = 20
+    p = Problem([T // 2, T // 2], N, K, R=3, seed=6)
     d = p.device()
     d["offsets"] = torch.tensor(off, dtype=torch.int32, device="cuda")
     big = torch.full((T + 64, N), 7.0, device="cuda")
@@ -257,7 +262,12 @@ def test_one_expert_is_pq2_gemm(M):
 @pytest.mark.gpu
 def test_repeats_and_streams_and_graph_replays():
     """Identical y on repeats; a captured call replayed with other sizes."""
-    p = Problem([5, 0, 40, 3], 100, 640, R=12, seed=10, weighted=True)
+    repeats_and_streams_and_graph_replays(640, 1)
+    repeats_and_streams_and_graph_replays(1024, 10)
+
+
+def repeats_and_streams_and_graph_replays(K, times):
+    p = Problem([5 * times, 0, 40 * times, 3 * times], 100, K, R=12, seed=10, weighted=True)
     a = p.run()
     assert (a == p.run()).all()
     st = torch.cuda.Stream()
@@ -271,6 +281,7 @@ def test_repeats_and_streams_and_graph_replays():
     with torch.cuda.graph(graph):
         pq2.pq2_gemm_grouped(y=y, **d)
     for counts in ([48, 0, 0, 0], [1, 2, 3, 4], [0, 0, 0, 48], [16, 16, 0, 16]):
+        counts = [c * times for c in counts]
         off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
         d["offsets"].copy_(torch.from_numpy(off))
         y.fill_(7.0)
