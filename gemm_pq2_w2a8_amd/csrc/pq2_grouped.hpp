@@ -86,11 +86,40 @@ __device__ __forceinline__ int64_t source_row(const GroupedArgs &p, const RowTil
     return row >= 0 && row < p.R ? row : -1;
 }
 
+// Dispatch slot b of nb to tile: slot b runs on XCD b % 8, and XCD x receives
+// the x-th contiguous run of tile numbers.
+constexpr int kNumXcd = 8;
+
+__device__ __forceinline__ int64_t xcd_tile(int64_t b, int64_t nb) {
+    const int64_t xcd = b % kNumXcd, idx = b / kNumXcd;
+    const int64_t per = nb / kNumXcd, rem = nb % kNumXcd;
+    return xcd < rem ? xcd * (per + 1) + idx : rem * (per + 1) + (xcd - rem) * per + idx;
+}
+
+// The block's tile of BM slots x BN columns (columns fastest, numbered over the
+// XCDs by the number of tiles there really are): its slots and first column.
+// False: a block past the last tile.
+template <int BM, int BN>
+__device__ __forceinline__ bool grouped_tile(const GroupedArgs &p, RowTile &slots, int64_t &n0) {
+    const TileScan scan(p.offsets, (int)p.E, (int)p.T, BM);
+    const int64_t tiles_n = (p.N + BN - 1) / BN;
+    const int64_t blocks = scan.total * tiles_n;
+    if ((int64_t)blockIdx.x >= blocks) return false;
+    const int64_t tile = xcd_tile(blockIdx.x, blocks);
+    if (!scan.find((int)(tile / tiles_n), slots)) return false;
+    n0 = tile % tiles_n * BN;
+    return true;
+}
+
 // Tiles of bm slots that T slots of E experts can form at most: every expert
 // with slots has one partly filled tile, the others are full.
 inline int64_t max_tiles(int64_t T, int64_t E, int64_t bm) {
     const int64_t some = T < E ? T : E;
     return some + (T - some) / bm;
+}
+
+inline int64_t grouped_blocks(const GroupedArgs &a, int64_t bm, int64_t bn) {
+    return max_tiles(a.T, a.E, bm) * ((a.N + bn - 1) / bn);
 }
 
 }  // namespace pq2

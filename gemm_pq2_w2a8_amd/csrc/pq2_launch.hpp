@@ -59,9 +59,16 @@ struct GroupedArgs {
     int64_t T, N, K;
 };
 hipError_t launch_grouped(const GroupedArgs &a, hipStream_t stream);
-// The wide prefill tiles over the experts' slots, and whether they pay there.
-bool grouped_wide_fits(const GroupedArgs &a);
-hipError_t launch_grouped_wide(const GroupedArgs &a, hipStream_t stream);
+// The prefill tile kernels over the experts' slots.
+enum GroupedTile {
+    kGroupedRing64,      // 64 columns x 16 slots
+    kGroupedRing128,     // 128 x 16
+    kGroupedWide32,      // 256 x 32
+    kGroupedWide128,     // 256 x 128
+    kGroupedStaged32,    // 32 x 32, any number of groups
+    kGroupedStaged64     // 64 x 64, any number of groups
+};
+hipError_t launch_grouped_tiles(const GroupedArgs &a, GroupedTile tile, hipStream_t stream);
 
 // pq2_lora_add (arguments as in the header; base is never nullptr here).
 struct LoraArgs {

@@ -49,7 +49,6 @@ namespace {
 
 constexpr int kCodeStride = 48;          // LDS bytes per code row (32 + pad)
 constexpr int kQStride = 144;            // LDS bytes per token row (128 + pad)
-constexpr int kNumXcd = 8;
 // Scales are staged kScaleChunk groups at a time: lanes walk along the group
 // dimension of the [rows][G] scale arrays, so one load instruction touches a
 // few cache lines instead of one line per lane.
@@ -62,12 +61,29 @@ __device__ __forceinline__ float scale_product(float sv, _Float16 w) {
     return fmaf(sv, (float)w, 0.0f);
 }
 
-// Bijection from dispatch order to tile order: dispatch slot b runs on XCD
-// b % 8; XCD x receives the x-th contiguous run of tile numbers.
-__device__ __forceinline__ int64_t xcd_tile(int64_t b, int64_t nb) {
-    const int64_t xcd = b % kNumXcd, idx = b / kNumXcd;
-    const int64_t per = nb / kNumXcd, rem = nb % kNumXcd;
-    return xcd < rem ? xcd * (per + 1) + idx : rem * (per + 1) + (xcd - rem) * per + idx;
+// The last argument of a tile kernel: pq2_gemm_grouped's, or nothing.
+template <bool GROUPED>
+using GroupedOr = std::conditional_t<GROUPED, GroupedArgs, int>;
+
+// Activation row of token `tok` of a tile with `toks`, counted from the tile's
+// first row or, for the slots of an expert, from the first of all rows; -1:
+// none (its copies and loads read zeros).
+template <bool GROUPED>
+__device__ __forceinline__ int tile_row(const GroupedOr<GROUPED> &grp, const RowTile &slots,
+                                        int tok, int toks) {
+    if constexpr (GROUPED)
+        return (int)source_row(grp, slots, tok);
+    else
+        return tok < toks ? tok : -1;
+}
+
+// Factor of a tile row's outputs.
+template <bool GROUPED>
+__device__ __forceinline__ float row_factor(const GroupedOr<GROUPED> &grp, int64_t m) {
+    if constexpr (GROUPED)
+        return grp.row_scale ? grp.row_scale[m] : 1.0f;
+    else
+        return 1.0f;
 }
 
 template <int WN, int WM, int WAVES_N, int WAVES_M>
@@ -198,11 +214,12 @@ __device__ __forceinline__ void compute_group(const Stage &cur, const uint16_t *
     }
 }
 
-template <int WN, int WM, int WAVES_N, int WAVES_M, int DEPTH, bool DOTS>
+template <int WN, int WM, int WAVES_N, int WAVES_M, int DEPTH, bool DOTS, bool GROUPED = false>
 __global__ __launch_bounds__(64 * WAVES_N * WAVES_M) void prefill_mfma_kernel(
     const int8_t *__restrict__ q, const float *__restrict__ s, const int32_t *__restrict__ t,
     const uint8_t *__restrict__ codes, const uint16_t *__restrict__ ws, float *__restrict__ y,
-    uint16_t *__restrict__ y16, int32_t *__restrict__ d, int64_t M, int64_t N, int64_t K) {
+    uint16_t *__restrict__ y16, int32_t *__restrict__ d, int64_t M, int64_t N, int64_t K,
+    GroupedOr<GROUPED> grp) {
     using C = PfCfg<WN, WM, WAVES_N, WAVES_M>;
     using Stage = typename C::Stage;
     using Scales = typename C::Scales;
@@ -218,20 +235,45 @@ __global__ __launch_bounds__(64 * WAVES_N * WAVES_M) void prefill_mfma_kernel(
     const int G = (int)(K / kGroup);
     const int64_t KB = K / 4;                // code bytes per row
 
-    const int64_t tiles_n = (N + C::BN - 1) / C::BN;
-    const int64_t tiles_m = (M + C::BM - 1) / C::BM;
-    const int64_t tile = xcd_tile(blockIdx.x, tiles_n * tiles_m);
-    const int64_t n0 = (tile % tiles_n) * C::BN;
-    const int64_t m0 = (tile / tiles_n) * C::BM;
+    int64_t n0, m0, m_end = M;
+    RowTile slots{0, 0, 0};
+    if constexpr (GROUPED) {
+        if (!grouped_tile<C::BM, C::BN>(grp, slots, n0)) return;
+        codes += slots.e * N * KB;
+        ws += slots.e * N * G;
+        m0 = slots.first;
+        m_end = m0 + slots.count;
+    } else {
+        const int64_t tiles_n = (N + C::BN - 1) / C::BN;
+        const int64_t tiles_m = (M + C::BM - 1) / C::BM;
+        const int64_t tile = xcd_tile(blockIdx.x, tiles_n * tiles_m);
+        n0 = (tile % tiles_n) * C::BN;
+        m0 = (tile / tiles_n) * C::BM;
+    }
+    // first row and rows of the activation resources
+    const int64_t first = GROUPED ? 0 : m0;
+    int64_t span = M - m0;
+    if constexpr (GROUPED) span = grp.R;
+    // Offset of a token's data from the resource's base, `step` bytes a row.
+    // Tokens past the end are clamped to the last one (their results are never
+    // stored); slots without activations read zeros.
+    auto tok_off = [&](int tok, int64_t step) __attribute__((always_inline)) -> uint32_t {
+        if constexpr (GROUPED) {
+            const int row = (int)source_row(grp, slots, tok);
+            return row >= 0 ? (uint32_t)(row * step) : (uint32_t)kCopyOob;
+        } else {
+            return (uint32_t)((m0 + tok < M ? tok : M - 1 - m0) * step);
+        }
+    };
 
     // Buffer resources based at the block's first row and token; per-lane
     // 32-bit offsets (the host bounds K so that BN * K / 4 and BM * K fit in
     // 32 bits) and a uniform offset per group.
     const __amdgpu_buffer_rsrc_t rs_codes = make_rsrc(codes + n0 * KB, (N - n0) * KB);
-    const __amdgpu_buffer_rsrc_t rs_q = make_rsrc(q + m0 * K, (M - m0) * K);
-    const __amdgpu_buffer_rsrc_t rs_t = make_rsrc(t + m0 * G, (M - m0) * G * 4);
+    const __amdgpu_buffer_rsrc_t rs_q = make_rsrc(q + first * K, span * K);
+    const __amdgpu_buffer_rsrc_t rs_t = make_rsrc(t + first * G, span * G * 4);
     const __amdgpu_buffer_rsrc_t rs_ws = make_rsrc(DOTS ? nullptr : ws + n0 * G, DOTS ? 0 : (N - n0) * G * 2);
-    const __amdgpu_buffer_rsrc_t rs_s = make_rsrc(DOTS ? nullptr : s + m0 * G, DOTS ? 0 : (M - m0) * G * 4);
+    const __amdgpu_buffer_rsrc_t rs_s = make_rsrc(DOTS ? nullptr : s + first * G, DOTS ? 0 : span * G * 4);
 
     // staging assignment: chunk c of codes is (row c/2, half c%2); chunk c of
     // q is (token c/8, 16-byte piece c%8). Rows and tokens past the end are
@@ -254,8 +296,7 @@ __global__ __launch_bounds__(64 * WAVES_N * WAVES_M) void prefill_mfma_kernel(
         int c = tid + i * C::kThreads;
         if (c >= C::kQChunks) c = C::kQChunks - 1;
         const int tok = c >> 3, piece = c & 7;
-        const int64_t rel = (m0 + tok < M) ? tok : M - 1 - m0;
-        q_off[i] = (uint32_t)(rel * K + 16 * piece);
+        q_off[i] = tok_off(tok, K) + 16 * piece;
         q_dst[i] = tok * kQStride + 16 * piece;
     }
     // scale-chunk assignment: element e = tid + i * kThreads is (row or token
@@ -265,6 +306,12 @@ __global__ __launch_bounds__(64 * WAVES_N * WAVES_M) void prefill_mfma_kernel(
     static_assert(C::kThreads % kScaleChunk == 0, "scale chunk layout");
     constexpr int kRowStep = C::kThreads / kScaleChunk;
     const int sc_j = tid % kScaleChunk, sc_row = tid / kScaleChunk;
+    uint32_t slot_off[C::kStPer];            // s and t of the thread's slots
+#pragma unroll
+    for (int i = 0; i < C::kStPer; ++i) {
+        const int tok = sc_row + i * kRowStep;
+        slot_off[i] = GROUPED ? tok_off(tok < C::BM ? tok : C::BM - 1, 4 * (int64_t)G) : 0;
+    }
     // Staging loads are never predicated (groups past the end are clamped to
     // the last group), which keeps their registers out of scratch memory and
     // the wait counts exact; only the LDS writes of ragged chunk counts are.
@@ -298,7 +345,8 @@ __global__ __launch_bounds__(64 * WAVES_N * WAVES_M) void prefill_mfma_kernel(
             int tok = sc_row + i * kRowStep;                                        \
             tok = tok < C::BM ? tok : C::BM - 1;                                    \
             tok = m0 + tok < M ? tok : (int)(M - 1 - m0);                           \
-            const int off = (int)(4u * ((uint32_t)tok * (uint32_t)G + (uint32_t)gi_)); \
+            const int off = GROUPED ? (int)(slot_off[i] + 4u * (uint32_t)gi_)       \
+                                    : (int)(4u * ((uint32_t)tok * (uint32_t)G + (uint32_t)gi_)); \
             if (!DOTS) rss[i] = __builtin_amdgcn_raw_buffer_load_b32(rs_s, off, 0, 0); \
             rts[i] = __builtin_amdgcn_raw_buffer_load_b32(rs_t, off, 0, 0);         \
         }                                                                           \
@@ -400,10 +448,12 @@ __global__ __launch_bounds__(64 * WAVES_N * WAVES_M) void prefill_mfma_kernel(
 #pragma unroll
             for (int a = 0; a < WN; ++a) {
                 const int64_t nb = n0 + ctx.row_base + 16 * a + 4 * lg;
-                if (m < M) {
+                if (m < m_end) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (nb + i < N) store_y(y, y16, m * N + nb + i, acc[a][b][i]);
+                        if (nb + i < N)
+                            store_y(y, y16, m * N + nb + i,
+                                    GROUPED ? acc[a][b][i] * row_factor<GROUPED>(grp, m) : acc[a][b][i]);
                 }
             }
         }
@@ -448,11 +498,12 @@ struct PfRing {
     static constexpr int kSinkBytes = 1024;
 };
 
-template <int WN, int WM, int WAVES_N, int WAVES_M, int R, bool DOTS>
+template <int WN, int WM, int WAVES_N, int WAVES_M, int R, bool DOTS, bool GROUPED = false>
 __global__ __launch_bounds__(64 * WAVES_N * WAVES_M) void prefill_ring_kernel(
     const int8_t *__restrict__ q, const float *__restrict__ s, const int32_t *__restrict__ t,
     const uint8_t *__restrict__ codes, const uint16_t *__restrict__ ws, float *__restrict__ y,
-    uint16_t *__restrict__ y16, int32_t *__restrict__ d, int64_t M, int64_t N, int64_t K) {
+    uint16_t *__restrict__ y16, int32_t *__restrict__ d, int64_t M, int64_t N, int64_t K,
+    GroupedOr<GROUPED> grp) {
     using C = PfCfg<WN, WM, WAVES_N, WAVES_M>;
     constexpr int T = C::kThreads;
     using L = PfRing<C::BN, C::BM, T, DOTS>;
@@ -482,19 +533,34 @@ __global__ __launch_bounds__(64 * WAVES_N * WAVES_M) void prefill_ring_kernel(
     const int G = (int)(K / kGroup);
     const int KB = (int)(K / 4);
 
-    const int64_t tiles_n = (N + C::BN - 1) / C::BN;
-    const int64_t tiles_m = (M + C::BM - 1) / C::BM;
-    const int64_t tile = xcd_tile(blockIdx.x, tiles_n * tiles_m);
-    const int64_t n0 = (tile % tiles_n) * C::BN;
-    const int64_t m0 = (tile / tiles_n) * C::BM;
+    int64_t n0, m0;
+    int toks;
+    RowTile slots{0, 0, 0};
+    if constexpr (GROUPED) {
+        if (!grouped_tile<C::BM, C::BN>(grp, slots, n0)) return;
+        codes += slots.e * N * KB;
+        ws += slots.e * N * G;
+        m0 = slots.first;
+        toks = slots.count;
+    } else {
+        const int64_t tiles_n = (N + C::BN - 1) / C::BN;
+        const int64_t tiles_m = (M + C::BM - 1) / C::BM;
+        const int64_t tile = xcd_tile(blockIdx.x, tiles_n * tiles_m);
+        n0 = (tile % tiles_n) * C::BN;
+        m0 = (tile / tiles_n) * C::BM;
+        toks = M - m0 < C::BM ? (int)(M - m0) : C::BM;
+    }
     const int rows = N - n0 < C::BN ? (int)(N - n0) : C::BN;
-    const int toks = M - m0 < C::BM ? (int)(M - m0) : C::BM;
+    // first row and rows of the activation resources
+    const int64_t first = GROUPED ? 0 : m0;
+    int64_t span = toks;
+    if constexpr (GROUPED) span = grp.R;
 
     const __amdgpu_buffer_rsrc_t rs_codes = make_rsrc(codes + n0 * KB, (int64_t)rows * KB);
-    const __amdgpu_buffer_rsrc_t rs_q = make_rsrc(q + m0 * K, (int64_t)toks * K);
-    const __amdgpu_buffer_rsrc_t rs_t = make_rsrc(t + m0 * G, (int64_t)toks * G * 4);
+    const __amdgpu_buffer_rsrc_t rs_q = make_rsrc(q + first * K, span * K);
+    const __amdgpu_buffer_rsrc_t rs_t = make_rsrc(t + first * G, span * G * 4);
     const __amdgpu_buffer_rsrc_t rs_ws = make_rsrc(DOTS ? nullptr : ws + n0 * G, DOTS ? 0 : (int64_t)rows * G * 2);
-    const __amdgpu_buffer_rsrc_t rs_s = make_rsrc(DOTS ? nullptr : s + m0 * G, DOTS ? 0 : (int64_t)toks * G * 4);
+    const __amdgpu_buffer_rsrc_t rs_s = make_rsrc(DOTS ? nullptr : s + first * G, DOTS ? 0 : span * G * 4);
 
     // per-thread copy sources (group 0; group g adds 32 g or 128 g); rows and
     // tokens past the end read past the range (zeros, never stored)
@@ -511,7 +577,8 @@ __global__ __launch_bounds__(64 * WAVES_N * WAVES_M) void prefill_ring_kernel(
         const int u = i * T + tid;
         const int tok = u >> 3;
         const int piece = (u & 7) ^ (tok & 7);
-        qoff[i] = u < 8 * C::BM && tok < toks ? tok * (int)K + 16 * piece : kCopyOob;
+        const int row = u < 8 * C::BM ? tile_row<GROUPED>(grp, slots, tok, toks) : -1;
+        qoff[i] = row >= 0 ? row * (int)K + 16 * piece : kCopyOob;
     }
     // scale chunk sources (chunk 0; chunk c adds 16 c bytes for ws, 32 c for s / t)
     int wsoff[L::kWsInst > 0 ? L::kWsInst : 1], toff[L::kTokInst];
@@ -524,7 +591,8 @@ __global__ __launch_bounds__(64 * WAVES_N * WAVES_M) void prefill_ring_kernel(
     for (int i = 0; i < L::kTokInst; ++i) {
         const int u = i * T + tid;
         const int tok = u >> 1;
-        toff[i] = u < 2 * C::BM && tok < toks ? 4 * (tok * G + 4 * (u & 1)) : kCopyOob;
+        const int row = u < 2 * C::BM ? tile_row<GROUPED>(grp, slots, tok, toks) : -1;
+        toff[i] = row >= 0 ? 4 * (row * G + 4 * (u & 1)) : kCopyOob;
     }
 
     auto issue_stage = [&](int g) __attribute__((always_inline)) {
@@ -676,10 +744,12 @@ __global__ __launch_bounds__(64 * WAVES_N * WAVES_M) void prefill_ring_kernel(
 #pragma unroll
             for (int a = 0; a < WN; ++a) {
                 const int64_t nb = n0 + row_base + 16 * a + 4 * lg;
-                if (m < M) {
+                if (tok_base + 16 * b + r < toks) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (nb + i < N) store_y(y, y16, m * N + nb + i, acc[a][b][i]);
+                        if (nb + i < N)
+                            store_y(y, y16, m * N + nb + i,
+                                    GROUPED ? acc[a][b][i] * row_factor<GROUPED>(grp, m) : acc[a][b][i]);
                 }
             }
         }
@@ -774,7 +844,7 @@ void prefill_wide_kernel(const int8_t *__restrict__ q, const float *__restrict__
                          const uint16_t *__restrict__ ws, float *__restrict__ y,
                          uint16_t *__restrict__ y16, int32_t *__restrict__ d, int64_t M,
                          int64_t N, int64_t K, WideSplit sp,
-                         std::conditional_t<GROUPED, GroupedArgs, int> grp) {
+                         GroupedOr<GROUPED> grp) {
     using L = PfWide<DOTS, WM_>;
     constexpr int T = L::T, WN = L::WN, WM = L::WM;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -801,16 +871,11 @@ void prefill_wide_kernel(const int8_t *__restrict__ q, const float *__restrict__
     float *partial = nullptr;
     RowTile slots{0, 0, 0};
     if constexpr (GROUPED) {
-        const TileScan scan(grp.offsets, (int)grp.E, (int)M, L::BM);
-        const int64_t blocks = scan.total * tiles_n;
-        if ((int64_t)blockIdx.x >= blocks) return;
-        const int64_t tile = xcd_tile(blockIdx.x, blocks);
-        if (!scan.find((int)(tile / tiles_n), slots)) return;
-        n0 = (tile % tiles_n) * L::BN;
-        m0 = slots.first;
-        toks = slots.count;
+        if (!grouped_tile<L::BM, L::BN>(grp, slots, n0)) return;
         codes += slots.e * N * KB;
         ws += slots.e * N * G;
+        m0 = slots.first;
+        toks = slots.count;
     } else {
         int64_t tile;
         if ((int64_t)blockIdx.x < sp.full) {
@@ -831,13 +896,6 @@ void prefill_wide_kernel(const int8_t *__restrict__ q, const float *__restrict__
     const int64_t first = GROUPED ? 0 : m0;
     int64_t span = toks;
     if constexpr (GROUPED) span = grp.R;
-    auto row_of = [&](int tok) __attribute__((always_inline)) -> int {
-        if constexpr (GROUPED)
-            return (int)source_row(grp, slots, tok);
-        else
-            return tok < toks ? tok : -1;
-    };
-
     const __amdgpu_buffer_rsrc_t rs_codes = make_rsrc(codes + n0 * KB, (int64_t)rows * KB);
     const __amdgpu_buffer_rsrc_t rs_q = make_rsrc(q + first * K, span * K);
     const __amdgpu_buffer_rsrc_t rs_t = make_rsrc(t + first * G, span * G * 4);
@@ -862,14 +920,14 @@ void prefill_wide_kernel(const int8_t *__restrict__ q, const float *__restrict__
         const int u = i * T + tid;
         const int tok = u >> 3;
         const int piece = (u & 7) ^ (tok & 7);
-        const int row = row_of(tok);
+        const int row = tile_row<GROUPED>(grp, slots, tok, toks);
         qoff[i] = row >= 0 ? row * (int)K + 16 * piece : kCopyOob;
     }
     // scale chunk c: ws unit tid = row tid, groups 8c .. 8c + 7 (byte offset
     // 2 (row G + 8c)); s / t unit tid = token tid / 2, groups 8c + 4 (tid & 1)
     // .. + 3 (byte offset 4 (token G + 8c + 4 (tid & 1)))
     const int wsoff = tid < rows ? 2 * tid * G : kCopyOob;
-    const int tokrow = (tid >> 1) < L::BM ? row_of(tid >> 1) : -1;
+    const int tokrow = (tid >> 1) < L::BM ? tile_row<GROUPED>(grp, slots, tid >> 1, toks) : -1;
     const int tokoff = tokrow >= 0 ? 4 * (tokrow * G + 4 * (tid & 1)) : kCopyOob;
 
     auto issue_stage = [&](int g, uint8_t *st) __attribute__((always_inline)) {
@@ -911,7 +969,9 @@ void prefill_wide_kernel(const int8_t *__restrict__ q, const float *__restrict__
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[a][b][i] = 0.0f;
 
-    auto compute = [&](const uint8_t *st, int g) __attribute__((always_inline)) {
+    // the first NT token tiles of the block's WM
+    auto compute = [&](auto nt, const uint8_t *st, int g) __attribute__((always_inline)) {
+        constexpr int NT = decltype(nt)::value;
         const uint8_t *sc = scl0 + ((g >> 3) & 1) * L::kScaleBytes;
         const int j = g & 7;
         v4i w[WN];
@@ -920,14 +980,14 @@ void prefill_wide_kernel(const int8_t *__restrict__ q, const float *__restrict__
         // weight-scale operand of the outer products: lane 4k + i of row tile a
         // supplies ws of row 16 a + 4 (lane / 16) + i
         float wsa[WN];
-        float sv[WM];
+        float sv[NT];
         if (!DOTS) {
 #pragma unroll
             for (int a = 0; a < WN; ++a)
                 wsa[a] = half_bits_to_float(
                     *reinterpret_cast<const uint16_t *>(sc + wsb + 256 * a + 2 * j));
 #pragma unroll
-            for (int b = 0; b < WM; ++b)
+            for (int b = 0; b < NT; ++b)
                 sv[b] = *reinterpret_cast<const float *>(sc + L::kSBase + tokb + 512 * b + 4 * j);
         }
         v4i a0[WN], a1[WN];
@@ -959,13 +1019,13 @@ void prefill_wide_kernel(const int8_t *__restrict__ q, const float *__restrict__
             for (int a = 0; a < WN; ++a) c[slot][a] = mfma16x16x64(a1[a], bq1[slot], c[slot][a]);
         };
         load_tile(0, 0);
-        load_tile(1, 1);
+        if (NT > 1) load_tile(1, 1);
         mma(0);
 #pragma unroll
-        for (int b = 0; b < WM; ++b) {
+        for (int b = 0; b < NT; ++b) {
             const int cur = b & 1;
-            if (b + 2 < WM) load_tile(b + 2, cur);
-            if (b + 1 < WM) mma(cur ^ 1);
+            if (b + 2 < NT) load_tile(b + 2, cur);
+            if (b + 1 < NT) mma(cur ^ 1);
             if (DOTS) {
                 const int64_t m = m0 + 16 * b + r;
                 int64_t at = (m * N + n0 + row_base + 4 * lg) * G + g;
@@ -1013,7 +1073,7 @@ void prefill_wide_kernel(const int8_t *__restrict__ q, const float *__restrict__
     };
     // one group: stage g in LDS once this wave's copies older than the last
     // scale chunk have landed and every wave has passed the barrier
-    auto step = [&](int g, const uint8_t *cur, uint8_t *nxt) __attribute__((always_inline)) {
+    auto step = [&](auto nt, int g, const uint8_t *cur, uint8_t *nxt) __attribute__((always_inline)) {
         if (g > g0 && scales_at(g - 1))
             wait_vmem<L::kScaleInst>();          // that chunk may still be in flight
         else
@@ -1021,7 +1081,7 @@ void prefill_wide_kernel(const int8_t *__restrict__ q, const float *__restrict__
         ring_barrier();
         if (g + 1 < g1) issue_stage(g + 1, nxt);
         if (scales_at(g)) issue_scales((g >> 3) + 1);
-        compute(cur, g);
+        compute(nt, cur, g);
     };
 
     // scale chunk of group g0, and the next one when g0 starts mid-chunk
@@ -1029,9 +1089,28 @@ void prefill_wide_kernel(const int8_t *__restrict__ q, const float *__restrict__
     issue_scales(g0 >> 3);
     if ((g0 & 7) != 0 && ((g0 >> 3) + 1) * 8 < g1) issue_scales((g0 >> 3) + 1);
     issue_stage(g0, stage0);
-    for (int g = g0; g < g1; g += 2) {           // g0 and g1 - g0 are even
-        step(g, stage0, stage1);
-        step(g + 1, stage1, stage0);
+    auto run = [&](auto nt) __attribute__((always_inline)) {
+        for (int g = g0; g < g1; g += 2) {       // g0 and g1 - g0 are even
+            step(nt, g, stage0, stage1);
+            step(nt, g + 1, stage1, stage0);
+        }
+    };
+    // an expert's last tile computes no more token tiles than it has slots for,
+    // in halves
+    if constexpr (GROUPED && WM == 8) {
+        if (toks <= 4 * WM)
+            run(std::integral_constant<int, WM / 4>{});
+        else if (toks <= 8 * WM)
+            run(std::integral_constant<int, WM / 2>{});
+        else
+            run(std::integral_constant<int, WM>{});
+    } else if constexpr (GROUPED && WM == 2) {
+        if (toks <= 8 * WM)
+            run(std::integral_constant<int, WM / 2>{});
+        else
+            run(std::integral_constant<int, WM>{});
+    } else {
+        run(std::integral_constant<int, WM>{});
     }
     wait_vmem<0>();
 
@@ -1052,7 +1131,7 @@ void prefill_wide_kernel(const int8_t *__restrict__ q, const float *__restrict__
             const int64_t m = m0 + 16 * b + r;
             if (16 * b + r >= toks) continue;
             if constexpr (GROUPED) {
-                const float f = grp.row_scale ? grp.row_scale[m] : 1.0f;
+                const float f = row_factor<GROUPED>(grp, m);
 #pragma unroll
                 for (int a = 0; a < WN; ++a)
 #pragma unroll
@@ -1159,13 +1238,13 @@ hipError_t launch_ring_cfg(const int8_t *q, const int32_t *t, const uint8_t *cod
         const size_t lds = (size_t)R * L::kStageBytes + 2 * L::kScaleBytes + L::kSinkBytes;
         hipLaunchKernelGGL((prefill_ring_kernel<WN, WM, WAVES_N, WAVES_M, R, true>),
                            dim3((unsigned)blocks), dim3(C::kThreads), lds, stream, q, nullptr, t,
-                           codes, nullptr, nullptr, nullptr, out.d, M, N, K);
+                           codes, nullptr, nullptr, nullptr, out.d, M, N, K, 0);
     } else {
         using L = PfRing<C::BN, C::BM, C::kThreads, false>;
         const size_t lds = (size_t)R * L::kStageBytes + 2 * L::kScaleBytes + L::kSinkBytes;
         hipLaunchKernelGGL((prefill_ring_kernel<WN, WM, WAVES_N, WAVES_M, R, false>),
                            dim3((unsigned)blocks), dim3(C::kThreads), lds, stream, q, out.s, t,
-                           codes, out.ws, out.y, out.y16, nullptr, M, N, K);
+                           codes, out.ws, out.y, out.y16, nullptr, M, N, K, 0);
     }
     return hipGetLastError();
 }
@@ -1179,11 +1258,11 @@ hipError_t launch_cfg(const int8_t *q, const int32_t *t, const uint8_t *codes,
     if (out.d) {
         hipLaunchKernelGGL((prefill_mfma_kernel<WN, WM, WAVES_N, WAVES_M, DEPTH, true>),
                            dim3((unsigned)blocks), dim3(C::kThreads), 0, stream, q, nullptr, t,
-                           codes, nullptr, nullptr, nullptr, out.d, M, N, K);
+                           codes, nullptr, nullptr, nullptr, out.d, M, N, K, 0);
     } else {
         hipLaunchKernelGGL((prefill_mfma_kernel<WN, WM, WAVES_N, WAVES_M, DEPTH, false>),
                            dim3((unsigned)blocks), dim3(C::kThreads), 0, stream, q, out.s, t,
-                           codes, out.ws, out.y, out.y16, nullptr, M, N, K);
+                           codes, out.ws, out.y, out.y16, nullptr, M, N, K, 0);
     }
     return hipGetLastError();
 }
@@ -1252,32 +1331,53 @@ int prefill_cfg(int64_t M, int64_t N, int64_t K) {
 
 }  // namespace
 
-bool grouped_wide_fits(const GroupedArgs &a) {
-    const int64_t G = a.K / kGroup, some = a.T < a.E ? a.T : a.E;
-    // scale chunks of eight groups; gathered rows within 31-bit offsets
-    if (G % 8 != 0 || a.R * a.K >= kCopyOob || a.R * G * 4 >= kCopyOob || a.K > 65536) return false;
-    if (max_tiles(a.T, a.E, 64) * ((a.N + kWideBN - 1) / kWideBN) >= (int64_t(1) << 24)) return false;
-    return a.T >= 32 * some;
-}
+// ---------------------------------------------------------------- experts
 
 namespace {
 
 template <int WM>
-hipError_t launch_grouped_wide_as(const GroupedArgs &a, hipStream_t stream) {
+hipError_t grouped_wide(const GroupedArgs &a, hipStream_t stream) {
     using L = PfWide<false, WM>;
-    const int64_t blocks = max_tiles(a.T, a.E, L::BM) * ((a.N + L::BN - 1) / L::BN);
+    const int64_t blocks = grouped_blocks(a, L::BM, L::BN);
     hipLaunchKernelGGL((prefill_wide_kernel<false, WM, true>), dim3((unsigned)blocks), dim3(L::T),
                        (size_t)L::kLdsBytes, stream, a.q, a.s, a.t, a.codes, a.ws, a.y, a.y16,
                        nullptr, a.T, a.N, a.K, WideSplit{}, a);
     return hipGetLastError();
 }
 
+template <int WN, int WM, int WAVES_N, int WAVES_M, int R>
+hipError_t grouped_ring(const GroupedArgs &a, hipStream_t stream) {
+    using C = PfCfg<WN, WM, WAVES_N, WAVES_M>;
+    using L = PfRing<C::BN, C::BM, C::kThreads, false>;
+    const int64_t blocks = grouped_blocks(a, C::BM, C::BN);
+    const size_t lds = (size_t)R * L::kStageBytes + 2 * L::kScaleBytes + L::kSinkBytes;
+    hipLaunchKernelGGL((prefill_ring_kernel<WN, WM, WAVES_N, WAVES_M, R, false, true>),
+                       dim3((unsigned)blocks), dim3(C::kThreads), lds, stream, a.q, a.s, a.t,
+                       a.codes, a.ws, a.y, a.y16, nullptr, a.T, a.N, a.K, a);
+    return hipGetLastError();
+}
+
+template <int WN, int WM, int WAVES_N, int WAVES_M, int DEPTH>
+hipError_t grouped_staged(const GroupedArgs &a, hipStream_t stream) {
+    using C = PfCfg<WN, WM, WAVES_N, WAVES_M>;
+    const int64_t blocks = grouped_blocks(a, C::BM, C::BN);
+    hipLaunchKernelGGL((prefill_mfma_kernel<WN, WM, WAVES_N, WAVES_M, DEPTH, false, true>),
+                       dim3((unsigned)blocks), dim3(C::kThreads), 0, stream, a.q, a.s, a.t,
+                       a.codes, a.ws, a.y, a.y16, nullptr, a.T, a.N, a.K, a);
+    return hipGetLastError();
+}
+
 }  // namespace
 
-hipError_t launch_grouped_wide(const GroupedArgs &a, hipStream_t stream) {
-    const int64_t some = a.T < a.E ? a.T : a.E;
-    return a.T >= 192 * some ? launch_grouped_wide_as<8>(a, stream)
-                             : launch_grouped_wide_as<4>(a, stream);
+hipError_t launch_grouped_tiles(const GroupedArgs &a, GroupedTile tile, hipStream_t stream) {
+    switch (tile) {
+        case kGroupedRing64: return grouped_ring<1, 1, 4, 1, 4>(a, stream);
+        case kGroupedRing128: return grouped_ring<2, 1, 4, 1, 3>(a, stream);
+        case kGroupedWide32: return grouped_wide<2>(a, stream);
+        case kGroupedWide128: return grouped_wide<8>(a, stream);
+        case kGroupedStaged32: return grouped_staged<1, 1, 2, 2, 2>(a, stream);
+        default: return grouped_staged<2, 2, 2, 2, 2>(a, stream);
+    }
 }
 
 size_t prefill_workspace_bytes(int64_t M, int64_t N, int64_t K) {

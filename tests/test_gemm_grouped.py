@@ -167,6 +167,10 @@ SHAPES = {
     "tiles_of_64": ([40, 70, 33, 0, 64, 129], 300, 2048),
     "tiles_of_128": ([600, 0, 513, 255, 1], 515, 1024),
     "one_long": ([391], 257, 5120),
+    "few_blocks_of_16": ([9, 5, 0, 14, 7], 70, 1024),
+    "many_blocks_of_16": ([8, 3, 11] * 20, 1100, 1024),
+    "many_streams": ([1, 0, 2] * 20 + [6, 1], 1000, 1152),
+    "staged_32": ([8, 17, 33, 3], 100, 1152),
     "many_experts": ([i % 4 for i in range(200)], 17, 256),
     "over_4_per_lane": ([(i * 7) % 3 for i in range(700)], 16, 128),
 }
@@ -257,6 +261,63 @@ def test_one_expert_is_pq2_gemm(M):
     ref, tabs = p.reference()
     got = p.run()
     assert (np.abs(got - y.cpu().double().numpy()) <= 2 * (p.G + 4) * U * tabs).all()
+
+
+# counts, N, K whose tiles fill the GPU, by kernel
+LARGE = {
+    "256x32": ([40, 13, 0, 70, 33, 1, 64, 32, 31, 5, 16, 90, 48, 47, 49, 100], 2500, 1024),
+    "256x128": ([500, 385, 130, 33, 64, 0, 65, 400], 8500, 1024),
+    "64x64": ([130, 64, 3, 200], 3000, 640),
+    "stream": ([1, 2, 4, 0, 3, 5, 1, 1] * 4, 4100, 4096),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", list(LARGE))
+def test_large_shapes(name):
+    """Every expert's slots against pq2_gemm on the gathered rows: equal with
+    unit scales, and within both bounds (on sampled columns) with real ones."""
+    counts, N, K = LARGE[name]
+    print(f"gemm_grouped large {name}", flush=True)
+    for unit in (True, False):
+        p = Problem(counts, N, K, R=77, seed=21, unit=unit)
+        d = p.device()
+        y = torch.full((p.T, N), 7.0, device="cuda")
+        pq2.pq2_gemm_grouped(y=y, **d)
+        for e in range(p.E):
+            lo, hi = int(p.off[e]), int(p.off[e + 1])
+            if lo == hi:
+                continue
+            at = d["rows"][lo:hi].long()
+            want = torch.empty(hi - lo, N, device="cuda")
+            pq2.pq2_gemm(d["q"][at], d["s"][at], d["t"][at], d["codes"][e], d["wscale"][e], want)
+            if unit:
+                assert torch.equal(y[lo:hi], want), (name, e)
+        if not unit:
+            keep = np.random.default_rng(1).permutation(N)[:60]
+            keep[:3] = 0, N - 1, N // 2
+            p.codes, p.ws, p.N = p.codes[:, keep], p.ws[:, keep], len(keep)
+            p.check(y.cpu().double().numpy()[:, keep])
+
+
+@pytest.mark.gpu
+def test_gathered_rows_past_31_bits():
+    """Activations beyond 2^31 bytes: the rows at the end and beyond it against
+    the same rows in a small array."""
+    K, N = 16384, 50
+    R = (1 << 31) // K + 40
+    print(f"gemm_grouped {R} x {K} activations", flush=True)
+    p = Problem([3, 0, 5, 30], N, K, R=60, seed=12, weighted=True, invalid=True)
+    d = p.device()
+    q = torch.zeros(R, K, dtype=torch.int8, device="cuda")
+    s, t = torch.zeros(R, K // 128, device="cuda"), torch.zeros(R, K // 128, dtype=torch.int32, device="cuda")
+    q[R - 60:], s[R - 60:], t[R - 60:] = d["q"], d["s"], d["t"]
+    rows = d["rows"]
+    good = (rows >= 0) & (rows < 60)
+    d.update(q=q, s=s, t=t, rows=torch.where(good, rows + (R - 60), torch.full_like(rows, -1)))
+    y = torch.full((p.T, N), 7.0, device="cuda")
+    pq2.pq2_gemm_grouped(y=y, **d)
+    p.check(y.cpu().double().numpy())
 
 
 @pytest.mark.gpu
