@@ -7,11 +7,10 @@
 // one copy per K chunk), the expand adds the chunks in order, multiplies by B
 // and adds to the base.
 //
-// Both products run on the matrix cores in 16 x 16 tiles, 16 consecutive rows
-// at a time. Rows of a tile may have different adapters: the tile's distinct
-// adapters are walked one by one, each with all 16 rows as operand, and only
-// the results of the adapter's own rows are kept (selected, not multiplied by
-// zero: another adapter's infinities or NaN stay with its rows).
+// Both products run on the matrix cores in 16 x 16 tiles. A block takes up to
+// 128 consecutive rows, walks the distinct adapters among them and gathers each
+// one's rows into tiles, so an adapter is read once per block however its rows
+// are spread, and rows of different adapters never share an MFMA.
 //
 // Operands that are not both bfloat16 (or both binary16) are split exactly into
 // bfloat16 parts of 8 significant bits -- a binary16 value into two, a float32
@@ -97,102 +96,187 @@ __device__ __forceinline__ v4f mfma_parts(const v4u (&a)[NA], const v4u (&b)[NB]
     return c;
 }
 
-// The adapters of the 16 rows from m0: this lane's row lane % 16 (-1: none, or
-// past M).
-__device__ __forceinline__ int row_adapter(const LoraArgs &p, int64_t m0, int r) {
-    if (m0 + r >= p.M) return -1;
-    const int id = p.adapter[m0 + r];
-    return id >= 0 && id < p.L ? id : -1;
-}
+// The rows m0 .. m0 + rows - 1 (at most 128) of a block and their adapters, two
+// rows to a lane. next() takes the distinct adapters one by one and lists the
+// rows that have them; every wave of a block sees the same sequence.
+constexpr int kWindow = 128;
 
-// Takes the next distinct adapter off `left` (a bit per row): its id, and the
-// rows that have it.
-__device__ __forceinline__ int next_adapter(int id_of_row, uint32_t &left, uint32_t &mine) {
-    const int id = __builtin_amdgcn_readlane(id_of_row, __builtin_ctz(left));
-    mine = (uint32_t)__ballot(id_of_row == id) & 0xffffu;
-    left &= ~mine;
-    return id;
-}
+struct Rows {
+    int64_t m0;
+    int id0, id1;            // adapters of rows lane and 64 + lane; -1: none, -2: past the end
+    uint64_t left0, left1;   // rows whose adapter has not been taken
+    uint8_t *list;           // the wave's own list in LDS
+
+    __device__ __forceinline__ Rows(const LoraArgs &p, int64_t first, int64_t rows, uint8_t *own)
+        : m0(first), list(own) {
+        const int lane = threadIdx.x & (kWave - 1);
+        auto adapter = [&](int i) __attribute__((always_inline)) {
+            if (i >= rows || m0 + i >= p.M) return -2;
+            const int id = p.adapter[m0 + i];
+            return id >= 0 && id < p.L ? id : -1;
+        };
+        id0 = adapter(lane);
+        id1 = adapter(kWave + lane);
+        left0 = __ballot(id0 >= 0);
+        left1 = __ballot(id1 >= 0);
+    }
+
+    // Lists the rows with this id; their number.
+    __device__ __forceinline__ int take(int id) {
+        const int lane = threadIdx.x & (kWave - 1);
+        const uint64_t a = __ballot(id0 == id), b = __ballot(id1 == id);
+        const uint64_t below = (uint64_t(1) << lane) - 1;
+        const int n = __popcll(a);
+        __builtin_amdgcn_wave_barrier();
+        if (id0 == id) list[__popcll(a & below)] = (uint8_t)lane;
+        if (id1 == id) list[n + __popcll(b & below)] = (uint8_t)(kWave + lane);
+        __builtin_amdgcn_wave_barrier();
+        left0 &= ~a;
+        left1 &= ~b;
+        return n + __popcll(b);
+    }
+
+    __device__ __forceinline__ bool any() const { return (left0 | left1) != 0; }
+
+    __device__ __forceinline__ int next(int &count) {
+        const int id = left0 ? __builtin_amdgcn_readlane(id0, __builtin_ctzll(left0))
+                             : __builtin_amdgcn_readlane(id1, __builtin_ctzll(left1));
+        count = take(id);
+        return id;
+    }
+
+    // Row of entry i of the list (the first one past its end).
+    __device__ __forceinline__ int64_t row(int i, int count) const {
+        return m0 + list[i < count ? i : 0];
+    }
+};
 
 __device__ __forceinline__ int rank_of(const LoraArgs &p, int id) {
     const int R = (int)p.R;
     return p.ranks ? min(max(p.ranks[id], 0), R) : R;
 }
 
-// Shrink: a block sums one K chunk of 16 rows x 64 ranks; its four waves take a
-// quarter of the chunk each and meet in LDS, added in wave order.
-template <int XF, int WF>
-__global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs p, float *__restrict__ v,
-                                                          int64_t chunk) {
-    constexpr int T = kShrinkRanks / 16;
-    __shared__ v4f part[4][T][kWave];
+// Shrink: a block sums one K chunk of its rows x 64 ranks, adapter by adapter,
+// 16 * TR rows at a time; its eight waves share the chunk's groups of 128 and
+// meet in LDS, added in wave order.
+constexpr int kShrinkWaves = 8;
+
+// One wave's part of TR x T tiles: rows x (16 * TR), ranks w (16 * T), groups of
+// 128 from k to k1, each loaded whole before its four MFMA steps of 32.
+template <int XF, int WF, int TR, int T>
+__device__ __forceinline__ void shrink_steps(const char *const (&xrow)[TR],
+                                             const uint16_t *const (&wrow)[4], int64_t k, int64_t k1,
+                                             v4f (&acc)[TR][4]) {
+    constexpr int XV = XF == kF32 ? 2 : 1;     // 16-byte vectors of eight x
+    for (; k < k1; k += kGroup) {
+        v4u w[4][T], xr[4][TR][XV];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int j = 0; j < T; ++j) w[i][j] = *reinterpret_cast<const v4u *>(wrow[j] + k + 32 * i);
+#pragma unroll
+            for (int u = 0; u < TR; ++u)
+#pragma unroll
+                for (int h = 0; h < XV; ++h)
+                    xr[i][u][h] = *reinterpret_cast<const v4u *>(xrow[u] + (k + 32 * i) * (2 * XV) + 16 * h);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int u = 0; u < TR; ++u) {
+                v4u xp[kParts<XF>];
+                if constexpr (XF == kF32) {
+                    float f[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t b = xr[i][u][e >> 2][e & 3];
+                        f[e] = __builtin_bit_cast(float, b);
+                    }
+                    split8(f, xp);
+                } else if constexpr (XF != WF) {
+                    parts_of<XF>(xr[i][u][0], xp);
+                }
+#pragma unroll
+                for (int j = 0; j < T; ++j) {
+                    if constexpr (XF == WF && WF == kBf16) {
+                        acc[u][j] = mfma_bf16(xr[i][u][0], w[i][j], acc[u][j]);
+                    } else if constexpr (XF == WF) {
+                        acc[u][j] = mfma_f16(xr[i][u][0], w[i][j], acc[u][j]);
+                    } else {
+                        v4u wp[kParts<WF>];
+                        parts_of<WF>(w[i][j], wp);
+                        acc[u][j] = mfma_parts(xp, wp, acc[u][j]);
+                    }
+                }
+            }
+    }
+}
+
+template <int XF, int WF, int TR>
+__global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(LoraArgs p,
+                                                                        float *__restrict__ v,
+                                                                        int64_t chunk, int window,
+                                                                        int turns) {
+    __shared__ v4f part[kShrinkWaves][TR * 4][kWave];
+    __shared__ uint8_t lists[kShrinkWaves][kWindow];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int r = lane & 15, c = lane >> 4;
-    const int64_t m0 = (int64_t)blockIdx.x * 16;
-    const int r0 = (int)blockIdx.z * kShrinkRanks;
+    const int turn = (int)blockIdx.z % turns;
+    const int r0 = (int)blockIdx.z / turns * kShrinkRanks;
     const int64_t k0 = (int64_t)blockIdx.y * chunk;
     const int64_t k1 = k0 + chunk < p.K ? k0 + chunk : p.K;
-    const int64_t quarter = (k1 - k0) / 4;                 // a multiple of 32
-    const int64_t kw = k0 + wave * quarter + 8 * c;
-    const int64_t m = m0 + r < p.M ? m0 + r : p.M - 1;
-    const int id_of_row = row_adapter(p, m0, r);
-    uint32_t left = (uint32_t)__ballot(id_of_row >= 0) & 0xffffu, mine;
+    const int64_t each = ((k1 - k0) / kGroup + kShrinkWaves - 1) / kShrinkWaves * kGroup;
+    const int64_t kw = k0 + wave * each + 8 * c;
+    const int64_t kw1 = k0 + (wave + 1) * each < k1 ? k0 + (wave + 1) * each : k1;
+    Rows rows(p, (int64_t)blockIdx.x * window, window, lists[wave]);
     v += (int64_t)blockIdx.y * p.M * p.R;
-    while (left) {
-        const int id = next_adapter(id_of_row, left, mine);
+    for (int at = 0; rows.any(); ++at) {
+        int count;
+        const int id = rows.next(count);
+        if (at % turns != turn) continue;
         const int rank = rank_of(p, id);
         if (r0 >= rank) continue;
-        v4f acc[T] = {};
-        for (int64_t k = kw; k < kw + quarter; k += 32) {
-            v4u xr[XF == kF32 ? 2 : 1];
-            const char *xs = static_cast<const char *>(p.x) + (m * p.K + k) * (XF == kF32 ? 4 : 2);
+        // ranks past R are read from the last one; their sums are not kept
+        const uint16_t *wrow[4];
 #pragma unroll
-            for (int i = 0; i < (XF == kF32 ? 2 : 1); ++i)
-                xr[i] = *reinterpret_cast<const v4u *>(xs + 16 * i);
-            v4u xp[kParts<XF>];
-            if constexpr (XF == kF32) {
-                float f[8];
+        for (int j = 0; j < 4; ++j)
+            wrow[j] = static_cast<const uint16_t *>(p.a) +
+                      ((int64_t)id * p.R + min(r0 + 16 * j + r, (int)p.R - 1)) * p.K;
+        const int tiles = min((rank - r0 + 15) / 16, 4);
+        for (int i0 = 0; i0 < count; i0 += 16 * TR) {
+            const char *xrow[TR];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t u = xr[e >> 2][e & 3];
-                    f[e] = __builtin_bit_cast(float, u);
+            for (int u = 0; u < TR; ++u)
+                xrow[u] = static_cast<const char *>(p.x) +
+                          rows.row(i0 + 16 * u + r, count) * p.K * (XF == kF32 ? 4 : 2);
+            v4f acc[TR][4] = {};
+            if (tiles == 1)
+                shrink_steps<XF, WF, TR, 1>(xrow, wrow, kw, kw1, acc);
+            else if (tiles == 2)
+                shrink_steps<XF, WF, TR, 2>(xrow, wrow, kw, kw1, acc);
+            else
+                shrink_steps<XF, WF, TR, 4>(xrow, wrow, kw, kw1, acc);
+#pragma unroll
+            for (int u = 0; u < TR; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < tiles) part[wave][4 * u + j][lane] = acc[u][j];
+            __syncthreads();
+            // wave 4 u + j stores tile (u, j): rank r0 + 16 j + r of entries 4 c + i
+            const int u = wave / 4, j = wave % 4;
+            if (wave < 4 * TR && j < tiles) {
+                v4f sum = part[0][wave][lane];
+#pragma unroll
+                for (int w = 1; w < kShrinkWaves; ++w) sum += part[w][wave][lane];
+                const int rk = r0 + 16 * j + r;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = i0 + 16 * u + 4 * c + i;
+                    if (e < count && rk < rank) v[rows.row(e, count) * p.R + rk] = sum[i];
                 }
-                split8(f, xp);
-            } else if constexpr (XF != WF) {
-                parts_of<XF>(xr[0], xp);
             }
-#pragma unroll
-            for (int j = 0; j < T; ++j) {
-                if (r0 + 16 * j >= rank) continue;
-                // ranks past R are read from the last one; their sums are not kept
-                const int row = min(r0 + 16 * j + r, (int)p.R - 1);
-                const v4u w = *reinterpret_cast<const v4u *>(
-                    static_cast<const uint16_t *>(p.a) + ((int64_t)id * p.R + row) * p.K + k);
-                if constexpr (XF == WF && WF == kBf16) {
-                    acc[j] = mfma_bf16(xr[0], w, acc[j]);
-                } else if constexpr (XF == WF) {
-                    acc[j] = mfma_f16(xr[0], w, acc[j]);
-                } else {
-                    v4u wp[kParts<WF>];
-                    parts_of<WF>(w, wp);
-                    acc[j] = mfma_parts(xp, wp, acc[j]);
-                }
-            }
+            __syncthreads();
         }
-#pragma unroll
-        for (int j = 0; j < T; ++j) part[wave][j][lane] = acc[j];
-        __syncthreads();
-        // wave j stores rank tile j: rank r0 + 16 j + r of rows 4 c + i
-        v4f sum = part[0][wave][lane];
-#pragma unroll
-        for (int w = 1; w < 4; ++w) sum += part[w][wave][lane];
-        const int rk = r0 + 16 * wave + r;
-        if (rk < rank) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (mine >> (4 * c + i) & 1) v[(m0 + 4 * c + i) * p.R + rk] = sum[i];
-        }
-        __syncthreads();
     }
 }
 
@@ -204,97 +288,259 @@ __device__ __forceinline__ v4u keep_first(v4u w, int keep) {
     return w;
 }
 
-// Expand: a wave forms 16 rows x 16 columns of y.
+// 16 consecutive values of a row, as loaded.
+template <int YF>
+struct Raw16 {
+    uint32_t w[YF == kF32 ? 16 : 8];
+};
+
+// base of row m from column n on; `wide`: all 16 in 16-byte accesses.
+template <int YF>
+__device__ __forceinline__ void load16(const LoraArgs &p, int64_t m, int64_t n, bool wide, Raw16<YF> &o) {
+    constexpr int V = YF == kF32 ? 4 : 2;
+    const int64_t at = m * p.N + n;
+    if (wide) {
+        const v4u *b = reinterpret_cast<const v4u *>(static_cast<const char *>(p.base) + at * (YF == kF32 ? 4 : 2));
+#pragma unroll
+        for (int a = 0; a < V; ++a) {
+            const v4u u = b[a];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o.w[4 * a + k] = u[k];
+        }
+    } else if constexpr (YF == kF32) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            o.w[e] = n + e < p.N ? static_cast<const uint32_t *>(p.base)[at + e] : 0;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+            const uint16_t *b = static_cast<const uint16_t *>(p.base) + at + e;
+            o.w[e / 2] = (n + e < p.N ? b[0] : 0) | (n + e + 1 < p.N ? (uint32_t)b[1] << 16 : 0);
+        }
+    }
+}
+
+// y of row m from column n on: the loaded base, plus d (ADD) rounded once.
+template <int YF, bool ADD>
+__device__ __forceinline__ void store16(const LoraArgs &p, int64_t m, int64_t n, bool wide,
+                                        const Raw16<YF> &base, const v4f (&d)[4]) {
+    const int64_t at = m * p.N + n;
+    uint32_t o[YF == kF32 ? 16 : 8];
+#pragma unroll
+    for (int i = 0; i < (YF == kF32 ? 16 : 8); ++i) {
+        const uint32_t u = base.w[i];
+        if constexpr (!ADD) {
+            o[i] = u;
+        } else if constexpr (YF == kF32) {
+            const float f = d[i >> 2][i & 3];
+            o[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, u) + f);
+        } else {
+            const float lo = d[i >> 1][2 * i & 3], hi = d[i >> 1][(2 * i & 3) + 1];
+            o[i] = (uint32_t)bf16_rne(__builtin_bit_cast(float, u << 16) + lo) |
+                   ((uint32_t)bf16_rne(__builtin_bit_cast(float, u & 0xffff0000u) + hi) << 16);
+        }
+    }
+    if (wide) {
+        v4u *y = reinterpret_cast<v4u *>(static_cast<char *>(p.y) + at * (YF == kF32 ? 4 : 2));
+#pragma unroll
+        for (int a = 0; a < (YF == kF32 ? 4 : 2); ++a)
+            y[a] = v4u{o[4 * a], o[4 * a + 1], o[4 * a + 2], o[4 * a + 3]};
+    } else if constexpr (YF == kF32) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (n + e < p.N) static_cast<uint32_t *>(p.y)[at + e] = o[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (n + e < p.N)
+                static_cast<uint16_t *>(p.y)[at + e] = (uint16_t)(e & 1 ? o[e / 2] >> 16 : o[e / 2]);
+    }
+}
+
+// Expand: a block forms its rows x 256 columns of y, adapter by adapter, 32 rows
+// and 64 ranks at a time: the block's threads add the K chunks' sums of v,
+// apply the adapter's scale and leave v's three bfloat16 parts in LDS, then each
+// wave multiplies them by B's rows of its 64 columns (in registers; kept from
+// tile to tile up to rank 64). Operand A is B's rows (columns of y), operand B
+// the rows' v: row 4 c + i of MFMA tile a is column 16 c + 4 a + i, so that the
+// four tiles leave a lane with 16 consecutive columns of one row, and four
+// lanes with 64.
+constexpr int kExpandRows = 32;
+constexpr int kExpandStride = 144;             // LDS bytes of a row's 64 ranks (128 + pad)
+
 template <int WF, int YF>
 __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs p, const float *__restrict__ v,
-                                                          int chunks) {
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+                                                          int chunks, int window, int turns) {
+    __shared__ uint8_t lists[4][kWindow];
+    __shared__ __attribute__((aligned(16))) uint8_t vparts[3][kExpandRows * kExpandStride];
+    constexpr int U = kExpandRows / 16;
+    const int tid = threadIdx.x;
+    const int lane = tid & (kWave - 1), wave = tid / kWave;
     const int r = lane & 15, c = lane >> 4;
-    const int64_t m0 = (int64_t)blockIdx.x * 16;
-    const int64_t n0 = ((int64_t)blockIdx.y * 4 + wave) * 16;
-    if (n0 >= p.N) return;
-    const int64_t n = n0 + r < p.N ? n0 + r : p.N - 1;
-    const int64_t m = m0 + r < p.M ? m0 + r : p.M - 1;
-    const int id_of_row = row_adapter(p, m0, r);
-    uint32_t left = (uint32_t)__ballot(id_of_row >= 0) & 0xffffu, mine;
-    const uint32_t some = left;
-    v4f out = {};
-    while (left) {
-        const int id = next_adapter(id_of_row, left, mine);
+    const int64_t n0 = ((int64_t)blockIdx.y * 4 + wave) * 64;
+    const int64_t n = n0 + 16 * c;             // this lane's columns
+    // 16-byte accesses of 16 columns
+    const bool wide = n + 16 <= p.N && p.N % (YF == kF32 ? 4 : 8) == 0 &&
+                      (((uintptr_t)p.base | (uintptr_t)p.y) & 15) == 0;
+    const uint16_t *wrow[4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+        const int64_t col = n0 + 16 * (r >> 2) + 4 * a + (r & 3);
+        wrow[a] = static_cast<const uint16_t *>(p.b) + (col < p.N ? col : p.N - 1) * p.R + 8 * c;
+    }
+    Rows rows(p, (int64_t)blockIdx.x * window, window, lists[wave]);
+    for (int at = 0; rows.any(); ++at) {
+        int count;
+        const int id = rows.next(count);
+        if (at % turns != (int)blockIdx.z) continue;
         const int rank = rank_of(p, id);
         const float scale = p.scale ? p.scale[id] : 1.0f;
-        const bool own = mine >> r & 1;
-        v4f acc = {};
-        for (int k0 = 0; k0 < rank; k0 += 32) {
-            const int k = k0 + 8 * c;
-            const int keep = rank - k;                     // ranks of this lane's vector
-            float f[8] = {};
-            v4u w = {};
-            if (keep > 0) {
-                w = *reinterpret_cast<const v4u *>(
-                    static_cast<const uint16_t *>(p.b) + ((int64_t)id * p.N + n) * p.R + k);
-                w = keep_first(w, keep);
-                if (own) {
-                    const float *src = v + m * p.R + k;
-                    for (int s = 0; s < chunks; ++s, src += p.M * p.R) {
+        const int64_t wbase = (int64_t)id * p.N * p.R;
+        v4u w[2][4] = {};
+        for (int i0 = 0; i0 < count; i0 += kExpandRows) {
+            const int live = min(count - i0, kExpandRows);
+            // the base, B's vectors and v are requested together
+            int64_t m[U];
+            Raw16<YF> base[U];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float4 u = *reinterpret_cast<const float4 *>(src + 4 * h);
-                            f[4 * h] += u.x;
-                            f[4 * h + 1] += u.y;
-                            f[4 * h + 2] += u.z;
-                            f[4 * h + 3] += u.w;
+            for (int u = 0; u < U; ++u) {
+                m[u] = rows.row(i0 + 16 * u + r, count);
+                if (16 * u + r < live && n < p.N) load16<YF>(p, m[u], n, wide, base[u]);
+            }
+            v4f acc[U][4] = {};
+            for (int kc = 0; kc < rank; kc += 64) {
+                if (i0 == 0 || rank > 64) {    // else B's vectors are those of the last rows
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) {
+                            const int keep = rank - (kc + 32 * j + 8 * c);
+                            w[j][a] = v4u{};
+                            if (keep > 0)
+                                w[j][a] = *reinterpret_cast<const v4u *>(wrow[a] + wbase + kc + 32 * j);
+                        }
+                }
+                v4f f[U];                      // four ranks of an entry each
+#pragma unroll
+                for (int e = 0; e < U; ++e) {
+                    const int entry = 16 * e + (tid >> 4), k = kc + 4 * (tid & 15);
+                    f[e] = v4f{};
+                    if (entry < live && k < rank) {
+                        const float *src = v + rows.row(i0 + entry, count) * p.R + k;
+#pragma unroll 4
+                        for (int s = 0; s < chunks; ++s)
+                            f[e] += *reinterpret_cast<const v4f *>(src + s * p.M * p.R);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) f[e][q] = k + q < rank ? f[e][q] * scale : 0.0f;
+                }
+                ring_barrier();                // the parts of the last step have been read
+#pragma unroll
+                for (int e = 0; e < U; ++e) {
+                    const float g[8] = {f[e][0], f[e][1], f[e][2], f[e][3]};
+                    v4u part[3];
+                    split8(g, part);
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        *reinterpret_cast<uint2 *>(vparts[i] + (16 * e + (tid >> 4)) * kExpandStride +
+                                                   8 * (tid & 15)) = make_uint2(part[i][0], part[i][1]);
+                }
+                ring_barrier();
+                if ((rank & 7) && (i0 == 0 || rank > 64)) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int a = 0; a < 4; ++a)
+                            w[j][a] = keep_first(w[j][a], rank - (kc + 32 * j + 8 * c));
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (16 * u >= live) continue;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if (kc + 32 * j >= rank) continue;
+                        v4u vp[3];
+#pragma unroll
+                        for (int i = 0; i < 3; ++i)
+                            vp[i] = *reinterpret_cast<const v4u *>(
+                                vparts[i] + (16 * u + r) * kExpandStride + 64 * j + 16 * c);
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) {
+                            v4u wp[kParts<WF>];
+                            parts_of<WF>(w[j][a], wp);
+                            acc[u][a] = mfma_parts(wp, vp, acc[u][a]);
                         }
                     }
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = e < keep ? f[e] * scale : 0.0f;
-            v4u vp[3], wp[kParts<WF>];
-            split8(f, vp);
-            parts_of<WF>(w, wp);
-            acc = mfma_parts(vp, wp, acc);
+            for (int u = 0; u < U; ++u)
+                if (16 * u + r < live && n < p.N) store16<YF, true>(p, m[u], n, wide, base[u], acc[u]);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (mine >> (4 * c + i) & 1) out[i] = acc[i];
     }
-    if (n0 + r >= p.N) return;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (m0 + 4 * c + i >= p.M) continue;
-        const int64_t at = (m0 + 4 * c + i) * p.N + n0 + r;
-        const bool add = some >> (4 * c + i) & 1;
-        if (!add && p.base == p.y) continue;
-        if constexpr (YF == kF32) {
-            const float b = static_cast<const float *>(p.base)[at];
-            static_cast<float *>(p.y)[at] = add ? b + out[i] : b;
-        } else {
-            const uint16_t u = static_cast<const uint16_t *>(p.base)[at];
-            const float b = __builtin_bit_cast(float, (uint32_t)u << 16);
-            static_cast<uint16_t *>(p.y)[at] = add ? bf16_rne(b + out[i]) : u;
-        }
+    if (blockIdx.z != 0) return;
+    if (p.base == p.y) return;
+    const int count = rows.take(-1);           // rows without an adapter (every lane takes part)
+    if (n >= p.N) return;
+    const v4f none[4] = {};
+    for (int i = r; i < count; i += 16) {
+        const int64_t m = rows.row(i, count);
+        Raw16<YF> base;
+        load16<YF>(p, m, n, wide, base);
+        store16<YF, false>(p, m, n, wide, base, none);
     }
 }
 
-// K chunks of the shrink: about 512 blocks in all, at least 512 of K each.
+// How the rows are dealt to blocks, each of which stands `per` times in the
+// grid: windows of rows (a power of two of them, as many as leave `least`
+// blocks, so that rows share an adapter's reads), and turns -- blocks of one
+// window that take its adapters in turn, for batches of few rows with many
+// adapters.
+struct Deal {
+    int window, turns;
+    int64_t windows;
+};
+
+Deal deal_rows(int64_t M, int64_t L, int64_t per, int64_t least, int64_t most) {
+    Deal d{kWindow, 1, 0};
+    while (d.window > 32 && (M + d.window - 1) / d.window * per < least) d.window /= 2;
+    d.windows = (M + d.window - 1) / d.window;
+    int64_t t = most / (d.windows * per);
+    const int64_t ids = M < d.window ? M : d.window;
+    if (t > ids) t = ids;
+    if (t > L) t = L;
+    d.turns = t < 1 ? 1 : (int)t;
+    return d;
+}
+
+// K chunks of the shrink: at least 1024 of K each.
 int plan_chunks(int64_t M, int64_t K) {
-    const int64_t tiles = (M + 15) / 16;
-    int64_t s = 512 / tiles;
-    const int64_t most = (K + 511) / 512 < 16 ? (K + 511) / 512 : 16;
+    const int64_t most = (K + 1023) / 1024 < 16 ? (K + 1023) / 1024 : 16;
+    int64_t s = 256 / ((M + 31) / 32);
     if (s > most) s = most;
     return s < 1 ? 1 : (int)s;
 }
 
 template <int XF, int WF>
-void launch_shrink(const LoraArgs &a, float *v, int64_t chunk, dim3 grid, hipStream_t stream) {
-    hipLaunchKernelGGL((lora_shrink_kernel<XF, WF>), grid, dim3(256), 0, stream, a, v, chunk);
+void launch_shrink(const LoraArgs &a, float *v, int64_t chunk, int64_t chunks, hipStream_t stream) {
+    const int64_t blocks = (a.R + kShrinkRanks - 1) / kShrinkRanks;
+    const Deal d = deal_rows(a.M, a.L, chunks * blocks, 192, 1024);
+    const dim3 grid((unsigned)d.windows, (unsigned)chunks, (unsigned)(blocks * d.turns));
+    if (a.M > 16)
+        hipLaunchKernelGGL((lora_shrink_kernel<XF, WF, 2>), grid, dim3(64 * kShrinkWaves), 0, stream,
+                           a, v, chunk, d.window, d.turns);
+    else
+        hipLaunchKernelGGL((lora_shrink_kernel<XF, WF, 1>), grid, dim3(64 * kShrinkWaves), 0, stream,
+                           a, v, chunk, d.window, d.turns);
 }
 
 template <int WF, int YF>
-void launch_expand(const LoraArgs &a, const float *v, int chunks, hipStream_t stream) {
-    const dim3 grid((unsigned)((a.M + 15) / 16), (unsigned)((a.N + 63) / 64));
-    hipLaunchKernelGGL((lora_expand_kernel<WF, YF>), grid, dim3(256), 0, stream, a, v, chunks);
+void launch_expand(const LoraArgs &a, const float *v, int64_t chunks, hipStream_t stream) {
+    const int64_t cols = (a.N + 255) / 256;
+    const Deal d = deal_rows(a.M, a.L, cols, 256, 2048);
+    hipLaunchKernelGGL((lora_expand_kernel<WF, YF>),
+                       dim3((unsigned)d.windows, (unsigned)cols, (unsigned)d.turns), dim3(256), 0,
+                       stream, a, v, (int)chunks, d.window, d.turns);
 }
 
 }  // namespace
@@ -308,29 +554,28 @@ hipError_t launch_lora(const LoraArgs &a, int x_format, int w_format, int y_form
     const size_t per = (size_t)a.M * (size_t)a.R * sizeof(float);
     int64_t chunks = plan_chunks(a.M, a.K);
     if ((uint64_t)chunks > work_bytes / per) chunks = (int64_t)(work_bytes / per);
-    // chunks are whole groups of 128 (a quarter is whole MFMA steps of 32)
-    const int64_t chunk = (a.K / 128 + chunks - 1) / chunks * 128;
+    // a chunk is a group of 128 or more for each wave of a block
+    const int64_t share = kGroup * kShrinkWaves;
+    const int64_t chunk = (a.K + share * chunks - 1) / (share * chunks) * share;
     chunks = (a.K + chunk - 1) / chunk;
-    const dim3 grid((unsigned)((a.M + 15) / 16), (unsigned)chunks,
-                    (unsigned)((a.R + kShrinkRanks - 1) / kShrinkRanks));
     const bool wb = w_format == kBf16;
     if (x_format == kF32)
-        wb ? launch_shrink<kF32, kBf16>(a, work, chunk, grid, stream)
-           : launch_shrink<kF32, kF16>(a, work, chunk, grid, stream);
+        wb ? launch_shrink<kF32, kBf16>(a, work, chunk, chunks, stream)
+           : launch_shrink<kF32, kF16>(a, work, chunk, chunks, stream);
     else if (x_format == kBf16)
-        wb ? launch_shrink<kBf16, kBf16>(a, work, chunk, grid, stream)
-           : launch_shrink<kBf16, kF16>(a, work, chunk, grid, stream);
+        wb ? launch_shrink<kBf16, kBf16>(a, work, chunk, chunks, stream)
+           : launch_shrink<kBf16, kF16>(a, work, chunk, chunks, stream);
     else
-        wb ? launch_shrink<kF16, kBf16>(a, work, chunk, grid, stream)
-           : launch_shrink<kF16, kF16>(a, work, chunk, grid, stream);
+        wb ? launch_shrink<kF16, kBf16>(a, work, chunk, chunks, stream)
+           : launch_shrink<kF16, kF16>(a, work, chunk, chunks, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (y_format == kF32)
-        wb ? launch_expand<kBf16, kF32>(a, work, (int)chunks, stream)
-           : launch_expand<kF16, kF32>(a, work, (int)chunks, stream);
+        wb ? launch_expand<kBf16, kF32>(a, work, chunks, stream)
+           : launch_expand<kF16, kF32>(a, work, chunks, stream);
     else
-        wb ? launch_expand<kBf16, kBf16>(a, work, (int)chunks, stream)
-           : launch_expand<kF16, kBf16>(a, work, (int)chunks, stream);
+        wb ? launch_expand<kBf16, kBf16>(a, work, chunks, stream)
+           : launch_expand<kF16, kBf16>(a, work, chunks, stream);
     return hipGetLastError();
 }
 
