@@ -97,8 +97,8 @@ __device__ __forceinline__ v4f mfma_parts(const v4u (&a)[NA], const v4u (&b)[NB]
 }
 
 // The rows m0 .. m0 + rows - 1 (at most 128) of a block and their adapters, two
-// rows to a lane. next() takes the distinct adapters one by one and lists the
-// rows that have them; every wave of a block sees the same sequence.
+// rows to a lane. next() gives the distinct adapters one by one, take() lists
+// the rows that have one; every wave of a block sees the same sequence.
 constexpr int kWindow = 128;
 
 struct Rows {
@@ -131,17 +131,17 @@ struct Rows {
         if (id0 == id) list[__popcll(a & below)] = (uint8_t)lane;
         if (id1 == id) list[n + __popcll(b & below)] = (uint8_t)(kWave + lane);
         __builtin_amdgcn_wave_barrier();
-        left0 &= ~a;
-        left1 &= ~b;
         return n + __popcll(b);
     }
 
     __device__ __forceinline__ bool any() const { return (left0 | left1) != 0; }
 
-    __device__ __forceinline__ int next(int &count) {
+    // The next distinct adapter.
+    __device__ __forceinline__ int next() {
         const int id = left0 ? __builtin_amdgcn_readlane(id0, __builtin_ctzll(left0))
                              : __builtin_amdgcn_readlane(id1, __builtin_ctzll(left1));
-        count = take(id);
+        left0 &= ~__ballot(id0 == id);
+        left1 &= ~__ballot(id1 == id);
         return id;
     }
 
@@ -157,21 +157,25 @@ __device__ __forceinline__ int rank_of(const LoraArgs &p, int id) {
 }
 
 // Shrink: a block sums one K chunk of its rows x 64 ranks, adapter by adapter,
-// 16 * TR rows at a time; its eight waves share the chunk's groups of 128 and
-// meet in LDS, added in wave order.
+// 16 * TR rows at a time; its eight waves share the chunk's steps and meet in
+// LDS, added in wave order.
 constexpr int kShrinkWaves = 8;
 
-// One wave's part of TR x T tiles: rows x (16 * TR), ranks w (16 * T), groups of
-// 128 from k to k1, each loaded whole before its four MFMA steps of 32.
+// One wave's part of TR x T tiles: rows x (16 * TR), ranks w (16 * T), from k to
+// k1, the operands of kSteps MFMA steps of 32 loaded together.
+template <int TR>
+constexpr int kSteps = TR == 1 ? 4 : 2;
+
 template <int XF, int WF, int TR, int T>
 __device__ __forceinline__ void shrink_steps(const char *const (&xrow)[TR],
                                              const uint16_t *const (&wrow)[4], int64_t k, int64_t k1,
                                              v4f (&acc)[TR][4]) {
     constexpr int XV = XF == kF32 ? 2 : 1;     // 16-byte vectors of eight x
-    for (; k < k1; k += kGroup) {
-        v4u w[4][T], xr[4][TR][XV];
+    constexpr int S = kSteps<TR>;
+    for (; k < k1; k += 32 * S) {
+        v4u w[S][T], xr[S][TR][XV];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < S; ++i) {
 #pragma unroll
             for (int j = 0; j < T; ++j) w[i][j] = *reinterpret_cast<const v4u *>(wrow[j] + k + 32 * i);
 #pragma unroll
@@ -181,7 +185,7 @@ __device__ __forceinline__ void shrink_steps(const char *const (&xrow)[TR],
                     xr[i][u][h] = *reinterpret_cast<const v4u *>(xrow[u] + (k + 32 * i) * (2 * XV) + 16 * h);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < S; ++i)
 #pragma unroll
             for (int u = 0; u < TR; ++u) {
                 v4u xp[kParts<XF>];
@@ -217,7 +221,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(LoraArgs
                                                                         float *__restrict__ v,
                                                                         int64_t chunk, int window,
                                                                         int turns) {
-    __shared__ v4f part[kShrinkWaves][TR * 4][kWave];
+    __shared__ v4f part[kShrinkWaves][4][kWave];
     __shared__ uint8_t lists[kShrinkWaves][kWindow];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int r = lane & 15, c = lane >> 4;
@@ -225,17 +229,18 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(LoraArgs
     const int r0 = (int)blockIdx.z / turns * kShrinkRanks;
     const int64_t k0 = (int64_t)blockIdx.y * chunk;
     const int64_t k1 = k0 + chunk < p.K ? k0 + chunk : p.K;
-    const int64_t each = ((k1 - k0) / kGroup + kShrinkWaves - 1) / kShrinkWaves * kGroup;
+    constexpr int kBatch = 32 * kSteps<TR>;    // divides 128, and so the chunk
+    const int64_t each = ((k1 - k0) / kBatch + kShrinkWaves - 1) / kShrinkWaves * kBatch;
     const int64_t kw = k0 + wave * each + 8 * c;
     const int64_t kw1 = k0 + (wave + 1) * each < k1 ? k0 + (wave + 1) * each : k1;
     Rows rows(p, (int64_t)blockIdx.x * window, window, lists[wave]);
     v += (int64_t)blockIdx.y * p.M * p.R;
     for (int at = 0; rows.any(); ++at) {
-        int count;
-        const int id = rows.next(count);
+        const int id = rows.next();
         if (at % turns != turn) continue;
         const int rank = rank_of(p, id);
         if (r0 >= rank) continue;
+        const int count = rows.take(id);
         // ranks past R are read from the last one; their sums are not kept
         const uint16_t *wrow[4];
 #pragma unroll
@@ -257,25 +262,26 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(LoraArgs
             else
                 shrink_steps<XF, WF, TR, 4>(xrow, wrow, kw, kw1, acc);
 #pragma unroll
-            for (int u = 0; u < TR; ++u)
+            for (int u = 0; u < TR; ++u) {
+                if (u > 0 && i0 + 16 * u >= count) break;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (j < tiles) part[wave][4 * u + j][lane] = acc[u][j];
-            __syncthreads();
-            // wave 4 u + j stores tile (u, j): rank r0 + 16 j + r of entries 4 c + i
-            const int u = wave / 4, j = wave % 4;
-            if (wave < 4 * TR && j < tiles) {
-                v4f sum = part[0][wave][lane];
+                    if (j < tiles) part[wave][j][lane] = acc[u][j];
+                __syncthreads();
+                // wave j stores rank tile j: rank r0 + 16 j + r of entries 4 c + i
+                if (wave < tiles) {
+                    v4f sum = part[0][wave][lane];
 #pragma unroll
-                for (int w = 1; w < kShrinkWaves; ++w) sum += part[w][wave][lane];
-                const int rk = r0 + 16 * j + r;
+                    for (int w = 1; w < kShrinkWaves; ++w) sum += part[w][wave][lane];
+                    const int rk = r0 + 16 * wave + r;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int e = i0 + 16 * u + 4 * c + i;
-                    if (e < count && rk < rank) v[rows.row(e, count) * p.R + rk] = sum[i];
+                    for (int i = 0; i < 4; ++i) {
+                        const int e = i0 + 16 * u + 4 * c + i;
+                        if (e < count && rk < rank) v[rows.row(e, count) * p.R + rk] = sum[i];
+                    }
                 }
+                __syncthreads();
             }
-            __syncthreads();
         }
     }
 }
@@ -294,18 +300,25 @@ struct Raw16 {
     uint32_t w[YF == kF32 ? 16 : 8];
 };
 
-// base of row m from column n on; `wide`: all 16 in 16-byte accesses.
+// Four words that are aligned like an element only (rows of an odd N).
+template <int YF>
+struct __attribute__((packed, aligned(YF == kF32 ? 4 : 2))) Words4 {
+    uint32_t w[4];
+};
+
+// base of row m from column n on; `wide`: all 16 columns exist.
 template <int YF>
 __device__ __forceinline__ void load16(const LoraArgs &p, int64_t m, int64_t n, bool wide, Raw16<YF> &o) {
     constexpr int V = YF == kF32 ? 4 : 2;
     const int64_t at = m * p.N + n;
     if (wide) {
-        const v4u *b = reinterpret_cast<const v4u *>(static_cast<const char *>(p.base) + at * (YF == kF32 ? 4 : 2));
+        const Words4<YF> *b = reinterpret_cast<const Words4<YF> *>(
+            static_cast<const char *>(p.base) + at * (YF == kF32 ? 4 : 2));
 #pragma unroll
         for (int a = 0; a < V; ++a) {
-            const v4u u = b[a];
+            const Words4<YF> u = b[a];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) o.w[4 * a + k] = u[k];
+            for (int k = 0; k < 4; ++k) o.w[4 * a + k] = u.w[k];
         }
     } else if constexpr (YF == kF32) {
 #pragma unroll
@@ -341,10 +354,10 @@ __device__ __forceinline__ void store16(const LoraArgs &p, int64_t m, int64_t n,
         }
     }
     if (wide) {
-        v4u *y = reinterpret_cast<v4u *>(static_cast<char *>(p.y) + at * (YF == kF32 ? 4 : 2));
+        Words4<YF> *y = reinterpret_cast<Words4<YF> *>(static_cast<char *>(p.y) + at * (YF == kF32 ? 4 : 2));
 #pragma unroll
         for (int a = 0; a < (YF == kF32 ? 4 : 2); ++a)
-            y[a] = v4u{o[4 * a], o[4 * a + 1], o[4 * a + 2], o[4 * a + 3]};
+            y[a] = Words4<YF>{{o[4 * a], o[4 * a + 1], o[4 * a + 2], o[4 * a + 3]}};
     } else if constexpr (YF == kF32) {
 #pragma unroll
         for (int e = 0; e < 16; ++e)
@@ -357,7 +370,7 @@ __device__ __forceinline__ void store16(const LoraArgs &p, int64_t m, int64_t n,
     }
 }
 
-// Expand: a block forms its rows x 256 columns of y, adapter by adapter, 32 rows
+// Expand: a block forms its rows x 256 columns of y, adapter by adapter, 16 rows
 // and 64 ranks at a time: the block's threads add the K chunks' sums of v,
 // apply the adapter's scale and leave v's three bfloat16 parts in LDS, then each
 // wave multiplies them by B's rows of its 64 columns (in registers; kept from
@@ -365,7 +378,7 @@ __device__ __forceinline__ void store16(const LoraArgs &p, int64_t m, int64_t n,
 // the rows' v: row 4 c + i of MFMA tile a is column 16 c + 4 a + i, so that the
 // four tiles leave a lane with 16 consecutive columns of one row, and four
 // lanes with 64.
-constexpr int kExpandRows = 32;
+constexpr int kExpandRows = 16;
 constexpr int kExpandStride = 144;             // LDS bytes of a row's 64 ranks (128 + pad)
 
 template <int WF, int YF>
@@ -379,9 +392,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs p, const floa
     const int r = lane & 15, c = lane >> 4;
     const int64_t n0 = ((int64_t)blockIdx.y * 4 + wave) * 64;
     const int64_t n = n0 + 16 * c;             // this lane's columns
-    // 16-byte accesses of 16 columns
-    const bool wide = n + 16 <= p.N && p.N % (YF == kF32 ? 4 : 8) == 0 &&
-                      (((uintptr_t)p.base | (uintptr_t)p.y) & 15) == 0;
+    const bool wide = n + 16 <= p.N;
     const uint16_t *wrow[4];
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
@@ -390,9 +401,9 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs p, const floa
     }
     Rows rows(p, (int64_t)blockIdx.x * window, window, lists[wave]);
     for (int at = 0; rows.any(); ++at) {
-        int count;
-        const int id = rows.next(count);
+        const int id = rows.next();
         if (at % turns != (int)blockIdx.z) continue;
+        const int count = rows.take(id);
         const int rank = rank_of(p, id);
         const float scale = p.scale ? p.scale[id] : 1.0f;
         const int64_t wbase = (int64_t)id * p.N * p.R;
@@ -501,9 +512,12 @@ struct Deal {
     int64_t windows;
 };
 
+// Up to 1024 rows, a batch with many adapters is taken for requests of a few
+// rows each, whose windows hold several adapters.
 Deal deal_rows(int64_t M, int64_t L, int64_t per, int64_t least, int64_t most) {
     Deal d{kWindow, 1, 0};
-    while (d.window > 32 && (M + d.window - 1) / d.window * per < least) d.window /= 2;
+    const int64_t adapters = M > 1024 || L < 4 ? 1 : L < 8 ? L / 2 : 4;
+    while (d.window > 32 && (M + d.window - 1) / d.window * per * adapters < least) d.window /= 2;
     d.windows = (M + d.window - 1) / d.window;
     int64_t t = most / (d.windows * per);
     const int64_t ids = M < d.window ? M : d.window;
@@ -524,7 +538,7 @@ int plan_chunks(int64_t M, int64_t K) {
 template <int XF, int WF>
 void launch_shrink(const LoraArgs &a, float *v, int64_t chunk, int64_t chunks, hipStream_t stream) {
     const int64_t blocks = (a.R + kShrinkRanks - 1) / kShrinkRanks;
-    const Deal d = deal_rows(a.M, a.L, chunks * blocks, 192, 1024);
+    const Deal d = deal_rows(a.M, a.L, chunks * blocks, 160, 1024);
     const dim3 grid((unsigned)d.windows, (unsigned)chunks, (unsigned)(blocks * d.turns));
     if (a.M > 16)
         hipLaunchKernelGGL((lora_shrink_kernel<XF, WF, 2>), grid, dim3(64 * kShrinkWaves), 0, stream,
@@ -554,8 +568,8 @@ hipError_t launch_lora(const LoraArgs &a, int x_format, int w_format, int y_form
     const size_t per = (size_t)a.M * (size_t)a.R * sizeof(float);
     int64_t chunks = plan_chunks(a.M, a.K);
     if ((uint64_t)chunks > work_bytes / per) chunks = (int64_t)(work_bytes / per);
-    // a chunk is a group of 128 or more for each wave of a block
-    const int64_t share = kGroup * kShrinkWaves;
+    // whole batches of steps for every wave of a block
+    const int64_t share = (a.M > 16 ? 64 : 128) * kShrinkWaves;
     const int64_t chunk = (a.K + share * chunks - 1) / (share * chunks) * share;
     chunks = (a.K + chunk - 1) / chunk;
     const bool wb = w_format == kBf16;
