@@ -26,6 +26,8 @@ namespace {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
@@ -145,10 +147,11 @@ struct Rows {
         return id;
     }
 
-    // Row of entry i of the list (the first one past its end).
-    __device__ __forceinline__ int64_t row(int i, int count) const {
-        return m0 + list[i < count ? i : 0];
+    // Row of entry i of the list (the first one past its end), from m0 on.
+    __device__ __forceinline__ uint32_t local(int i, int count) const {
+        return list[i < count ? i : 0];
     }
+    __device__ __forceinline__ int64_t row(int i, int count) const { return m0 + local(i, count); }
 };
 
 __device__ __forceinline__ int rank_of(const LoraArgs &p, int id) {
@@ -294,211 +297,262 @@ __device__ __forceinline__ v4u keep_first(v4u w, int keep) {
     return w;
 }
 
-// 16 consecutive values of a row, as loaded.
+// Four consecutive values of a row, as loaded; rows of an odd N are aligned like
+// their elements only.
 template <int YF>
-struct Raw16 {
-    uint32_t w[YF == kF32 ? 16 : 8];
+struct __attribute__((packed, aligned(YF == kF32 ? 4 : 2))) Four {
+    uint32_t w[YF == kF32 ? 4 : 2];
 };
 
-// Four words that are aligned like an element only (rows of an odd N).
-template <int YF>
-struct __attribute__((packed, aligned(YF == kF32 ? 4 : 2))) Words4 {
-    uint32_t w[4];
-};
+// A window's rows of base or y: 16 or 8 bytes a lane. Rows are addressed from the
+// window's first (128 rows of PQ2_LORA_MAX_N float32 are 2^29 bytes).
+// EVEN: every row begins at a multiple of four bytes, and the accesses are buffer
+// accesses that a lane without a row, or at the end of a row, makes outside the
+// resource: no branches, so requests stay in flight across them. The ends of
+// rows (N % 4 columns) go element by element, as all does with other rows.
+template <int YF, bool EVEN>
+struct RowsOf {
+    static constexpr int kSize = YF == kF32 ? 4 : 2;
+    char *at;
+    int N;
+    __amdgpu_buffer_rsrc_t rs;
 
-// base of row m from column n on; `wide`: all 16 columns exist.
-template <int YF>
-__device__ __forceinline__ void load16(const LoraArgs &p, int64_t m, int64_t n, bool wide, Raw16<YF> &o) {
-    constexpr int V = YF == kF32 ? 4 : 2;
-    const int64_t at = m * p.N + n;
-    if (wide) {
-        const Words4<YF> *b = reinterpret_cast<const Words4<YF> *>(
-            static_cast<const char *>(p.base) + at * (YF == kF32 ? 4 : 2));
-#pragma unroll
-        for (int a = 0; a < V; ++a) {
-            const Words4<YF> u = b[a];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o.w[4 * a + k] = u.w[k];
-        }
-    } else if constexpr (YF == kF32) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-            o.w[e] = n + e < p.N ? static_cast<const uint32_t *>(p.base)[at + e] : 0;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-            const uint16_t *b = static_cast<const uint16_t *>(p.base) + at + e;
-            o.w[e / 2] = (n + e < p.N ? b[0] : 0) | (n + e + 1 < p.N ? (uint32_t)b[1] << 16 : 0);
-        }
-    }
-}
+    __device__ __forceinline__ RowsOf(const void *first, int N_, int64_t m0, int64_t rows)
+        : at(const_cast<char *>(static_cast<const char *>(first)) + m0 * N_ * kSize), N(N_),
+          rs(make_rsrc(at, rows * N_ * kSize)) {}
 
-// y of row m from column n on: the loaded base, plus d (ADD) rounded once.
-template <int YF, bool ADD>
-__device__ __forceinline__ void store16(const LoraArgs &p, int64_t m, int64_t n, bool wide,
-                                        const Raw16<YF> &base, const v4f (&d)[4]) {
-    const int64_t at = m * p.N + n;
-    uint32_t o[YF == kF32 ? 16 : 8];
+    __device__ __forceinline__ void load(uint32_t off, int n, bool live, Four<YF> &o) const {
+        if constexpr (EVEN) {
+            const int off4 = live && n + 4 <= N ? (int)off : kCopyOob;
+            if constexpr (YF == kF32) {
+                const v4u u = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rs, off4, 0, 0));
 #pragma unroll
-    for (int i = 0; i < (YF == kF32 ? 16 : 8); ++i) {
-        const uint32_t u = base.w[i];
-        if constexpr (!ADD) {
-            o[i] = u;
-        } else if constexpr (YF == kF32) {
-            const float f = d[i >> 2][i & 3];
-            o[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, u) + f);
+                for (int e = 0; e < 4; ++e) o.w[e] = u[e];
+            } else {
+                const v2u u = __builtin_bit_cast(v2u, __builtin_amdgcn_raw_buffer_load_b64(rs, off4, 0, 0));
+                o.w[0] = u[0];
+                o.w[1] = u[1];
+            }
+            if ((N & 3) == 0 || !live || n + 4 <= N) return;
         } else {
-            const float lo = d[i >> 1][2 * i & 3], hi = d[i >> 1][(2 * i & 3) + 1];
-            o[i] = (uint32_t)bf16_rne(__builtin_bit_cast(float, u << 16) + lo) |
-                   ((uint32_t)bf16_rne(__builtin_bit_cast(float, u & 0xffff0000u) + hi) << 16);
+            if (!live || n >= N) return;
+            if (n + 4 <= N) {
+                o = *reinterpret_cast<const Four<YF> *>(at + off);
+                return;
+            }
+            o = Four<YF>{};
+        }
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+            if (n + e >= N) continue;
+            if constexpr (YF == kF32)
+                o.w[e] = reinterpret_cast<const uint32_t *>(at + off)[e];
+            else
+                o.w[e / 2] |= (uint32_t) reinterpret_cast<const uint16_t *>(at + off)[e] << (16 * (e & 1));
         }
     }
-    if (wide) {
-        Words4<YF> *y = reinterpret_cast<Words4<YF> *>(static_cast<char *>(p.y) + at * (YF == kF32 ? 4 : 2));
+
+    __device__ __forceinline__ void store(uint32_t off, int n, bool live, const Four<YF> &o) const {
+        if constexpr (EVEN) {
+            const int off4 = live && n + 4 <= N ? (int)off : kCopyOob;
+            if constexpr (YF == kF32)
+                __builtin_amdgcn_raw_buffer_store_b128(v4u{o.w[0], o.w[1], o.w[2], o.w[3]}, rs, off4, 0, 0);
+            else
+                __builtin_amdgcn_raw_buffer_store_b64(v2u{o.w[0], o.w[1]}, rs, off4, 0, 0);
+            if ((N & 3) == 0 || !live || n + 4 <= N) return;
+        } else {
+            if (!live || n >= N) return;
+            if (n + 4 <= N) {
+                *reinterpret_cast<Four<YF> *>(at + off) = o;
+                return;
+            }
+        }
 #pragma unroll
-        for (int a = 0; a < (YF == kF32 ? 4 : 2); ++a)
-            y[a] = Words4<YF>{{o[4 * a], o[4 * a + 1], o[4 * a + 2], o[4 * a + 3]}};
-    } else if constexpr (YF == kF32) {
+        for (int e = 0; e < 3; ++e) {
+            if (n + e >= N) continue;
+            if constexpr (YF == kF32)
+                reinterpret_cast<uint32_t *>(at + off)[e] = o.w[e];
+            else
+                reinterpret_cast<uint16_t *>(at + off)[e] = (uint16_t)(o.w[e / 2] >> (16 * (e & 1)));
+        }
+    }
+};
+
+// base + d, rounded once.
+template <int YF>
+__device__ __forceinline__ Four<YF> add4(Four<YF> base, const float (&d)[4]) {
+    if constexpr (YF == kF32) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-            if (n + e < p.N) static_cast<uint32_t *>(p.y)[at + e] = o[e];
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t u = base.w[e];
+            base.w[e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, u) + d[e]);
+        }
     } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-            if (n + e < p.N)
-                static_cast<uint16_t *>(p.y)[at + e] = (uint16_t)(e & 1 ? o[e / 2] >> 16 : o[e / 2]);
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t u = base.w[e];
+            // v_cvt_pk_bf16_f32: to nearest even, two at once
+            const v2bf o = {(__bf16)(__builtin_bit_cast(float, u << 16) + d[2 * e]),
+                            (__bf16)(__builtin_bit_cast(float, u & 0xffff0000u) + d[2 * e + 1])};
+            base.w[e] = __builtin_bit_cast(uint32_t, o);
+        }
     }
+    return base;
 }
 
-// Expand: a block forms its rows x 256 columns of y, adapter by adapter, 16 rows
-// and 64 ranks at a time: the block's threads add the K chunks' sums of v,
+// Expand: a block forms its rows x 256 columns of y, adapter by adapter, in stages
+// of 16 rows and 64 ranks: the block's threads add the K chunks' sums of v,
 // apply the adapter's scale and leave v's three bfloat16 parts in LDS, then each
-// wave multiplies them by B's rows of its 64 columns (in registers; kept from
-// tile to tile up to rank 64). Operand A is B's rows (columns of y), operand B
-// the rows' v: row 4 c + i of MFMA tile a is column 16 c + 4 a + i, so that the
-// four tiles leave a lane with 16 consecutive columns of one row, and four
-// lanes with 64.
+// wave multiplies them by B's rows of its 64 columns. Operand A is the rows' v,
+// operand B is B's rows (columns of y): column r of MFMA tile a is column
+// 4 r + a, so that the four tiles leave a lane with four consecutive columns of
+// the rows 4 c + i, and 16 neighbouring lanes read and write 64 consecutive
+// columns of one row.
+// PIPE (R <= 64): B's vectors stay in registers over an adapter's stages, and a
+// stage's v and base are requested while the one before is computed.
+// Memory-bound for many rows (4096 x 17408 bfloat16, rank 64: 74 us, 3.9 TB/s of
+// base, y and v), a chain of four dependent reads for a few.
 constexpr int kExpandRows = 16;
 constexpr int kExpandStride = 144;             // LDS bytes of a row's 64 ranks (128 + pad)
 
-template <int WF, int YF>
+template <int WF, int YF, bool EVEN, bool PIPE>
 __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs p, const float *__restrict__ v,
                                                           int chunks, int window, int turns) {
     __shared__ uint8_t lists[4][kWindow];
-    __shared__ __attribute__((aligned(16))) uint8_t vparts[3][kExpandRows * kExpandStride];
-    constexpr int U = kExpandRows / 16;
+    __shared__ __attribute__((aligned(16))) uint8_t vparts[2][3][kExpandRows * kExpandStride];
     const int tid = threadIdx.x;
     const int lane = tid & (kWave - 1), wave = tid / kWave;
     const int r = lane & 15, c = lane >> 4;
-    const int64_t n0 = ((int64_t)blockIdx.y * 4 + wave) * 64;
-    const int64_t n = n0 + 16 * c;             // this lane's columns
-    const bool wide = n + 16 <= p.N;
-    const uint16_t *wrow[4];
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-        const int64_t col = n0 + 16 * (r >> 2) + 4 * a + (r & 3);
-        wrow[a] = static_cast<const uint16_t *>(p.b) + (col < p.N ? col : p.N - 1) * p.R + 8 * c;
-    }
-    Rows rows(p, (int64_t)blockIdx.x * window, window, lists[wave]);
+    const int N = (int)p.N, R = (int)p.R;
+    const int n = ((int)blockIdx.y * 4 + wave) * 64 + 4 * r;   // this lane's columns
+    const int64_t m0 = (int64_t)blockIdx.x * window;
+    const int64_t in = p.M - m0 < window ? p.M - m0 : window;  // rows of the window
+    const RowsOf<YF, EVEN> base(p.base, N, m0, in), y(p.y, N, m0, in);
+    const int entry = tid >> 4, k = 4 * (tid & 15);            // this thread's part of a stage's v
+    Rows rows(p, m0, window, lists[wave]);
+    int stage = 0;
     for (int at = 0; rows.any(); ++at) {
         const int id = rows.next();
         if (at % turns != (int)blockIdx.z) continue;
         const int count = rows.take(id);
         const int rank = rank_of(p, id);
         const float scale = p.scale ? p.scale[id] : 1.0f;
-        const int64_t wbase = (int64_t)id * p.N * p.R;
-        v4u w[2][4] = {};
-        for (int i0 = 0; i0 < count; i0 += kExpandRows) {
-            const int live = min(count - i0, kExpandRows);
-            // the base, B's vectors and v are requested together
-            int64_t m[U];
-            Raw16<YF> base[U];
+        // B's rows of the lane's columns: columns past N read zeros
+        const __amdgpu_buffer_rsrc_t rs_b = make_rsrc(
+            static_cast<const uint16_t *>(p.b) + (int64_t)id * N * R, (int64_t)N * R * 2);
+        v4u w[2][4];
+        auto load_w = [&](int kc) __attribute__((always_inline)) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                m[u] = rows.row(i0 + 16 * u + r, count);
-                if (16 * u + r < live && n < p.N) load16<YF>(p, m[u], n, wide, base[u]);
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int a = 0; a < 4; ++a)
+                    w[j][a] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(
+                        rs_b, rank > kc + 32 * j + 8 * c ? 2 * (n * R + kc + 32 * j + 8 * c) : kCopyOob,
+                        2 * a * R, 0));
+        };
+        auto mask_w = [&](int kc) __attribute__((always_inline)) {
+            if ((rank & 7) == 0) return;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int a = 0; a < 4; ++a) w[j][a] = keep_first(w[j][a], rank - (kc + 32 * j + 8 * c));
+        };
+        // v of a stage: four ranks of an entry, from kc on, chunk s (ranks past
+        // R and entries past the list read zeros)
+        auto load_v = [&](int i0, int kc, int s) __attribute__((always_inline)) -> v4f {
+            const __amdgpu_buffer_rsrc_t rs_v = make_rsrc(v + (s * p.M + m0) * R, in * R * 4);
+            const int off = i0 + entry < count && kc + k < R
+                                ? 4 * ((int)rows.local(i0 + entry, count) * R + kc + k) : kCopyOob;
+            return __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rs_v, off, 0, 0));
+        };
+        // A stage's first two chunks of v and its base, requested a stage ahead
+        // and in this order: waiting for v is then waiting for neither the base
+        // nor the stores of the stage before.
+        struct Stage {
+            v4f v[2];
+            uint32_t at[4];
+            Four<YF> b[4];
+        } cur, nxt;
+        auto request = [&](int i0, Stage &o) __attribute__((always_inline)) {
+            if constexpr (PIPE) {
+                o.v[0] = load_v(i0, 0, 0);
+                o.v[1] = chunks > 1 ? load_v(i0, 0, 1) : v4f{};
             }
-            v4f acc[U][4] = {};
-            for (int kc = 0; kc < rank; kc += 64) {
-                if (i0 == 0 || rank > 64) {    // else B's vectors are those of the last rows
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int a = 0; a < 4; ++a) {
-                            const int keep = rank - (kc + 32 * j + 8 * c);
-                            w[j][a] = v4u{};
-                            if (keep > 0)
-                                w[j][a] = *reinterpret_cast<const v4u *>(wrow[a] + wbase + kc + 32 * j);
-                        }
+            for (int i = 0; i < 4; ++i) {
+                const int e = i0 + 4 * c + i;
+                o.at[i] = (rows.local(e, count) * (uint32_t)N + (uint32_t)n) * RowsOf<YF, EVEN>::kSize;
+                base.load(o.at[i], n, e < count, o.b[i]);
+            }
+        };
+        if constexpr (PIPE) load_w(0);
+        request(0, cur);
+        if constexpr (PIPE) {
+            mask_w(0);
+            wait_vmem<0>();                    // B's vectors stay: no later wait is for them
+        }
+        for (int i0 = 0; i0 < count; i0 += kExpandRows) {
+            v4f acc[4] = {};
+            const int steps = PIPE ? 1 : rank;
+            for (int kc = 0; kc < steps; kc += 64, stage ^= 1) {
+                v4f f;
+                int s = 0;
+                if constexpr (!PIPE) {
+                    load_w(kc);
+                    f = v4f{};
+                } else {
+                    f = cur.v[0] + cur.v[1];
+                    s = 2;
                 }
-                v4f f[U];                      // four ranks of an entry each
-#pragma unroll
-                for (int e = 0; e < U; ++e) {
-                    const int entry = 16 * e + (tid >> 4), k = kc + 4 * (tid & 15);
-                    f[e] = v4f{};
-                    if (entry < live && k < rank) {
-                        const float *src = v + rows.row(i0 + entry, count) * p.R + k;
 #pragma unroll 4
-                        for (int s = 0; s < chunks; ++s)
-                            f[e] += *reinterpret_cast<const v4f *>(src + s * p.M * p.R);
-                    }
+                for (; s < chunks; ++s) f += load_v(i0, kc, s);
+                float g[8] = {};
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) f[e][q] = k + q < rank ? f[e][q] * scale : 0.0f;
-                }
-                ring_barrier();                // the parts of the last step have been read
+                for (int q = 0; q < 4; ++q) g[q] = kc + k + q < rank ? f[q] * scale : 0.0f;
+                v4u part[3];
+                split8(g, part);
 #pragma unroll
-                for (int e = 0; e < U; ++e) {
-                    const float g[8] = {f[e][0], f[e][1], f[e][2], f[e][3]};
-                    v4u part[3];
-                    split8(g, part);
+                for (int i = 0; i < 3; ++i)
+                    *reinterpret_cast<uint2 *>(vparts[stage][i] + entry * kExpandStride + 2 * k) =
+                        make_uint2(part[i][0], part[i][1]);
+                // one barrier a step: the other buffer's readers are past it
+                ring_barrier();
+                if ((PIPE || kc + 64 >= rank) && i0 + kExpandRows < count)
+                    request(i0 + kExpandRows, nxt);
+                if constexpr (!PIPE) mask_w(kc);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (kc + 32 * j >= rank) continue;
+                    v4u vp[3];
 #pragma unroll
                     for (int i = 0; i < 3; ++i)
-                        *reinterpret_cast<uint2 *>(vparts[i] + (16 * e + (tid >> 4)) * kExpandStride +
-                                                   8 * (tid & 15)) = make_uint2(part[i][0], part[i][1]);
-                }
-                ring_barrier();
-                if ((rank & 7) && (i0 == 0 || rank > 64)) {
+                        vp[i] = *reinterpret_cast<const v4u *>(
+                            vparts[stage][i] + r * kExpandStride + 64 * j + 16 * c);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int a = 0; a < 4; ++a)
-                            w[j][a] = keep_first(w[j][a], rank - (kc + 32 * j + 8 * c));
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (16 * u >= live) continue;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        if (kc + 32 * j >= rank) continue;
-                        v4u vp[3];
-#pragma unroll
-                        for (int i = 0; i < 3; ++i)
-                            vp[i] = *reinterpret_cast<const v4u *>(
-                                vparts[i] + (16 * u + r) * kExpandStride + 64 * j + 16 * c);
-#pragma unroll
-                        for (int a = 0; a < 4; ++a) {
-                            v4u wp[kParts<WF>];
-                            parts_of<WF>(w[j][a], wp);
-                            acc[u][a] = mfma_parts(wp, vp, acc[u][a]);
-                        }
+                    for (int a = 0; a < 4; ++a) {
+                        v4u wp[kParts<WF>];
+                        parts_of<WF>(w[j][a], wp);
+                        acc[a] = mfma_parts(vp, wp, acc[a]);
                     }
                 }
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (16 * u + r < live && n < p.N) store16<YF, true>(p, m[u], n, wide, base[u], acc[u]);
+            for (int i = 0; i < 4; ++i) {
+                const float d[4] = {acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
+                y.store(cur.at[i], n, i0 + 4 * c + i < count, add4<YF>(cur.b[i], d));
+            }
+            cur = nxt;
         }
     }
-    if (blockIdx.z != 0) return;
-    if (p.base == p.y) return;
+    if (blockIdx.z != 0 || p.base == p.y) return;
     const int count = rows.take(-1);           // rows without an adapter (every lane takes part)
-    if (n >= p.N) return;
-    const v4f none[4] = {};
-    for (int i = r; i < count; i += 16) {
-        const int64_t m = rows.row(i, count);
-        Raw16<YF> base;
-        load16<YF>(p, m, n, wide, base);
-        store16<YF, false>(p, m, n, wide, base, none);
+    for (int i = 0; i < count; i += 4) {
+        const uint32_t off = (rows.local(i + c, count) * (uint32_t)N + (uint32_t)n) *
+                             RowsOf<YF, EVEN>::kSize;
+        Four<YF> o;
+        base.load(off, n, i + c < count, o);
+        y.store(off, n, i + c < count, o);
     }
 }
 
@@ -552,9 +606,19 @@ template <int WF, int YF>
 void launch_expand(const LoraArgs &a, const float *v, int64_t chunks, hipStream_t stream) {
     const int64_t cols = (a.N + 255) / 256;
     const Deal d = deal_rows(a.M, a.L, cols, 256, 2048);
-    hipLaunchKernelGGL((lora_expand_kernel<WF, YF>),
-                       dim3((unsigned)d.windows, (unsigned)cols, (unsigned)d.turns), dim3(256), 0,
-                       stream, a, v, (int)chunks, d.window, d.turns);
+    const dim3 grid((unsigned)d.windows, (unsigned)cols, (unsigned)d.turns);
+    const bool even = YF == kF32 || (a.N % 2 == 0 && (((uintptr_t)a.base | (uintptr_t)a.y) & 3) == 0);
+    auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a, v, (int)chunks, d.window, d.turns);
+    };
+    // many 16-row stages of one adapter (4096 rows of 17408 columns, rank 64: 74 us
+    // pipelined, 101 not; 16 rows of 16 adapters: 19.6 against 15.1)
+    if (a.R <= 64 && a.M > 1024)
+        even ? launch(lora_expand_kernel<WF, YF, true, true>)
+             : launch(lora_expand_kernel<WF, YF, false, true>);
+    else
+        even ? launch(lora_expand_kernel<WF, YF, true, false>)
+             : launch(lora_expand_kernel<WF, YF, false, false>);
 }
 
 }  // namespace
