@@ -10,7 +10,6 @@ Importing this package raises if ``libpq2.so`` has not been built
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -159,28 +158,40 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape: Tuple[int, ...]
 
 
 def _ptr(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: Tuple[int, ...],
-         device: torch.device) -> int:
-    """Address of a contiguous tensor of this type and shape on `device` (0 for
-    None); raises what _need raises, and ValueError for another device."""
+         index: int) -> int:
+    """Address of a contiguous tensor of this type and shape on GPU `index` (0 for
+    None); raises what _need raises, and ValueError for another GPU."""
     if t is None:
         return 0
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda
-            and t.is_contiguous()):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == index and t.is_contiguous()):
         _need(t, name, dtype, shape)
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     return t.data_ptr()
 
 
-def _launch_on(device: torch.device):
-    """Context in which a launch goes to `device` (a kernel runs on the current
-    device, which need not be the tensors')."""
-    if torch.cuda.current_device() == device.index:
-        return _HERE_ALREADY
-    return torch.cuda.device(device)
+def _gpu(t: torch.Tensor, name: str) -> int:
+    """Index of the GPU a tensor is on."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return index
 
 
-_HERE_ALREADY = contextlib.nullcontext()
+def _launch(index: int, stream, call, *args) -> None:
+    """call(*args, stream) on GPU `index`: a kernel runs on the current device,
+    which need not be the tensors'."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if torch._C._cuda_getDevice() == index:
+        _check(call(*args, raw))
+        return
+    with torch.cuda.device(index):
+        _check(call(*args, raw))
+
+
 _ACT_FORMAT = {torch.float32: ACT_F32, torch.bfloat16: ACT_BF16, torch.float16: ACT_F16}
 
 
@@ -239,23 +250,20 @@ def pq2_norm_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     fmt = _format(x, "x")
     M, K = _mk(x)
     G = K // GROUP
-    ty, dev = x.dtype, x.device
-    xp = _ptr(x, "x", ty, (M, K), dev)
+    ty, at = x.dtype, _gpu(x, "x")
     gate_rows = 0
     if gate is not None:
         if not isinstance(gate, torch.Tensor) or gate.dim() not in (1, 2):
             raise ValueError("gate must be a 1-D or 2-D tensor")
         gate_rows = 1 if gate.dim() == 1 else int(gate.shape[0])
         gate = gate.view(1, -1) if gate.dim() == 1 else gate
-    args = (xp, fmt, _ptr(residual, "residual", ty, (M, K), dev),
-            _ptr(w_post, "w_post", torch.float32, (K,), dev),
-            _ptr(gate, "gate", ty, (gate_rows, K), dev), gate_rows, alpha,
-            _ptr(w_pre, "w_pre", torch.float32, (K,), dev), eps, _ptr(h, "h", ty, (M, K), dev),
-            _ptr(n, "n", ty, (M, K), dev), _ptr(q, "q", torch.int8, (M, K), dev),
-            _ptr(s, "s", torch.float32, (M, G), dev), _ptr(t, "t", torch.int32, (M, G), dev), M, K,
-            _stream(x, stream))
-    with _launch_on(dev):
-        _check(lib.pq2_norm_quantize(*args))
+    mk = (M, K)
+    _launch(at, stream, lib.pq2_norm_quantize, _ptr(x, "x", ty, mk, at), fmt,
+            _ptr(residual, "residual", ty, mk, at), _ptr(w_post, "w_post", torch.float32, (K,), at),
+            _ptr(gate, "gate", ty, (gate_rows, K), at), gate_rows, alpha,
+            _ptr(w_pre, "w_pre", torch.float32, (K,), at), eps, _ptr(h, "h", ty, mk, at),
+            _ptr(n, "n", ty, mk, at), _ptr(q, "q", torch.int8, mk, at),
+            _ptr(s, "s", torch.float32, (M, G), at), _ptr(t, "t", torch.int32, (M, G), at), M, K)
 
 
 def _workspace(workspace, M: int, N: int, K: int, device, stream,
@@ -369,21 +377,19 @@ def pq2_gemm_grouped(q: torch.Tensor, s: torch.Tensor, t: torch.Tensor, codes: t
     if codes.dim() != 3 or y.dim() != 2:
         raise ValueError("expected 3-D codes and 2-D y")
     E, N, T = int(codes.shape[0]), int(codes.shape[1]), int(y.shape[0])
-    dev = q.device
     if y.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"y must be float32 or bfloat16, got {y.dtype}")
+    at = _gpu(q, "q")
     if wscale.dtype == torch.float16:
         wscale = wscale.view(torch.int16)
-    args = (_ptr(q, "q", torch.int8, (R, K), dev), _ptr(s, "s", torch.float32, (R, G), dev),
-            _ptr(t, "t", torch.int32, (R, G), dev), R,
-            _ptr(codes, "codes", torch.uint8, (E, N, K // 4), dev),
-            _ptr(wscale, "wscale", torch.int16, (E, N, G), dev),
-            _ptr(offsets, "offsets", torch.int32, (E + 1,), dev), E,
-            _ptr(rows, "rows", torch.int32, (T,), dev),
-            _ptr(row_scale, "row_scale", torch.float32, (T,), dev),
-            _ptr(y, "y", y.dtype, (T, N), dev), _ACT_FORMAT[y.dtype], T, N, K, _stream(q, stream))
-    with _launch_on(dev):
-        _check(lib.pq2_gemm_grouped(*args))
+    _launch(at, stream, lib.pq2_gemm_grouped, _ptr(q, "q", torch.int8, (R, K), at),
+            _ptr(s, "s", torch.float32, (R, G), at), _ptr(t, "t", torch.int32, (R, G), at), R,
+            _ptr(codes, "codes", torch.uint8, (E, N, K // 4), at),
+            _ptr(wscale, "wscale", torch.int16, (E, N, G), at),
+            _ptr(offsets, "offsets", torch.int32, (E + 1,), at), E,
+            _ptr(rows, "rows", torch.int32, (T,), at),
+            _ptr(row_scale, "row_scale", torch.float32, (T,), at), _ptr(y, "y", y.dtype, (T, N), at),
+            _ACT_FORMAT[y.dtype], T, N, K)
 
 
 def pq2_lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter: torch.Tensor,
@@ -400,26 +406,23 @@ def pq2_lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter: tor
     tensor of lora_workspace_bytes(M, K, R) bytes (at least M * R floats)."""
     fmt = _format(x, "x")
     M, K = _mk(x)
-    dev = x.device
     if a.dim() != 3 or b.dim() != 3:
         raise ValueError("expected 3-D a and b")
     if a.dtype not in (torch.bfloat16, torch.float16):
         raise TypeError(f"a must be bfloat16 or float16, got {a.dtype}")
     if y.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"y must be float32 or bfloat16, got {y.dtype}")
+    at = _gpu(x, "x")
     L, R, N = int(a.shape[0]), int(a.shape[1]), int(b.shape[1])
-    args = (_ptr(x, "x", x.dtype, (M, K), dev), fmt, _ptr(a, "a", a.dtype, (L, R, K), dev),
-            _ptr(b, "b", a.dtype, (L, N, R), dev), _ACT_FORMAT[a.dtype],
-            _ptr(adapter, "adapter", torch.int32, (M,), dev),
-            _ptr(ranks, "ranks", torch.int32, (L,), dev),
-            _ptr(scale, "scale", torch.float32, (L,), dev),
-            _ptr(base, "base", y.dtype, (M, N), dev), _ptr(y, "y", y.dtype, (M, N), dev),
-            _ACT_FORMAT[y.dtype], M, N, K, R, L)
-    wp, wn, _keep = _workspace(workspace, M, K, R, dev, stream, lora_workspace_bytes)
-    if _keep is not None and _keep.device != dev:
-        raise ValueError(f"workspace must be on {dev}, got {_keep.device}")
-    with _launch_on(dev):
-        _check(lib.pq2_lora_add(*args, wp, wn, _stream(x, stream)))
+    args = (_ptr(x, "x", x.dtype, (M, K), at), fmt, _ptr(a, "a", a.dtype, (L, R, K), at),
+            _ptr(b, "b", a.dtype, (L, N, R), at), _ACT_FORMAT[a.dtype],
+            _ptr(adapter, "adapter", torch.int32, (M,), at), _ptr(ranks, "ranks", torch.int32, (L,), at),
+            _ptr(scale, "scale", torch.float32, (L,), at), _ptr(base, "base", y.dtype, (M, N), at),
+            _ptr(y, "y", y.dtype, (M, N), at), _ACT_FORMAT[y.dtype], M, N, K, R, L)
+    wp, wn, keep = _workspace(workspace, M, K, R, x.device, stream, lora_workspace_bytes)
+    if keep is not None and keep.get_device() != at:
+        raise ValueError(f"workspace must be on cuda:{at}, got {keep.device}")
+    _launch(at, stream, lib.pq2_lora_add, *args, wp, wn)
 
 
 def pq2_linear(x: torch.Tensor, codes: torch.Tensor, wscale: torch.Tensor, y: torch.Tensor,

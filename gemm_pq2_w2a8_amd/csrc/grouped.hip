@@ -182,6 +182,12 @@ __global__ __launch_bounds__(64 * kStreamMaxWaves) void grouped_stream_kernel(Gr
         aoff[pl] = (r >> 2) == c ? 512 * (r & 3) + kGroup * c + 32 * (pl ^ (r & 3)) : -1;
     load_acts(wave, 0, run0);
     if (second < runs) load_acts(second, 1, run1);
+    // both runs' codes went out before the first run's activations: the first
+    // run is there once only the second's activations are in flight
+    if (second < runs)
+        wait_vmem<4>();
+    else
+        wait_vmem<0>();
 
     float acc[2][4] = {};
     auto compute = [&](const Run &o, int slot) __attribute__((always_inline)) {

@@ -165,6 +165,9 @@ SHAPES = {
     "rank_72": (33, 256, 50, 72, 2, "rows", None),
     "long_k": (5, 17408, 30, 16, 2, "rows", None),
     "many_rows": (1100, 128, 20, 8, 4, "rows", None),
+    "pipelined_odd": (1500, 256, 131, 40, 5, "rows", [40, 3, 17, 0, 33]),
+    "pipelined_runs": (1300, 256, 262, 64, 3, "runs", [64, 64, 10]),
+    "deep_many": (1100, 256, 70, 136, 3, "runs", None),
     "prompt": (700, 640, 515, 64, 2, "runs", [64, 17]),
 }
 TYPES = [(BF16, BF16, F32), (BF16, BF16, BF16), (F16, F16, F32), (F16, F16, BF16), (F32, BF16, F32),
@@ -269,6 +272,24 @@ def test_workspace_sizes(M, K, R):
         p.run(workspace=None)
     with pytest.raises(ValueError):
         p.run(workspace=torch.empty(full, dtype=torch.uint8))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [5, 1200])
+@pytest.mark.parametrize("N", [64, 66, 67])
+@pytest.mark.parametrize("yt", [F32, BF16])
+def test_outputs_aligned_like_their_elements(yt, N, M):
+    """base and y that begin one element after a 16-byte boundary, with guards."""
+    p = Problem(M, 256, N, 24, 3, seed=11, yt=yt, ranks=[24, 5, 16])
+    want = p.run()
+    d = p.device()
+    flat = [torch.full((M * N + 32,), 7.0, dtype=yt, device="cuda") for _ in range(2)]
+    base, y = (f[1:1 + M * N].view(M, N) for f in flat)
+    base.copy_(d["base"])
+    pq2.pq2_lora_add(**{**d, "base": base, "y": y})
+    assert torch.equal(y.cpu(), want)
+    assert (flat[1][:1] == 7).all() and (flat[1][1 + M * N:] == 7).all()
+    assert torch.equal(base, d["base"])
 
 
 @pytest.mark.gpu

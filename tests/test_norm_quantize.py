@@ -79,14 +79,45 @@ def test_binding_refusals():
         pq2.pq2_norm_quantize(torch.zeros(2, 2, 128))
 
 
-def test_binding_refuses_another_device(monkeypatch):
-    """Tensors of one call share a device."""
-    class Fake:
-        dtype, shape, is_cuda, device = torch.float32, (2, 128), True, torch.device("cuda:1")
-        is_contiguous = staticmethod(lambda: True)
-    monkeypatch.setattr(pq2.torch, "Tensor", Fake)
-    with pytest.raises(ValueError, match="must be on cuda:0"):
-        pq2._ptr(Fake(), "residual", torch.float32, (2, 128), torch.device("cuda:0"))
+class Elsewhere(torch.Tensor):
+    """A tensor that says it is on another GPU (no such GPU is needed to ask)."""
+    get_device = lambda self: 1                      # noqa: E731
+    is_cuda, device = True, torch.device("cuda:1")
+
+
+def test_binding_refuses_another_device():
+    """Tensors of one call share a GPU, and the launch is made on theirs."""
+    other = torch.zeros(2, 128).as_subclass(Elsewhere)
+    assert pq2._ptr(other, "x", torch.float32, (2, 128), 1) == other.data_ptr()
+    with pytest.raises(ValueError, match="residual must be on cuda:0, got cuda:1"):
+        pq2._ptr(other, "residual", torch.float32, (2, 128), 0)
+    with pytest.raises(ValueError, match="GPU"):
+        pq2._gpu(torch.zeros(2, 128), "x")
+
+
+def test_launch_is_on_the_tensors_device(monkeypatch):
+    seen = []
+
+    class On:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            seen.append(("enter", self.index))
+
+        def __exit__(self, *_):
+            seen.append("exit")
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", On)
+    call = lambda *a: seen.append(a) or 0            # noqa: E731
+    pq2._launch(0, None, call, 1, 2)
+    pq2._launch(1, None, call, 3)
+    pq2._launch(1, 55, call, 4)
+    assert seen == [(1, 2, 100), ("enter", 1), (3, 101), "exit", ("enter", 1), (4, 55), "exit"]
+    with pytest.raises(pq2.PQ2Error):
+        pq2._launch(0, None, lambda *a: ERR_ARG)
 
 
 # ------------------------------------------------------------------ reference
