@@ -5,7 +5,11 @@
 //   y[i][n] = row_scale[i] * sum_g s[row][g] ws[e][n][g] D(q[row], codes[e][n], g).
 // The offsets are only known on the device, so the grid covers the largest
 // number of row tiles any offsets can give and every wave finds its own tile
-// (find_tile); blocks past the last tile end at once.
+// (TileScan); blocks past the last tile end at once.
+//
+// Kernels: the stream kernel below for a mean of up to four slots an expert, the
+// prefill tiles of prefill_mfma.hip over gathered slots above that, and a plain
+// kernel for arrays beyond 31-bit offsets.
 #include "pq2_device.hpp"
 #include "pq2_grouped.hpp"
 #include "pq2_launch.hpp"
@@ -71,8 +75,7 @@ __global__ __launch_bounds__(256) void grouped_small_kernel(GroupedArgs p) {
     for (int i = 0; i < 4; ++i) {
         if (4 * c + i >= tile.count) continue;
         const int64_t slot = tile.first + 4 * c + i;
-        const float v = p.row_scale ? p.row_scale[slot] * acc[i] : acc[i];
-        store_y(p.y, p.y16, slot * p.N + n0 + r, v);
+        store_y(p.y, p.y16, slot * p.N + n0 + r, slot_value(p, slot, acc[i]));
     }
 }
 
@@ -274,8 +277,7 @@ __global__ __launch_bounds__(64 * kStreamMaxWaves) void grouped_stream_kernel(Gr
         float v = red[o];
         for (int w = 1; w < waves; ++w) v += red[w * kStreamSlots * kStreamCols + o];
         const int64_t i = tile.first + slot;
-        if (p.row_scale) v *= p.row_scale[i];
-        store_y(p.y, p.y16, i * p.N + n0 + col, v);
+        store_y(p.y, p.y16, i * p.N + n0 + col, slot_value(p, i, v));
     }
 }
 

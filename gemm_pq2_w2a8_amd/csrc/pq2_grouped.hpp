@@ -86,6 +86,16 @@ __device__ __forceinline__ int64_t source_row(const GroupedArgs &p, const RowTil
     return row >= 0 && row < p.R ? row : -1;
 }
 
+// y of slot i from its float32 sum: the row scale
+// applied, and zero for a slot without activations whatever its scale holds.
+__device__ __forceinline__ float slot_value(const GroupedArgs &p, int64_t i, float sum) {
+    if (p.rows) {
+        const int64_t row = p.rows[i];
+        if (row < 0 || row >= p.R) return 0.0f;
+    }
+    return p.row_scale ? p.row_scale[i] * sum : sum;
+}
+
 // Dispatch slot b of nb to tile: slot b runs on XCD b % 8, and XCD x receives
 // the x-th contiguous run of tile numbers.
 constexpr int kNumXcd = 8;

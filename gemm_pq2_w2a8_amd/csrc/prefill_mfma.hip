@@ -77,15 +77,6 @@ __device__ __forceinline__ int tile_row(const GroupedOr<GROUPED> &grp, const Row
         return tok < toks ? tok : -1;
 }
 
-// Factor of a tile row's outputs.
-template <bool GROUPED>
-__device__ __forceinline__ float row_factor(const GroupedOr<GROUPED> &grp, int64_t m) {
-    if constexpr (GROUPED)
-        return grp.row_scale ? grp.row_scale[m] : 1.0f;
-    else
-        return 1.0f;
-}
-
 template <int WN, int WM, int WAVES_N, int WAVES_M>
 struct PfCfg {
     static constexpr int kThreads = 64 * WAVES_N * WAVES_M;
@@ -445,15 +436,21 @@ __global__ __launch_bounds__(64 * WAVES_N * WAVES_M) void prefill_mfma_kernel(
 #pragma unroll
         for (int b = 0; b < WM; ++b) {
             const int64_t m = m0 + ctx.tok_base + 16 * b + r;
+            if constexpr (GROUPED) {
+                if (m < m_end) {
+#pragma unroll
+                    for (int a = 0; a < WN; ++a)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[a][b][i] = slot_value(grp, m, acc[a][b][i]);
+                }
+            }
 #pragma unroll
             for (int a = 0; a < WN; ++a) {
                 const int64_t nb = n0 + ctx.row_base + 16 * a + 4 * lg;
                 if (m < m_end) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (nb + i < N)
-                            store_y(y, y16, m * N + nb + i,
-                                    GROUPED ? acc[a][b][i] * row_factor<GROUPED>(grp, m) : acc[a][b][i]);
+                        if (nb + i < N) store_y(y, y16, m * N + nb + i, acc[a][b][i]);
                 }
             }
         }
@@ -741,15 +738,21 @@ __global__ __launch_bounds__(64 * WAVES_N * WAVES_M) void prefill_ring_kernel(
 #pragma unroll
         for (int b = 0; b < WM; ++b) {
             const int64_t m = m0 + tok_base + 16 * b + r;
+            if constexpr (GROUPED) {
+                if (tok_base + 16 * b + r < toks) {
+#pragma unroll
+                    for (int a = 0; a < WN; ++a)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[a][b][i] = slot_value(grp, m, acc[a][b][i]);
+                }
+            }
 #pragma unroll
             for (int a = 0; a < WN; ++a) {
                 const int64_t nb = n0 + row_base + 16 * a + 4 * lg;
                 if (tok_base + 16 * b + r < toks) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (nb + i < N)
-                            store_y(y, y16, m * N + nb + i,
-                                    GROUPED ? acc[a][b][i] * row_factor<GROUPED>(grp, m) : acc[a][b][i]);
+                        if (nb + i < N) store_y(y, y16, m * N + nb + i, acc[a][b][i]);
                 }
             }
         }
@@ -1131,11 +1134,10 @@ void prefill_wide_kernel(const int8_t *__restrict__ q, const float *__restrict__
             const int64_t m = m0 + 16 * b + r;
             if (16 * b + r >= toks) continue;
             if constexpr (GROUPED) {
-                const float f = row_factor<GROUPED>(grp, m);
 #pragma unroll
                 for (int a = 0; a < WN; ++a)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[a][b][i] *= f;
+                    for (int i = 0; i < 4; ++i) acc[a][b][i] = slot_value(grp, m, acc[a][b][i]);
             }
 #pragma unroll
             for (int a = 0; a < WN; ++a) {

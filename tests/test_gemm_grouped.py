@@ -217,10 +217,18 @@ def test_random_shapes(seed):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("counts,N,K", [([3, 9, 0, 1], 50, 384), ([40, 9, 130], 70, 1024),
-                                        ([500, 1], 300, 1024)])
+                                        ([500, 1], 300, 1024), ([20, 5, 9], 40, 1024),
+                                        ([9, 5, 0, 14, 7], 70, 1024), ([170, 3], 9000, 1024)])
 def test_rows_out_of_range_give_zeros(counts, N, K):
+    """Also where such a slot's row scale is no number."""
     p = Problem(counts, N, K, R=6, seed=4, weighted=True, invalid=True)
-    p.check(p.run())
+    want = p.run()
+    p.check(want)
+    bad = (p.rows < 0) | (p.rows >= 6)
+    assert bad.any() and not want[bad].any()
+    p.row_scale[bad] = np.where(np.arange(bad.sum()) % 2 == 0, np.nan, np.inf)
+    got = p.run()
+    assert (got == want).all()
 
 
 @pytest.mark.gpu
