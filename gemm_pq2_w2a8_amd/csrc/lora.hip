@@ -485,13 +485,14 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs p, const floa
                 base.load(o.at[i], n, e < count, o.b[i]);
             }
         };
-        if constexpr (PIPE) load_w(0);
-        request(0, cur);
         if constexpr (PIPE) {
+            load_w(0);
+            request(0, cur);
             mask_w(0);
             wait_vmem<0>();                    // B's vectors stay: no later wait is for them
         }
         for (int i0 = 0; i0 < count; i0 += kExpandRows) {
+            if constexpr (!PIPE) request(i0, cur);
             v4f acc[4] = {};
             const int steps = PIPE ? 1 : rank;
             for (int kc = 0; kc < steps; kc += 64, stage ^= 1) {
@@ -517,9 +518,11 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs p, const floa
                         make_uint2(part[i][0], part[i][1]);
                 // one barrier a step: the other buffer's readers are past it
                 ring_barrier();
-                if ((PIPE || kc + 64 >= rank) && i0 + kExpandRows < count)
-                    request(i0 + kExpandRows, nxt);
-                if constexpr (!PIPE) mask_w(kc);
+                if constexpr (PIPE) {
+                    if (i0 + kExpandRows < count) request(i0 + kExpandRows, nxt);
+                } else {
+                    mask_w(kc);
+                }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -542,7 +545,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs p, const floa
                 const float d[4] = {acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
                 y.store(cur.at[i], n, i0 + 4 * c + i < count, add4<YF>(cur.b[i], d));
             }
-            cur = nxt;
+            if constexpr (PIPE) cur = nxt;
         }
     }
     if (blockIdx.z != 0 || p.base == p.y) return;
@@ -589,12 +592,17 @@ int plan_chunks(int64_t M, int64_t K) {
     return s < 1 ? 1 : (int)s;
 }
 
+// Whether the shrink takes 32 rows at once: prompts, or few adapters.
+bool shrink_pairs(int64_t M, int64_t L) {
+    return M > 1024 || (M < kWindow ? M : kWindow) > 16 * L;
+}
+
 template <int XF, int WF>
 void launch_shrink(const LoraArgs &a, float *v, int64_t chunk, int64_t chunks, hipStream_t stream) {
     const int64_t blocks = (a.R + kShrinkRanks - 1) / kShrinkRanks;
     const Deal d = deal_rows(a.M, a.L, chunks * blocks, 160, 1024);
     const dim3 grid((unsigned)d.windows, (unsigned)chunks, (unsigned)(blocks * d.turns));
-    if (a.M > 16)
+    if (shrink_pairs(a.M, a.L))
         hipLaunchKernelGGL((lora_shrink_kernel<XF, WF, 2>), grid, dim3(64 * kShrinkWaves), 0, stream,
                            a, v, chunk, d.window, d.turns);
     else
@@ -633,7 +641,7 @@ hipError_t launch_lora(const LoraArgs &a, int x_format, int w_format, int y_form
     int64_t chunks = plan_chunks(a.M, a.K);
     if ((uint64_t)chunks > work_bytes / per) chunks = (int64_t)(work_bytes / per);
     // whole batches of steps for every wave of a block
-    const int64_t share = (a.M > 16 ? 64 : 128) * kShrinkWaves;
+    const int64_t share = 32 * (shrink_pairs(a.M, a.L) ? kSteps<2> : kSteps<1>) * kShrinkWaves;
     const int64_t chunk = (a.K + share * chunks - 1) / (share * chunks) * share;
     chunks = (a.K + chunk - 1) / chunk;
     const bool wb = w_format == kBf16;
