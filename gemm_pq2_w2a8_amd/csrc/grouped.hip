@@ -75,7 +75,7 @@ __global__ __launch_bounds__(256) void grouped_small_kernel(GroupedArgs p) {
     for (int i = 0; i < 4; ++i) {
         if (4 * c + i >= tile.count) continue;
         const int64_t slot = tile.first + 4 * c + i;
-        store_y(p.y, p.y16, slot * p.N + n0 + r, slot_value(p, slot, acc[i]));
+        store_y(p.y, p.y16, slot * p.N + n0 + r, SlotScale(p, slot)(acc[i]));
     }
 }
 
@@ -277,7 +277,7 @@ __global__ __launch_bounds__(64 * kStreamMaxWaves) void grouped_stream_kernel(Gr
         float v = red[o];
         for (int w = 1; w < waves; ++w) v += red[w * kStreamSlots * kStreamCols + o];
         const int64_t i = tile.first + slot;
-        store_y(p.y, p.y16, i * p.N + n0 + col, slot_value(p, i, v));
+        store_y(p.y, p.y16, i * p.N + n0 + col, SlotScale(p, i)(v));
     }
 }
 

@@ -86,15 +86,21 @@ __device__ __forceinline__ int64_t source_row(const GroupedArgs &p, const RowTil
     return row >= 0 && row < p.R ? row : -1;
 }
 
-// y of slot i from its float32 sum: the row scale
-// applied, and zero for a slot without activations whatever its scale holds.
-__device__ __forceinline__ float slot_value(const GroupedArgs &p, int64_t i, float sum) {
-    if (p.rows) {
-        const int64_t row = p.rows[i];
-        if (row < 0 || row >= p.R) return 0.0f;
+// What a slot's float32 sums become: y = live ? scale * sum : 0 (a slot without
+// activations is zero whatever its row scale holds).
+struct SlotScale {
+    float scale;
+    bool live;
+
+    __device__ __forceinline__ SlotScale(const GroupedArgs &p, int64_t i) : scale(1.0f), live(true) {
+        if (p.row_scale) scale = p.row_scale[i];
+        if (p.rows) {
+            const int64_t row = p.rows[i];
+            live = row >= 0 && row < p.R;
+        }
     }
-    return p.row_scale ? p.row_scale[i] * sum : sum;
-}
+    __device__ __forceinline__ float operator()(float sum) const { return live ? scale * sum : 0.0f; }
+};
 
 // Dispatch slot b of nb to tile: slot b runs on XCD b % 8, and XCD x receives
 // the x-th contiguous run of tile numbers.

@@ -438,10 +438,11 @@ __global__ __launch_bounds__(64 * WAVES_N * WAVES_M) void prefill_mfma_kernel(
             const int64_t m = m0 + ctx.tok_base + 16 * b + r;
             if constexpr (GROUPED) {
                 if (m < m_end) {
+                    const SlotScale value(grp, m);
 #pragma unroll
                     for (int a = 0; a < WN; ++a)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[a][b][i] = slot_value(grp, m, acc[a][b][i]);
+                        for (int i = 0; i < 4; ++i) acc[a][b][i] = value(acc[a][b][i]);
                 }
             }
 #pragma unroll
@@ -740,10 +741,11 @@ __global__ __launch_bounds__(64 * WAVES_N * WAVES_M) void prefill_ring_kernel(
             const int64_t m = m0 + tok_base + 16 * b + r;
             if constexpr (GROUPED) {
                 if (tok_base + 16 * b + r < toks) {
+                    const SlotScale value(grp, m);
 #pragma unroll
                     for (int a = 0; a < WN; ++a)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[a][b][i] = slot_value(grp, m, acc[a][b][i]);
+                        for (int i = 0; i < 4; ++i) acc[a][b][i] = value(acc[a][b][i]);
                 }
             }
 #pragma unroll
@@ -1134,10 +1136,11 @@ void prefill_wide_kernel(const int8_t *__restrict__ q, const float *__restrict__
             const int64_t m = m0 + 16 * b + r;
             if (16 * b + r >= toks) continue;
             if constexpr (GROUPED) {
+                const SlotScale value(grp, m);
 #pragma unroll
                 for (int a = 0; a < WN; ++a)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[a][b][i] = slot_value(grp, m, acc[a][b][i]);
+                    for (int i = 0; i < 4; ++i) acc[a][b][i] = value(acc[a][b][i]);
             }
 #pragma unroll
             for (int a = 0; a < WN; ++a) {
