@@ -99,6 +99,8 @@ __global__ __launch_bounds__(256) void grouped_small_kernel(GroupedArgs p) {
 // Planes 1 and 3 of a code word are masked in place (4 * code) into an
 // accumulator of their own: 4 D = 4 d0 + d1, the factor taken out of the weight
 // scale, 5 bit operations per word instead of 7.
+// Bound by HBM: 64 experts of 2048 x 5120 with a slot each 45 us, 3.9 TB/s; 8 of
+// them (a chain of dependent reads: offsets, row, codes) 10.2 us.
 constexpr int kStreamCols = 32;
 constexpr int kStreamSlots = 4;
 constexpr int kStreamMaxWaves = 4;

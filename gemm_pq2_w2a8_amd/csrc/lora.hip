@@ -161,7 +161,8 @@ __device__ __forceinline__ int rank_of(const LoraArgs &p, int id) {
 
 // Shrink: a block sums one K chunk of its rows x 64 ranks, adapter by adapter,
 // 16 * TR rows at a time; its eight waves share the chunk's steps and meet in
-// LDS, added in wave order.
+// LDS, added in wave order. 4096 rows of 5120 bfloat16, rank 64: 28 us (42 MB of
+// x); 555 rows of 17408 with 11 adapters: 15 us.
 constexpr int kShrinkWaves = 8;
 
 // One wave's part of TR x T tiles: rows x (16 * TR), ranks w (16 * T), from k to
