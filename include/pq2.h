@@ -47,8 +47,10 @@
  *  PQ2_ERR_ALIGN a base pointer breaks the alignment stated above (a
  *                workspace, when given, must be 16-byte aligned);
  *  PQ2_ERR_ARG   an invalid path selector (pq2_gemm_group_dots), a shape
- *                and workspace no fused kernel of pq2_linear runs, or an
- *                unknown activation format (pq2_quantize_act_16);
+ *                and workspace no fused kernel of pq2_linear runs, an unknown
+ *                format (pq2_quantize_act_16, pq2_norm_quantize,
+ *                pq2_gemm_grouped, pq2_lora_add), or an eps or alpha that
+ *                pq2_norm_quantize does not take;
  *  PQ2_ERR_SCRATCH (pq2_gemm_noalloc) the small-batch plan's split-K partial
  *                sums need more than PQ2_NOALLOC_SCRATCH_BYTES; (pq2_lora_add)
  *                the workspace holds fewer than M * R floats;

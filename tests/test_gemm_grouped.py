@@ -172,6 +172,7 @@ SHAPES = {
     "many_streams": ([1, 0, 2] * 20 + [6, 1], 1000, 1152),
     "staged_32": ([8, 17, 33, 3], 100, 1152),
     "many_experts": ([i % 4 for i in range(200)], 17, 256),
+    "most_experts": ([i % 2 for i in range(4096)], 9, 128),
     "over_4_per_lane": ([(i * 7) % 3 for i in range(700)], 16, 128),
 }
 

@@ -165,6 +165,8 @@ SHAPES = {
     "rank_72": (33, 256, 50, 72, 2, "rows", None),
     "long_k": (5, 17408, 30, 16, 2, "rows", None),
     "many_rows": (1100, 128, 20, 8, 4, "rows", None),
+    "many_adapters": (300, 256, 70, 8, 250, "rows", None),
+    "window_edge": (129, 512, 300, 48, 130, list(range(129)), [48 - i % 48 for i in range(130)]),
     "pipelined_odd": (1500, 256, 131, 40, 5, "rows", [40, 3, 17, 0, 33]),
     "pipelined_runs": (1300, 256, 262, 64, 3, "runs", [64, 64, 10]),
     "deep_many": (1100, 256, 70, 136, 3, "runs", None),

@@ -282,10 +282,13 @@ def test_outputs_are_optional_and_in_place(ty):
 def test_in_place_long_rows(K):
     f = inputs(3, K, torch.bfloat16, 5, True, True, 1, True)
     full = run(f, 1.0)
-    d = {k: v.cuda() for k, v in f.items()}
-    x = d.pop("x")
-    pq2.pq2_norm_quantize(x, alpha=1.0, eps=EPS, h=d["residual"], **d)
-    assert torch.equal(d["residual"], full["h"])
+    for target in ("residual", "x"):
+        d = {k: v.cuda() for k, v in f.items()}
+        q = torch.empty_like(full["q"])
+        s, t = torch.empty_like(full["s"]), torch.empty_like(full["t"])
+        pq2.pq2_norm_quantize(d["x"], q, s, t, residual=d["residual"], w_post=d["w_post"],
+                              w_pre=d["w_pre"], gate=d["gate"], alpha=1.0, eps=EPS, h=d[target])
+        same({"h": d[target], "q": q, "s": s, "t": t}, {k: full[k] for k in "hqst"})
 
 
 @pytest.mark.gpu
