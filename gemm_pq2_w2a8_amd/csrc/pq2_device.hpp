@@ -31,11 +31,13 @@ __device__ __forceinline__ float half_bits_to_float(uint16_t h) {
     return (float)__builtin_bit_cast(_Float16, h);
 }
 
-// float32 -> bfloat16 bits, rounded to nearest, ties to even (infinities and
-// NaN stay infinities and NaN).
+// float32 -> bfloat16 bits, rounded to nearest, ties to even; infinities stay
+// infinities, subnormals are kept and every NaN stays a NaN. The conversion
+// instruction: an integer addition of half a step carries out of the NaN
+// patterns 0x7fff.... and 0xffff.... and leaves a zero (the two agree on every
+// other pattern).
 __device__ __forceinline__ uint16_t bf16_rne(float v) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, v);
-    return (uint16_t)((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
+    return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
 // Output element i: float32 into y, or bfloat16 into y16 when that is given.
