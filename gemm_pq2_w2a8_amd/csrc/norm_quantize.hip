@@ -106,17 +106,25 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
     return s;
 }
 
-// 16 elements of value 1 in a format.
+// 16 elements of value 1, or -0, in a format.
 template <int FMT>
-__device__ __forceinline__ void ones(Raw16<FMT> &r) {
-    constexpr uint32_t w = FMT == 0 ? 0x3f800000u : FMT == 1 ? 0x3f803f80u : 0x3c003c00u;
+__device__ __forceinline__ void fill(Raw16<FMT> &r, uint32_t w) {
 #pragma unroll
     for (int k = 0; k < (FMT == 0 ? 4 : 2); ++k) r.w[k] = v4u{w, w, w, w};
 }
+template <int FMT>
+__device__ __forceinline__ void ones(Raw16<FMT> &r) {
+    fill(r, FMT == 0 ? 0x3f800000u : FMT == 1 ? 0x3f803f80u : 0x3c003c00u);
+}
+template <int FMT>
+__device__ __forceinline__ void minus_zeros(Raw16<FMT> &r) {
+    fill(r, FMT == 0 ? 0x80000000u : 0x80008000u);
+}
 
 // h of 16 elements: residual + alpha * gate * (x * scale * w_post). What the
-// call leaves out is 1 (weights, gate, scale) or 0 (residual) here, which
-// changes no bit of what is left and keeps the elements free of branches.
+// call leaves out is 1 (weights, gate, scale) or -0 (residual) here, which
+// changes no bit of what is left (+0 would turn a -0 into a +0) and keeps the
+// elements free of branches.
 template <int FMT>
 __device__ __forceinline__ void form_h(float alpha, const Raw16<FMT> &x, const Raw16<FMT> &r,
                                        const Raw16<FMT> &gt, const Raw16<0> &wp, float scale,
@@ -183,8 +191,9 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_quantize_kernel(NormArgs
             // loads it is 109 and four (4096 x 5120 bfloat16, both norms and a
             // residual: 45.5 us against 55.5; one row: 5.0 both ways). With two
             // groups per slot only x fits in registers beside h.
-            Raw16<FMT> x[NR] = {}, r = {}, gt;
+            Raw16<FMT> x[NR] = {}, r, gt;
             Raw16<0> wp, wq;
+            minus_zeros(r);
             ones<FMT>(gt);
             ones<0>(wp);
             ones<0>(wq);
@@ -209,7 +218,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_quantize_kernel(NormArgs
             for (int i = 0; i < NR; ++i) {
                 const int g = slot + i * slots;
                 if (NR > 1) {
-                    r = Raw16<FMT>{};
+                    minus_zeros(r);
                     if (g < G) load_rest(g, r, gt);
                 }
                 if (g < G) load_weights(a.w_post, g, wp);
@@ -245,8 +254,9 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_quantize_kernel(NormArgs
                     const int g = g0 + slot;
                     const bool live = g < G;
                     const int at = live ? g : G - 1;
-                    Raw16<FMT> x, r = {}, gt;
+                    Raw16<FMT> x, r, gt;
                     Raw16<0> wp, wq;
+                    minus_zeros(r);
                     ones<FMT>(gt);
                     ones<0>(wp);
                     ones<0>(wq);

@@ -404,3 +404,26 @@ def test_many_rows_and_offsets_past_32_bits(M, K):
     for sl in (slice(0, 3), slice(M // 2, M // 2 + 3), slice(M - 3, M)):
         h, q, s, t = pq2.norm_quantize(x[sl].contiguous(), w_pre=w, alpha=0.5)
         same({k: out[k][sl] for k in out}, {"h": h, "q": q, "s": s, "t": t})
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ty", list(TYPES))
+@pytest.mark.parametrize("K", [640, 17408, 32896])
+def test_signed_zeros_without_a_residual(K, ty):
+    """alpha * gate * p of powers of two is exact, its signed zeros among it: what
+    a call leaves out adds nothing, not even +0 to a -0."""
+    g = torch.Generator().manual_seed(K)
+    x = torch.randint(-3, 4, (3, K), generator=g).float()
+    x[:, 1::5] = -0.0
+    x[:, 2::5] = 0.0
+    gate = torch.where(torch.rand(K, generator=g) < 0.5, -2.0, 0.5)
+    bits = torch.int32 if ty == "f32" else torch.int16
+    print(f"signed zeros K={K} {ty}", flush=True)
+    for alpha, gt in ((1.0, None), (-0.5, None), (2.0, gate), (0.0, None)):
+        want = (alpha * x if gt is None else alpha * (x * gt)).to(TYPES[ty])
+        xd = x.to(TYPES[ty]).cuda()
+        h, n = torch.empty_like(xd), torch.empty_like(xd)
+        pq2.pq2_norm_quantize(xd, h=h, n=n, alpha=alpha,
+                              gate=None if gt is None else gt.to(TYPES[ty]).cuda())
+        assert torch.equal(h.cpu().view(bits), want.view(bits))
+        assert torch.equal(n.cpu().view(bits), want.view(bits))
