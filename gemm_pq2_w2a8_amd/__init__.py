@@ -10,6 +10,7 @@ Importing this package raises if ``libpq2.so`` has not been built
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -266,24 +267,31 @@ def pq2_norm_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None,
             _ptr(s, "s", torch.float32, (M, G), at), _ptr(t, "t", torch.int32, (M, G), at), M, K)
 
 
+def _on(stream, device):
+    """Context in which torch allocates from the pool of the stream that a call is
+    launched on: a block of another stream's pool may have work pending there
+    that nothing orders before the call."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
+                             torch.cuda.ExternalStream(int(stream), device=device))
+
+
 def _workspace(workspace, M: int, N: int, K: int, device, stream,
                query=None) -> Tuple[int, int, object]:
     """(pointer, bytes, keep-alive) of the split-K workspace argument: "auto"
     allocates the size pq2_gemm_workspace_bytes (or `query`) asks for with
     torch (none when 0), None passes no workspace, a device tensor passes its storage. An
-    "auto" buffer is tied to the launch stream, so torch's allocator does not
-    hand it out again before the kernels on that stream are done with it."""
+    "auto" buffer comes from the launch stream's pool: its earlier uses and its
+    next ones are on that stream too, and so in order with this call's."""
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError('workspace must be "auto", None or a device tensor')
         n = (query or gemm_workspace_bytes)(M, N, K)
         if n == 0:
             return 0, 0, None
-        workspace = torch.empty(n, dtype=torch.uint8, device=device)
-        if stream is not None:
-            st = stream if isinstance(stream, torch.cuda.Stream) else \
-                torch.cuda.ExternalStream(int(stream), device=device)
-            workspace.record_stream(st)
+        with _on(stream, device):
+            workspace = torch.empty(n, dtype=torch.uint8, device=device)
     if workspace is None:
         return 0, 0, None
     if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda:
