@@ -468,32 +468,46 @@ def pq2_gemm_group_dots(q: torch.Tensor, t: torch.Tensor, codes: torch.Tensor,
 
 # ---------------------------------------------------------------- allocating helpers
 
+def _returned(stream, *tensors: torch.Tensor):
+    """The tensors, recorded on the caller's stream where they come from the pool
+    of another: their memory is not used again before what the caller enqueues
+    there while holding them is done."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(torch.cuda.current_stream(t.device))
+    return tensors
+
+
+def _qst(M: int, K: int, device) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    return (torch.empty((M, K), dtype=torch.int8, device=device),
+            torch.empty((M, K // GROUP), dtype=torch.float32, device=device),
+            torch.empty((M, K // GROUP), dtype=torch.int32, device=device))
+
+
 def quantize_act(x: torch.Tensor, stream=None):
-    """Allocate q/s/t with torch and run pq2_quantize_act."""
+    """Allocate q/s/t with torch (from the launch stream's pool) and run
+    pq2_quantize_act."""
     M, K = _mk(x)
-    G = K // GROUP
-    q = torch.empty((M, K), dtype=torch.int8, device=x.device)
-    s = torch.empty((M, G), dtype=torch.float32, device=x.device)
-    t = torch.empty((M, G), dtype=torch.int32, device=x.device)
+    with _on(stream, x.device):
+        q, s, t = _qst(M, K, x.device)
     pq2_quantize_act(x, q, s, t, stream)
-    return q, s, t
+    return _returned(stream, q, s, t)
 
 
 def norm_quantize(x: torch.Tensor, *, residual: Optional[torch.Tensor] = None,
                   w_post: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
                   alpha: float = 1.0, w_pre: Optional[torch.Tensor] = None, eps: float = 1e-6,
                   stream=None):
-    """Allocate h and q/s/t with torch and run pq2_norm_quantize: (h, q, s, t)."""
+    """Allocate h and q/s/t with torch (from the launch stream's pool) and run
+    pq2_norm_quantize: (h, q, s, t)."""
     _format(x, "x")
     M, K = _mk(x)
-    G = K // GROUP
-    h = torch.empty_like(x)
-    q = torch.empty((M, K), dtype=torch.int8, device=x.device)
-    s = torch.empty((M, G), dtype=torch.float32, device=x.device)
-    t = torch.empty((M, G), dtype=torch.int32, device=x.device)
+    with _on(stream, x.device):
+        h = torch.empty_like(x)
+        q, s, t = _qst(M, K, x.device)
     pq2_norm_quantize(x, q, s, t, residual=residual, w_post=w_post, gate=gate, alpha=alpha,
                       w_pre=w_pre, eps=eps, h=h, stream=stream)
-    return h, q, s, t
+    return _returned(stream, h, q, s, t)
 
 
 def linear(x: torch.Tensor, codes: torch.Tensor, wscale: torch.Tensor,
@@ -502,12 +516,17 @@ def linear(x: torch.Tensor, codes: torch.Tensor, wscale: torch.Tensor,
     row (where quantising inside the GEMV beats the separate launch), else
     pq2_quantize_act (float32, bfloat16 or float16 x) into torch-allocated
     q/s/t followed by pq2_gemm."""
-    M = int(x.shape[0])
+    M, K = _mk(x)
     N = int(codes.shape[0])
-    y = out if out is not None else torch.empty((M, N), dtype=torch.float32, device=x.device)
-    if M == 1 and x.dtype == torch.float32:
+    fused = M == 1 and x.dtype == torch.float32
+    with _on(stream, x.device):
+        y = out if out is not None else torch.empty((M, N), dtype=torch.float32, device=x.device)
+        q, s, t = (None, None, None) if fused else _qst(M, K, x.device)
+    if fused:
         pq2_linear(x, codes, wscale, y, stream=stream)
-        return y
-    q, s, t = quantize_act(x, stream)
-    pq2_gemm(q, s, t, codes, wscale, y, stream=stream)
+    else:
+        pq2_quantize_act(x, q, s, t, stream)
+        pq2_gemm(q, s, t, codes, wscale, y, stream=stream)
+    if out is None:
+        _returned(stream, y)
     return y

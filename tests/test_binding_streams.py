@@ -175,3 +175,68 @@ def test_split_k_workspace_beside_pending_work(M, N, K, linear):
         return [y]
 
     unordered(call, [n] * 2, [want])
+
+
+# ------------------------------------------------------------------ tensors that helpers return
+
+def test_returned_tensors_come_from_the_launch_streams_pool(allocations, monkeypatch):
+    """q/s/t, h and y are written on the launch stream, so they come from its pool;
+    the caller's stream reads them, so they are recorded there."""
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: ("current", str(device)))
+    for name in ("pq2_quantize_act", "pq2_norm_quantize", "pq2_gemm", "pq2_linear"):
+        monkeypatch.setattr(pq2, name, lambda *a, **k: None)
+    codes, ws = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.int16)
+    x = torch.zeros(3, 256)
+    st = Stream()
+    calls = [(lambda s: pq2.quantize_act(x, stream=s), 3, 3),
+             (lambda s: pq2.norm_quantize(x, w_pre=x[0], stream=s), 4, 4),
+             (lambda s: pq2.linear(x[:1], codes, ws, stream=s), 1, 1),
+             (lambda s: pq2.linear(x, codes, ws, stream=s), 4, 1),      # q/s/t stay inside
+             (lambda s: pq2.linear(x, codes, ws, out=torch.zeros(3, 4), stream=s), 3, 0)]
+    for call, count, returned in calls:
+        for stream, want in ((None, None), (st, st), (7, ("external", 7, x.device))):
+            allocations.clear(), LOG.clear()
+            call(stream)
+            assert allocations == [want] * count
+            assert LOG == [("record", ("current", "cpu"))] * (returned if stream is not None else 0)
+
+
+@pytest.mark.gpu
+def test_helpers_beside_pending_work():
+    M, K, N = 64, 5120, 1024
+    g = torch.Generator().manual_seed(6)
+    x = torch.randn(M, K, generator=g).cuda()
+    w = torch.randn(K, generator=g).cuda()
+    cd = torch.randint(0, 256, (N, K // 4), generator=g, dtype=torch.uint8).cuda()
+    wd = (torch.rand(N, K // 128, generator=g) + 0.5).half().cuda()
+    sizes = [M * K * 4, M * K, M * (K // 128) * 4, M * N * 4]
+    for name, run in (("quantize_act", lambda s: pq2.quantize_act(x, stream=s)),
+                      ("norm_quantize", lambda s: pq2.norm_quantize(x, w_pre=w, stream=s)),
+                      ("linear", lambda s: [pq2.linear(x, cd, wd, stream=s)]),
+                      ("linear one row", lambda s: [pq2.linear(x[:1], cd, wd, stream=s)])):
+        print(f"{name} beside pending work", flush=True)
+        want = [v.clone() for v in run(None)]
+        unordered(run, sizes, want)
+
+
+@pytest.mark.gpu
+def test_returned_tensors_outlive_the_callers_pending_reads():
+    """q of a call on another stream, read on the current one behind long work and
+    dropped: the next call on that stream leaves what is still to be read alone."""
+    g = torch.Generator().manual_seed(7)
+    x = [torch.randn(64, 5120, generator=g).cuda() for _ in range(2)]
+    want = pq2.quantize_act(x[0])[0].clone()
+    busy = torch.ones(8192, 8192, dtype=torch.bfloat16, device="cuda")
+    st, copy = torch.cuda.Stream(), torch.zeros_like(want)
+    print("returned tensors and pending reads", flush=True)
+    for _ in range(2):
+        torch.cuda.synchronize()
+        q = pq2.quantize_act(x[0], stream=st)[0]
+        torch.cuda.current_stream().wait_stream(st)
+        for _ in range(20):
+            torch.mm(busy, busy)
+        copy.copy_(q)
+        del q
+        pq2.quantize_act(x[1], stream=st)
+        torch.cuda.synchronize()
+        assert torch.equal(copy, want)
