@@ -380,3 +380,20 @@ def test_binding_checks_on_the_gpu():
     with pytest.raises(pq2.PQ2Error):
         pq2.pq2_lora_add(d["x"], d["a"][:, :12].contiguous(), d["b"][:, :, :12].contiguous(),
                          d["adapter"], d["y"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [3, 1100])
+@pytest.mark.parametrize("N", [1, 2, 3, 5, 63, 254, 257, 511])
+def test_columns_at_the_end_of_the_last_adapter(N, M):
+    """Columns that are no multiple of four, B followed by NaN: nothing behind an
+    adapter's last column counts, and no column is lost."""
+    p = Problem(M, 256, N, 24, 3, seed=N, ids=[2, 0, 2] + [i % 3 for i in range(M - 3)],
+                ranks=[24, 7, 17])
+    want = p.run()
+    p.check(want)
+    d = p.device()
+    flat = torch.full((p.b.numel() + 4096,), float("nan"), dtype=BF16, device="cuda")
+    flat[:p.b.numel()] = d["b"].view(-1)
+    pq2.pq2_lora_add(**{**d, "b": flat[:p.b.numel()].view(p.b.shape)})
+    assert torch.equal(d["y"].cpu(), want)
