@@ -267,12 +267,15 @@ def pq2_norm_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None,
             _ptr(s, "s", torch.float32, (M, G), at), _ptr(t, "t", torch.int32, (M, G), at), M, K)
 
 
+_CURRENT = contextlib.nullcontext()
+
+
 def _on(stream, device):
     """Context in which torch allocates from the pool of the stream that a call is
     launched on: a block of another stream's pool may have work pending there
     that nothing orders before the call."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _CURRENT
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
                              torch.cuda.ExternalStream(int(stream), device=device))
 
@@ -290,8 +293,11 @@ def _workspace(workspace, M: int, N: int, K: int, device, stream,
         n = (query or gemm_workspace_bytes)(M, N, K)
         if n == 0:
             return 0, 0, None
-        with _on(stream, device):
+        if stream is None:
             workspace = torch.empty(n, dtype=torch.uint8, device=device)
+        else:
+            with _on(stream, device):
+                workspace = torch.empty(n, dtype=torch.uint8, device=device)
     if workspace is None:
         return 0, 0, None
     if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda:
