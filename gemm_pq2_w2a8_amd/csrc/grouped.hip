@@ -143,7 +143,7 @@ __global__ __launch_bounds__(64 * kStreamMaxWaves) void grouped_stream_kernel(Gr
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 o.w[b][h] = __builtin_amdgcn_raw_buffer_load_b128(
-                    rs_codes, (16 * b + r) * KB + 32 * c + 16 * h, 128 * run, 0);
+                    rs_codes, live ? (16 * b + r) * KB + 32 * c + 16 * h : kCopyOob, 128 * run, 0);
             o.ws[b] = __builtin_amdgcn_raw_buffer_load_b16(
                 rs_ws, live ? 2 * ((16 * b + r) * G + c) : kCopyOob, 8 * run, 0);
         }

@@ -419,3 +419,22 @@ def test_binding_checks_on_the_gpu():
         pq2.pq2_gemm_grouped(y=torch.empty(9, 8, device="cuda"), **{**d, "rows": None})
     empty = torch.empty(0, 8, device="cuda")
     pq2.pq2_gemm_grouped(y=empty, **{**d, "rows": None})
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("counts", [[1, 0, 2, 3], [1] * 40])
+@pytest.mark.parametrize("N", [1, 16, 31, 33])
+@pytest.mark.parametrize("G", [1, 2, 3, 5, 6, 7, 9, 41])
+def test_groups_at_the_end_of_the_last_expert(G, N, counts):
+    """Few slots an expert, groups that are no multiple of four: exact with unit
+    scales whatever stands behind the codes and scales of the last expert."""
+    p = Problem(counts, N, 128 * G, seed=G + N, unit=True)
+    d = p.device()
+    codes = torch.full((p.codes.size + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+    codes[:p.codes.size] = d["codes"].view(-1)
+    ws = torch.full((p.ws.size + 4096,), float("nan"), dtype=torch.float16, device="cuda")
+    ws[:p.ws.size] = d["wscale"].view(-1)
+    y = torch.full((p.T, N), 7.0, device="cuda")
+    pq2.pq2_gemm_grouped(**{**d, "codes": codes[:p.codes.size].view(p.codes.shape),
+                            "wscale": ws[:p.ws.size].view(p.ws.shape)}, y=y)
+    p.check(y.cpu().double().numpy(), exact=True)
