@@ -397,3 +397,32 @@ def test_columns_at_the_end_of_the_last_adapter(N, M):
     flat[:p.b.numel()] = d["b"].view(-1)
     pq2.pq2_lora_add(**{**d, "b": flat[:p.b.numel()].view(p.b.shape)})
     assert torch.equal(d["y"].cpu(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K,N", [((1 << 17) + 128, 64), (128, (1 << 17) + 3)])
+def test_the_last_of_adapters_past_4_gib(K, N):
+    """A, then B, of 4.7 GB whose last adapter alone has contents of its own and a
+    stride that does not divide 2^32: an offset cut to 32 bits, or another
+    adapter's, gives another result. Equal to a call on that adapter by itself."""
+    L, R = 70, 256
+    assert L * R * max(K, N) * 2 > 1 << 32 and (1 << 32) % (R * max(K, N) * 2) != 0
+    print(f"lora_add last of {L} adapters K={K} N={N}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(12)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=g).bfloat16()  # noqa: E731
+    a, b = (rnd(1, R, K) / K ** 0.5).repeat(L, 1, 1), (rnd(1, N, R) / 16).repeat(L, 1, 1)
+    a[L - 1], b[L - 1] = rnd(R, K) / K ** 0.5, rnd(N, R) / 16
+    x = rnd(2, K)
+    ids = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    y, alone, first = (torch.zeros(2, N, device="cuda") for _ in range(3))
+    pq2.pq2_lora_add(x, a, b, ids(L - 1, 5), y)
+    pq2.pq2_lora_add(x, a[L - 1:], b[L - 1:], ids(0, 0), alone)
+    pq2.pq2_lora_add(x, a[:1], b[:1], ids(0, 0), first)
+    assert torch.equal(y[0], alone[0]) and torch.equal(y[1], first[1])
+    assert not torch.equal(alone[0], first[0])
+    v = a[L - 1].double() @ x[0].double()
+    ref = b[L - 1].double() @ v
+    size = b[L - 1].double().abs() @ (a[L - 1].double().abs() @ x[0].double().abs())
+    # the file's bounds: E_v = 2 (52 + K / 128) u, 160 u for B v, y's own rounding
+    bound = (2 * (52 + K / 128) + 8 + 160 + 1) * U * size
+    assert ((y[0].double() - ref).abs() <= bound).all()
