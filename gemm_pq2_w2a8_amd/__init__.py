@@ -137,12 +137,20 @@ def abi_version() -> int:
     return int(lib.pq2_abi_version())
 
 
+def _handle(stream, index: int) -> int:
+    """Handle of a stream argument; ValueError for a stream of another GPU than
+    the tensors' (a raw handle does not tell)."""
+    if not isinstance(stream, torch.cuda.Stream):
+        return int(stream)
+    if stream.device_index != index:
+        raise ValueError(f"stream must be on cuda:{index}, got cuda:{stream.device_index}")
+    return stream.cuda_stream
+
+
 def _stream(t: torch.Tensor, stream) -> int:
     if stream is None:
         return torch.cuda.current_stream(t.device).cuda_stream
-    if isinstance(stream, torch.cuda.Stream):
-        return stream.cuda_stream
-    return int(stream)
+    return _handle(stream, t.get_device())
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape: Tuple[int, ...]) -> None:
@@ -185,7 +193,7 @@ def _launch(index: int, stream, call, *args) -> None:
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(index)
     else:
-        raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+        raw = _handle(stream, index)
     if torch._C._cuda_getDevice() == index:
         _check(call(*args, raw))
         return

@@ -74,6 +74,25 @@ def test_workspace_comes_from_the_launch_streams_pool(allocations):
     assert pq2._workspace(None, 2, 128, 8, "cuda:0", st) == (0, 0, None)
 
 
+def test_a_stream_of_another_gpu_is_refused(monkeypatch):
+    """Before anything is launched; the stream's handle goes on as it is."""
+    st, seen = Stream(), []
+    st.device_index, st.cuda_stream = 1, 77
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    call = lambda *a: seen.append(a) or 0               # noqa: E731
+    with pytest.raises(ValueError, match="stream must be on cuda:0, got cuda:1"):
+        pq2._launch(0, st, call, 5)
+    assert seen == []
+    pq2._launch(1, st, call, 5)
+    assert seen == [(5, 77)]
+    x = torch.zeros(1).as_subclass(Memory)
+    monkeypatch.setattr(Memory, "get_device", lambda self: 0, raising=False)
+    with pytest.raises(ValueError, match="stream must be on cuda:0, got cuda:1"):
+        pq2._stream(x, st)
+    assert pq2._stream(x, 99) == 99
+
+
 # ------------------------------------------------------------------ beside pending work (GPU)
 
 def block_with_pending_copy(nbytes, busy):
