@@ -91,16 +91,22 @@ __global__ __launch_bounds__(256) void grouped_small_kernel(GroupedArgs p) {
 // 128 bytes of a column are read together; the MFMA count per group is the same.
 // A wave takes 32 columns (two tiles, sharing A) and every waves-th run of four
 // groups; the block's waves meet in LDS and are added in wave order.
-// Codes and scales go to registers two runs ahead, a run's activations to the
-// wave's own LDS (buffer -> LDS copies; 16-byte pieces permuted so that the four
-// slots of a read fall in different banks). Rows that do not exist and groups
-// past the last have offsets outside the resources, which read zeros and move
-// no memory; the lanes outside A's blocks read one zero piece.
+// Codes and scales are requested two runs ahead into registers, a run's
+// activations into the wave's own LDS (buffer -> LDS copies; 16-byte pieces
+// permuted so that the four slots of a read fall in different banks). As
+// compiled they do not stay in flight that long: the requests are conditional,
+// so where their paths meet the first of two runs waits for all of them
+// (vmcnt(0) before t) and the second run's 16-bit scales are copied, and so
+// waited for, where they are requested: a pair of runs shows about one memory
+// latency. Rows that do not exist and groups past the last have lane offsets
+// outside the resources, which read zeros and move no memory; the lanes outside
+// A's blocks read one zero piece.
 // Planes 1 and 3 of a code word are masked in place (4 * code) into an
 // accumulator of their own: 4 D = 4 d0 + d1, the factor taken out of the weight
 // scale, 5 bit operations per word instead of 7.
-// Bound by HBM: 64 experts of 2048 x 5120 with a slot each 45 us, 3.9 TB/s; 8 of
-// them (a chain of dependent reads: offsets, row, codes) 10.2 us.
+// 64 experts of 2048 x 5120 with a slot each 45 us, 3.9 TB/s; 8 of them 9.9 us: a
+// chain of dependent reads (offsets, then the codes, then three reads of rows[]
+// one after the other behind them, then the activations).
 constexpr int kStreamCols = 32;
 constexpr int kStreamSlots = 4;
 constexpr int kStreamMaxWaves = 4;
@@ -236,8 +242,9 @@ __global__ __launch_bounds__(64 * kStreamMaxWaves) void grouped_stream_kernel(Gr
                                  __builtin_bit_cast(float, sv[i]) * wv, acc[b][i]);
         }
     };
-    // one run: its loads are done once only the next run's are in flight; its
-    // LDS is read before the run after that is copied over it
+    // one run: its loads are done once only the next run's are in flight (the
+    // least wait that is right; the compiler's own are longer); its LDS is read
+    // before the run after that is copied over it
     auto step = [&](int run, Run &o, int slot) __attribute__((always_inline)) {
         if (run + waves < runs)
             wait_vmem<kStreamLoads>();
@@ -298,8 +305,11 @@ hipError_t launch_stream(const GroupedArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Tiles by the mean slots of the experts that can have any (MI355X, us, 64
-// experts with shares falling off as rank^-0.4, 2048 x 5120 and 5120 x 1024):
+// Tiles by the mean slots of the experts that can have any: the host knows no
+// more than T and E, so slots that gather on a few experts get the kernel of the
+// mean (up to a mean of four the stream kernel, which reads an expert's codes
+// once for every four of its slots). MI355X, us, 64 experts with shares falling
+// off as rank^-0.4, 2048 x 5120 and 5120 x 1024:
 //   mean        2        6        8       16       32       64      128      256
 //   stream  50 / 31  73 / 45  86 / 55
 //   128x16  54 / 30  62 / 33  62 / 34  74 / 43 101 / 68 158/113  281/209  510/386

@@ -14,9 +14,11 @@
 //
 // Operands that are not both bfloat16 (or both binary16) are split exactly into
 // bfloat16 parts of 8 significant bits -- a binary16 value into two, a float32
-// into three -- and the parts' products added; products of parts below 2^-24 of
-// the whole are left out. v stays float32 this way, so the rank dimension costs
-// no accuracy.
+// into three -- and the parts' products added. Only float32 (x or v) against
+// binary16 weights has a pair that is left out: the third part times the second,
+// below 2^-22 of the product (parts are cut, not rounded, so it has the product's
+// sign). Otherwise v stays float32 this way and the rank dimension costs no
+// accuracy.
 #include "pq2_device.hpp"
 #include "pq2_launch.hpp"
 
@@ -87,7 +89,8 @@ __device__ __forceinline__ void parts_of(v4u raw, v4u (&part)[kParts<FMT>]) {
     }
 }
 
-// Sum of the parts' products (a's parts times b's), without those below 2^-24.
+// Sum of the parts' products (a's parts times b's), without the pair of a third
+// and a second part (below 2^-22 of the product).
 template <int NA, int NB>
 __device__ __forceinline__ v4f mfma_parts(const v4u (&a)[NA], const v4u (&b)[NB], v4f c) {
 #pragma unroll
@@ -162,7 +165,9 @@ __device__ __forceinline__ int rank_of(const LoraArgs &p, int id) {
 // Shrink: a block sums one K chunk of its rows x 64 ranks, adapter by adapter,
 // 16 * TR rows at a time; its eight waves share the chunk's steps and meet in
 // LDS, added in wave order. 4096 rows of 5120 bfloat16, rank 64: 28 us (42 MB of
-// x); 555 rows of 17408 with 11 adapters: 15 us.
+// x, 8.8 us of HBM time); 555 rows of 17408 with 11 adapters: 15 us. A wave's
+// steps load, wait and multiply in turn, with nothing in flight from one to the
+// next: the block's other waves are what covers a load.
 constexpr int kShrinkWaves = 8;
 
 // One wave's part of TR x T tiles: rows x (16 * TR), ranks w (16 * T), from k to
@@ -410,7 +415,8 @@ __device__ __forceinline__ Four<YF> add4(Four<YF> base, const float (&d)[4]) {
 // the rows 4 c + i, and 16 neighbouring lanes read and write 64 consecutive
 // columns of one row.
 // PIPE (R <= 64): B's vectors stay in registers over an adapter's stages, and a
-// stage's v and base are requested while the one before is computed.
+// stage's v and base are requested while the one before is computed (and waited
+// for at its end, where they change registers).
 // Memory-bound for many rows (4096 x 17408 bfloat16, rank 64: 74 us, 3.9 TB/s of
 // base, y and v), a chain of four dependent reads for a few.
 constexpr int kExpandRows = 16;
@@ -472,9 +478,9 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs p, const floa
                                 ? 4 * ((int)rows.local(i0 + entry, count) * R + kc + k) : kCopyOob;
             return __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rs_v, off, 0, 0));
         };
-        // A stage's first two chunks of v and its base, requested a stage ahead
-        // and in this order: waiting for v is then waiting for neither the base
-        // nor the stores of the stage before.
+        // A stage's first two chunks of v and its base, requested a stage ahead.
+        // The stage's products cover them and nothing more does: the copy of nxt
+        // to cur waits for v, then the base (not for the stores issued behind).
         struct Stage {
             v4f v[2];
             uint32_t at[4];
@@ -577,7 +583,10 @@ struct Deal {
 };
 
 // Up to 1024 rows, a batch with many adapters is taken for requests of a few
-// rows each, whose windows hold several adapters.
+// rows each, whose windows hold several adapters. The host knows how many are
+// loaded, not how many the rows use: a prompt of one adapter among many gets
+// their windows and turns, most of which end at once. The limits here and in
+// shrink_pairs rest on 1, 16, 555 and 4096 rows; nothing between was timed.
 Deal deal_rows(int64_t M, int64_t L, int64_t per, int64_t least, int64_t most) {
     Deal d{kWindow, 1, 0};
     const int64_t adapters = M > 1024 || L < 4 ? 1 : L < 8 ? L / 2 : 4;

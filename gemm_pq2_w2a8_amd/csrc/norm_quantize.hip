@@ -15,9 +15,14 @@
 // registers between the two norms and every array is read and written once.
 // Rows too long for that (K > 32768) are read again in each of three sweeps,
 // each element always by the thread that stores it.
-// HBM-bound for many rows (4096 x 5120 bfloat16 with both norms and a residual:
-// 45.5 us, 3.3 TB/s of 148 MB); a single row is the latency of one block, two
-// reductions deep (5120: 4.3 us).
+// 4096 x 5120 bfloat16 with both norms and a residual: 45 us, where its 148 MB
+// need 30 at a large copy's rate. Neither memory nor issue is full: 648 vector
+// instructions a wave keep the SIMDs 56 % busy, and the waves wait for 59 % of
+// their time, since a row's phases follow one another -- its loads, the first
+// reduction, w_post, the second reduction, w_pre (whose wait, behind the
+// conditional store of h, is for that store too), the quantiser -- and a block
+// requests nothing of a next row meanwhile. A single row is the latency of one
+// block, two reductions deep (5120: 4.4 us).
 #include "pq2_device.hpp"
 #include "pq2_launch.hpp"
 

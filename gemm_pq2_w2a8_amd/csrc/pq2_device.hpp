@@ -281,10 +281,15 @@ __device__ __forceinline__ void quantize_groups8(const float4 (&v)[4], uint32_t 
     sum = t;
 }
 
-// Buffer resource over [base, base + bytes) (bytes clamped to 32 bits; every
-// offset used is in range by construction, the hardware range check is a
-// second guard: loads beyond the range return zero). Word 3 selects 32-bit
-// raw data, as for all gfx9 buffers.
+// Buffer resource over [base, base + bytes) (bytes clamped to 32 bits). Lanes
+// without data have offsets outside the range, for which loads return zero and
+// touch no memory. On gfx950 the check takes the lane's and the uniform offset
+// together (measured: a lane in range by its own offset and outside with the
+// uniform one reads zeros, also where the uniform offset alone exceeds the
+// range), but offsets are kept in range without it, but for one load: the
+// panel kernel's last pair of an odd number of groups, whose second half reads
+// past the last row by the uniform offset and is not used. Word 3 selects
+// 32-bit raw data, as for all gfx9 buffers.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base, int64_t bytes) {
     const int n = bytes >= 0xffffffffLL ? (int)0xffffffffu : (int)bytes;
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, n, 0x00020000);

@@ -283,8 +283,8 @@ pq2_status pq2_gemm_bf16(const int8_t *q, const float *s, const int32_t *t,
  *              slot without activations: its y is zero;
  *   row_scale  float32 [T] (a router's weights), or NULL;
  *   y          [T][N], PQ2_ACT_F32 (4-byte aligned) or PQ2_ACT_BF16 bit patterns
- *              (2-byte; the float32 result rounded to nearest even), by
- *              y_format (else PQ2_ERR_ARG).
+ *              (2-byte; the float32 result rounded to nearest even, NaN kept),
+ *              by y_format (else PQ2_ERR_ARG); it overlaps no input.
  * T = 0 returns PQ2_OK and does nothing. PQ2_ERR_SHAPE: E outside 1 ..
  * PQ2_GROUPED_MAX_E, T above PQ2_GROUPED_MAX_T, N above PQ2_GROUPED_MAX_N, the
  * limits of pq2_gemm for R, T, N, K, or E*N above PQ2_MAX_DIM or E*N*K/4 above
@@ -316,7 +316,9 @@ pq2_status pq2_gemm_grouped(const int8_t *q, const float *s, const int32_t *t, i
  *            columns of B from ranks[l] on have no influence whatever they hold;
  *   scale    float32 [L], or NULL (1);
  *   base, y  [M][N] of y_format (PQ2_ACT_F32, 4-byte aligned, or PQ2_ACT_BF16
- *            bit patterns, 2-byte); base NULL or the same as y adds in place;
+ *            bit patterns, 2-byte); base NULL or the same as y adds in place.
+ *            base overlaps y as that same array or not at all, y and the
+ *            workspace overlap nothing else;
  *   x, a, b  are 16-byte aligned, x finite (a row that is not affects itself
  *            alone, and so does an adapter that is not);
  *   workspace, workspace_bytes  device memory for A x, 16-byte aligned: at
