@@ -23,6 +23,8 @@ LIB_PATH = os.path.join(_HERE, "libpq2.so")
 GROUP = 128
 PATH_AUTO, PATH_GEMV, PATH_SMALL, PATH_PREFILL, PATH_PANEL = 0, 1, 2, 3, 4
 ACT_F32, ACT_BF16, ACT_F16 = 0, 1, 2
+MX4_BLOCK = 32
+GATE_ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}   # PQ2_GATE_*
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python gemm_pq2_w2a8_amd/build.py`")
@@ -67,6 +69,25 @@ lib.pq2_lora_add.argtypes = [_P, ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, _P,
                              ctypes.c_int, _I64, _I64, _I64, _I64, _I64, _P, _SZ, _P]
 lib.pq2_lora_workspace_bytes.restype = _SZ
 lib.pq2_lora_workspace_bytes.argtypes = [_I64, _I64, _I64]
+_INT = ctypes.c_int
+for _name, _args in {
+        "pq2_mx4_quantize": [_P, _INT, _P, _P, _I64, _I64, _P],
+        "pq2_mx4_dequantize": [_P, _P, _P, _INT, _I64, _I64, _P],
+        "pq2_mx4_gemm": [_P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _P, _SZ, _P],
+        "pq2_mx4_gated": [_P, _P, _P, _P, _INT, _P, _P, _INT, _P, _P, _I64, _I64, _I64, _P, _SZ,
+                          _P],
+        "pq2_mx4_gemm_grad": [_P, _P, _P, _P, _INT, _I64, _I64, _I64, _P, _SZ, _P],
+        "pq2_mx4_gated_grad": [_P, _P, _INT, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _P, _SZ, _P],
+}.items():
+    getattr(lib, _name).restype = _INT
+    getattr(lib, _name).argtypes = _args
+for _name, _args in {
+        "pq2_mx4_workspace_bytes": [_I64, _I64, _I64, _INT],
+        "pq2_mx4_grad_workspace_bytes": [_I64, _I64, _I64, _INT],
+        "pq2_mx4_gated_grad_workspace_bytes": [_I64, _I64, _I64, _INT, _INT],
+}.items():
+    getattr(lib, _name).restype = _SZ
+    getattr(lib, _name).argtypes = _args
 lib.pq2_linear.restype = ctypes.c_int
 lib.pq2_linear.argtypes = [_P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]
 lib.pq2_linear_workspace_bytes.restype = _SZ
@@ -81,7 +102,10 @@ ABI_SYMBOLS = ("pq2_abi_version", "pq2_status_str", "pq2_quantize_act", "pq2_qua
                "pq2_norm_quantize", "pq2_gemm_grouped", "pq2_lora_add", "pq2_lora_workspace_bytes",
                "pq2_gemm_workspace_bytes", "pq2_gemm", "pq2_gemm_noalloc", "pq2_gemm_bf16",
                "pq2_gemm_kernel_path", "pq2_gemm_path", "pq2_linear", "pq2_linear_workspace_bytes",
-               "pq2_linear_kernel_path", "pq2_gemm_group_dots")
+               "pq2_linear_kernel_path", "pq2_gemm_group_dots", "pq2_mx4_quantize",
+               "pq2_mx4_dequantize", "pq2_mx4_gemm", "pq2_mx4_workspace_bytes", "pq2_mx4_gated",
+               "pq2_mx4_gemm_grad", "pq2_mx4_grad_workspace_bytes", "pq2_mx4_gated_grad",
+               "pq2_mx4_gated_grad_workspace_bytes")
 
 NOALLOC_SCRATCH_BYTES = 16 << 20    # PQ2_NOALLOC_SCRATCH_BYTES
 
@@ -102,6 +126,23 @@ def linear_workspace_bytes(M: int, N: int, K: int) -> int:
 def lora_workspace_bytes(M: int, K: int, R: int) -> int:
     """Workspace bytes of pq2_lora_add's fastest plan for this shape."""
     return int(lib.pq2_lora_workspace_bytes(M, K, R))
+
+
+def mx4_workspace_bytes(M: int, N: int, K: int, gated: bool = False) -> int:
+    """Workspace bytes of the fastest plan of pq2_mx4_gemm, or with `gated` of
+    pq2_mx4_gated with N = F (0: none needed)."""
+    return int(lib.pq2_mx4_workspace_bytes(M, N, K, int(gated)))
+
+
+def mx4_grad_workspace_bytes(M: int, N: int, K: int, dtype: torch.dtype) -> int:
+    """Workspace bytes of pq2_mx4_gemm_grad's fastest plan for gradients of dtype."""
+    return int(lib.pq2_mx4_grad_workspace_bytes(M, N, K, _ACT_FORMAT[dtype]))
+
+
+def mx4_gated_grad_workspace_bytes(M: int, F: int, K: int, dtype: torch.dtype,
+                                   keeps_dgu: bool = True) -> int:
+    """Workspace bytes of pq2_mx4_gated_grad's fastest plan, with or without a dgu."""
+    return int(lib.pq2_mx4_gated_grad_workspace_bytes(M, F, K, _ACT_FORMAT[dtype], int(keeps_dgu)))
 
 
 def linear_kernel_path(M: int, N: int, K: int, workspace_bytes: Optional[int] = None) -> int:
@@ -447,6 +488,136 @@ def pq2_lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter: tor
     _launch(at, stream, lib.pq2_lora_add, *args, wp, wn)
 
 
+def pq2_mx4_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                     stream=None) -> None:
+    """x [M][K] float32, bfloat16 or float16 -> MX4: codes uint8 [M][K/2] (two
+    4-bit floats a byte), scales uint8 [M][K/32] (powers of two)."""
+    fmt = _format(x, "x")
+    M, K = _mk(x)
+    at = _gpu(x, "x")
+    _launch(at, stream, lib.pq2_mx4_quantize, _ptr(x, "x", x.dtype, (M, K), at), fmt,
+            _ptr(codes, "codes", torch.uint8, (M, K // 2), at),
+            _ptr(scales, "scales", torch.uint8, (M, K // MX4_BLOCK), at), M, K)
+
+
+def pq2_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor,
+                       stream=None) -> None:
+    """x [M][K] (float32, bfloat16 or float16) = the values of MX4 codes and scales."""
+    fmt = _format(x, "x")
+    M, K = _mk(x)
+    at = _gpu(x, "x")
+    _launch(at, stream, lib.pq2_mx4_dequantize, _ptr(codes, "codes", torch.uint8, (M, K // 2), at),
+            _ptr(scales, "scales", torch.uint8, (M, K // MX4_BLOCK), at),
+            _ptr(x, "x", x.dtype, (M, K), at), fmt, M, K)
+
+
+def _mx4_args(codes: torch.Tensor, scales: torch.Tensor, name: str, at: int, K: int):
+    """Pointers and rows of an MX4 matrix of rows of K."""
+    rows = _mk(codes)[0]
+    return (_ptr(codes, name, torch.uint8, (rows, K // 2), at),
+            _ptr(scales, name + "scale", torch.uint8, (rows, K // MX4_BLOCK), at)), rows
+
+
+def _mx4_work(workspace, at: int, device, stream, query, *args):
+    """(pointer, bytes, keep-alive) of an MX4 workspace argument, as _workspace."""
+    wp, wn, keep = _workspace(workspace, 0, 0, 0, device, stream, lambda *_: int(query(*args)))
+    if keep is not None and keep.get_device() != at:
+        raise ValueError(f"workspace must be on cuda:{at}, got {keep.device}")
+    return wp, wn, keep
+
+
+def pq2_mx4_gemm(a: torch.Tensor, ascale: torch.Tensor, w: torch.Tensor, wscale: torch.Tensor,
+                 y: torch.Tensor, workspace="auto", stream=None) -> None:
+    """y [M][N] (float32, bfloat16 or float16) = a w^T of MX4 a [M] and w [N]
+    (codes uint8 [.][K/2], scales uint8 [.][K/32], K a multiple of 128).
+    workspace as for pq2_gemm, sized by mx4_workspace_bytes."""
+    fmt = _format(y, "y")
+    K = 2 * _mk(a)[1]
+    at = _gpu(a, "a")
+    pa, M = _mx4_args(a, ascale, "a", at, K)
+    pw, N = _mx4_args(w, wscale, "w", at, K)
+    py = _ptr(y, "y", y.dtype, (M, N), at)
+    wp, wn, _keep = _mx4_work(workspace, at, a.device, stream, lib.pq2_mx4_workspace_bytes, M, N, K, 0)
+    _launch(at, stream, lib.pq2_mx4_gemm, *pa, *pw, py, fmt, M, N, K, wp, wn)
+
+
+def _gate_act(act: str) -> int:
+    if act not in GATE_ACTS:
+        raise ValueError(f"act must be one of {', '.join(GATE_ACTS)}, got {act!r}")
+    return GATE_ACTS[act]
+
+
+def pq2_mx4_gated(a: torch.Tensor, ascale: torch.Tensor, w: torch.Tensor, wscale: torch.Tensor,
+                  h: Optional[torch.Tensor] = None, *, act: str = "silu",
+                  gu: Optional[torch.Tensor] = None, hcodes: Optional[torch.Tensor] = None,
+                  hscales: Optional[torch.Tensor] = None, workspace="auto", stream=None) -> None:
+    """The gated feed-forward block h = act(a Wg^T) * (a Wu^T) of MX4 a [M] and
+    w [2F] (Wg's rows, then Wu's), K a multiple of 128.
+
+    act "silu", "gelu" or "gelu_tanh". Outputs, any of them: h [M][F] and gu
+    [M][2F] (both products, for pq2_mx4_gated_grad) of one type (float32,
+    bfloat16 or float16); hcodes, hscales: h in MX4, quantised unrounded.
+    workspace as for pq2_gemm, sized by mx4_workspace_bytes(gated=True)."""
+    kind = _gate_act(act)
+    K = 2 * _mk(a)[1]
+    at = _gpu(a, "a")
+    pa, M = _mx4_args(a, ascale, "a", at, K)
+    pw, rows = _mx4_args(w, wscale, "w", at, K)
+    if rows % 2:
+        raise ValueError(f"w must have an even number of rows, got {rows}")
+    F = rows // 2
+    some = h if h is not None else gu
+    ty = torch.float32 if some is None else some.dtype
+    fmt = ACT_F32 if some is None else _format(some, "h" if h is not None else "gu")
+    out = (_ptr(h, "h", ty, (M, F), at), _ptr(gu, "gu", ty, (M, rows), at), fmt,
+           _ptr(hcodes, "hcodes", torch.uint8, (M, F // 2), at),
+           _ptr(hscales, "hscales", torch.uint8, (M, F // MX4_BLOCK), at))
+    wp, wn, _keep = _mx4_work(workspace, at, a.device, stream, lib.pq2_mx4_workspace_bytes, M, F, K, 1)
+    _launch(at, stream, lib.pq2_mx4_gated, *pa, *pw, kind, *out, M, F, K, wp, wn)
+
+
+def pq2_mx4_gemm_grad(dy: torch.Tensor, w: torch.Tensor, wscale: torch.Tensor, dx: torch.Tensor,
+                      workspace="auto", stream=None) -> None:
+    """dx [M][K] = dy w of dy [M][N] (float32, bfloat16 or float16, dx alike) and
+    MX4 w [N]: the gradient of pq2_mx4_gemm's input. workspace: "auto" (torch
+    allocates) or a device tensor of mx4_grad_workspace_bytes bytes; None where
+    the call needs none (bfloat16 with N a multiple of 8)."""
+    fmt = _format(dy, "dy")
+    M, N = _mk(dy)
+    K = 2 * _mk(w)[1]
+    at = _gpu(dy, "dy")
+    pw, _rows = _mx4_args(w, wscale, "w", at, K)
+    args = (_ptr(dy, "dy", dy.dtype, (M, N), at), *pw, _ptr(dx, "dx", dy.dtype, (M, K), at), fmt, M, N, K)
+    if _rows != N:
+        raise ValueError(f"w must have {N} rows, got {_rows}")
+    wp, wn, _keep = _mx4_work(workspace, at, dy.device, stream, lib.pq2_mx4_grad_workspace_bytes,
+                              M, N, K, fmt)
+    _launch(at, stream, lib.pq2_mx4_gemm_grad, *args, wp, wn)
+
+
+def pq2_mx4_gated_grad(dh: torch.Tensor, gu: torch.Tensor, w: torch.Tensor, wscale: torch.Tensor,
+                       dx: torch.Tensor, *, dgu: Optional[torch.Tensor] = None, act: str = "silu",
+                       workspace="auto", stream=None) -> None:
+    """Backward pass of pq2_mx4_gated: from dh [M][F] and the gu [M][2F] it
+    stored, dgu [M][2F] = (dh u act'(g) | dh act(g)) and dx [M][K] = dgu w; all of
+    dh's type. dgu may be gu itself, or None (not returned). workspace as for
+    pq2_mx4_gemm_grad, sized by mx4_gated_grad_workspace_bytes."""
+    kind = _gate_act(act)
+    fmt = _format(dh, "dh")
+    M, F = _mk(dh)
+    K = 2 * _mk(w)[1]
+    at = _gpu(dh, "dh")
+    ty = dh.dtype
+    pw, rows = _mx4_args(w, wscale, "w", at, K)
+    if rows != 2 * F:
+        raise ValueError(f"w must have {2 * F} rows, got {rows}")
+    args = (_ptr(dh, "dh", ty, (M, F), at), _ptr(gu, "gu", ty, (M, rows), at), kind, *pw,
+            _ptr(dgu, "dgu", ty, (M, rows), at), _ptr(dx, "dx", ty, (M, K), at), fmt, M, F, K)
+    wp, wn, _keep = _mx4_work(workspace, at, dh.device, stream, lib.pq2_mx4_gated_grad_workspace_bytes,
+                              M, F, K, fmt, int(dgu is not None))
+    _launch(at, stream, lib.pq2_mx4_gated_grad, *args, wp, wn)
+
+
 def pq2_linear(x: torch.Tensor, codes: torch.Tensor, wscale: torch.Tensor, y: torch.Tensor,
                workspace="auto", stream=None) -> None:
     """y float32 [M][N] from float32 x [M][K] with the quantisation inside the
@@ -522,6 +693,36 @@ def norm_quantize(x: torch.Tensor, *, residual: Optional[torch.Tensor] = None,
     pq2_norm_quantize(x, q, s, t, residual=residual, w_post=w_post, gate=gate, alpha=alpha,
                       w_pre=w_pre, eps=eps, h=h, stream=stream)
     return _returned(stream, h, q, s, t)
+
+
+def mx4_quantize(x: torch.Tensor, stream=None):
+    """Allocate MX4 codes and scales with torch (from the launch stream's pool)
+    and run pq2_mx4_quantize: (codes, scales)."""
+    _format(x, "x")
+    M, K = _mk(x)
+    with _on(stream, x.device):
+        codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((M, K // MX4_BLOCK), dtype=torch.uint8, device=x.device)
+    pq2_mx4_quantize(x, codes, scales, stream)
+    return _returned(stream, codes, scales)
+
+
+def mx4_linear(x: torch.Tensor, w: torch.Tensor, wscale: torch.Tensor,
+               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Whole path, y [M][N] of x's type (or out): pq2_mx4_quantize into
+    torch-allocated codes and scales, then pq2_mx4_gemm."""
+    _format(x, "x")
+    M, K = _mk(x)
+    with _on(stream, x.device):
+        y = out if out is not None else torch.empty((M, int(w.shape[0])), dtype=x.dtype,
+                                                    device=x.device)
+        codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((M, K // MX4_BLOCK), dtype=torch.uint8, device=x.device)
+    pq2_mx4_quantize(x, codes, scales, stream)
+    pq2_mx4_gemm(codes, scales, w, wscale, y, stream=stream)
+    if out is None:
+        _returned(stream, y)
+    return y
 
 
 def linear(x: torch.Tensor, codes: torch.Tensor, wscale: torch.Tensor,

@@ -7,6 +7,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include "mx4_launch.hpp"
 #include "pq2_launch.hpp"
 
 namespace {
@@ -18,6 +19,28 @@ pq2_status check_mnk(int64_t M, int64_t N, int64_t K) {
     if (M > PQ2_MAX_DIM || N > PQ2_MAX_DIM || K > PQ2_MAX_K) return PQ2_ERR_SHAPE;
     // no buffer beyond 2^40 elements (every grid then stays below 2^31 blocks)
     if (M * N > PQ2_MAX_ELEMS || M * K > PQ2_MAX_ELEMS || N * (K / 4) > PQ2_MAX_ELEMS)
+        return PQ2_ERR_SHAPE;
+    return PQ2_OK;
+}
+
+bool known_format(int f) { return f == PQ2_ACT_F32 || f == PQ2_ACT_BF16 || f == PQ2_ACT_F16; }
+
+// Rows of the MX4 quantiser, M >= 1 unless the caller has returned.
+pq2_status check_mx4_rows(int64_t M, int64_t K) {
+    if (M < 0 || M > PQ2_MAX_DIM || K < PQ2_MX4_BLOCK || K % PQ2_MX4_BLOCK != 0 || K > PQ2_MAX_K ||
+        M * K > PQ2_MAX_ELEMS)
+        return PQ2_ERR_SHAPE;
+    return PQ2_OK;
+}
+
+// MX4 products. The kernels address a tile's rows (at most 256) with 32-bit
+// offsets, and both halves of a gated block's scales with one resource.
+pq2_status check_mx4(int64_t M, int64_t N, int64_t K, bool gated) {
+    if (M < 0 || M > PQ2_MAX_DIM || N < 1 || N > (gated ? PQ2_MX4_MAX_N / 2 : PQ2_MX4_MAX_N) ||
+        K < PQ2_MX4_STEP || K % PQ2_MX4_STEP != 0 || K > PQ2_MX4_MAX_K)
+        return PQ2_ERR_SHAPE;
+    const int64_t rows = gated ? 2 * N : N;
+    if (M * rows > PQ2_MAX_ELEMS || M * K > PQ2_MAX_ELEMS || (gated && rows * K > PQ2_MX4_MAX_GATED))
         return PQ2_ERR_SHAPE;
     return PQ2_OK;
 }
@@ -154,11 +177,11 @@ const char *pq2_status_str(int status) {
     switch (status) {
         case PQ2_OK: return "PQ2_OK";
         case PQ2_ERR_NULL: return "PQ2_ERR_NULL: a required pointer is NULL";
-        case PQ2_ERR_SHAPE: return "PQ2_ERR_SHAPE: need M >= 1, N >= 1, K a positive multiple of 128, K <= 2^24";
+        case PQ2_ERR_SHAPE: return "PQ2_ERR_SHAPE: need M >= 1, N >= 1, K a positive multiple of 128, K <= 2^24 (pq2_mx4_*: the limits in the header)";
         case PQ2_ERR_ALIGN: return "PQ2_ERR_ALIGN: a base pointer is misaligned";
         case PQ2_ERR_HIP: return "PQ2_ERR_HIP: the HIP runtime rejected a launch";
-        case PQ2_ERR_ARG: return "PQ2_ERR_ARG: invalid path selector for this shape and workspace, no fused kernel of pq2_linear for this shape and workspace, unknown format, or eps or alpha out of range";
-        case PQ2_ERR_SCRATCH: return "PQ2_ERR_SCRATCH: the shape needs more split-K scratch than pq2_gemm_noalloc holds (PQ2_NOALLOC_SCRATCH_BYTES), or pq2_lora_add more workspace than it was given";
+        case PQ2_ERR_ARG: return "PQ2_ERR_ARG: invalid path selector for this shape and workspace, no fused kernel of pq2_linear for this shape and workspace, unknown format or activation, or eps or alpha out of range";
+        case PQ2_ERR_SCRATCH: return "PQ2_ERR_SCRATCH: the shape needs more split-K scratch than pq2_gemm_noalloc holds (PQ2_NOALLOC_SCRATCH_BYTES), or pq2_lora_add, pq2_mx4_gemm_grad or pq2_mx4_gated_grad more workspace than it was given";
         default: return "PQ2 unknown status";
     }
 }
@@ -371,6 +394,120 @@ pq2_status pq2_lora_add(const void *x, int x_format, const void *a, const void *
     return from_hip(pq2::launch_lora(args, x_format, w_format, y_format,
                                      static_cast<float *>(workspace), workspace_bytes,
                                      static_cast<hipStream_t>(hip_stream)));
+}
+
+pq2_status pq2_mx4_quantize(const void *x, int x_format, uint8_t *codes, uint8_t *scales,
+                            int64_t M, int64_t K, void *hip_stream) {
+    if (M == 0) return PQ2_OK;
+    if (!x || !codes || !scales) return PQ2_ERR_NULL;
+    const pq2_status st = check_mx4_rows(M, K);
+    if (st != PQ2_OK) return st;
+    if (!known_format(x_format)) return PQ2_ERR_ARG;
+    if (!aligned(x, 16) || !aligned(codes, 16)) return PQ2_ERR_ALIGN;
+    return from_hip(pq2::launch_mx4_quantize(x, x_format, codes, scales, M, K,
+                                             static_cast<hipStream_t>(hip_stream)));
+}
+
+pq2_status pq2_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, void *x, int x_format,
+                              int64_t M, int64_t K, void *hip_stream) {
+    if (M == 0) return PQ2_OK;
+    if (!x || !codes || !scales) return PQ2_ERR_NULL;
+    const pq2_status st = check_mx4_rows(M, K);
+    if (st != PQ2_OK) return st;
+    if (!known_format(x_format)) return PQ2_ERR_ARG;
+    if (!aligned(x, 16) || !aligned(codes, 16)) return PQ2_ERR_ALIGN;
+    return from_hip(pq2::launch_mx4_dequantize(codes, scales, x, x_format, M, K,
+                                               static_cast<hipStream_t>(hip_stream)));
+}
+
+size_t pq2_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K, int gated) {
+    if (M < 1 || check_mx4(M, N, K, gated != 0) != PQ2_OK) return 0;
+    return pq2::mx4_gemm_workspace_bytes(M, N, K, gated != 0);
+}
+
+pq2_status pq2_mx4_gemm(const uint8_t *a, const uint8_t *ascale, const uint8_t *w,
+                        const uint8_t *wscale, void *y, int y_format, int64_t M, int64_t N,
+                        int64_t K, void *workspace, size_t workspace_bytes, void *hip_stream) {
+    if (M == 0) return PQ2_OK;
+    if (!a || !ascale || !w || !wscale || !y) return PQ2_ERR_NULL;
+    const pq2_status st = check_mx4(M, N, K, false);
+    if (st != PQ2_OK) return st;
+    if (!known_format(y_format)) return PQ2_ERR_ARG;
+    if (!aligned(a, 16) || !aligned(w, 16) || !aligned(ascale, 4) || !aligned(wscale, 4) ||
+        !aligned(y, y_format == PQ2_ACT_F32 ? 4 : 2) || !aligned(workspace, 16))
+        return PQ2_ERR_ALIGN;
+    const pq2::Mx4Args args{a, ascale, w, wscale, y, y_format, 0, nullptr, nullptr, nullptr, M, N, K};
+    return from_hip(pq2::launch_mx4_gemm(args, false, workspace, workspace ? workspace_bytes : 0,
+                                         static_cast<hipStream_t>(hip_stream)));
+}
+
+pq2_status pq2_mx4_gated(const uint8_t *a, const uint8_t *ascale, const uint8_t *w,
+                         const uint8_t *wscale, int act, void *h, void *gu, int h_format,
+                         uint8_t *hcodes, uint8_t *hscales, int64_t M, int64_t F, int64_t K,
+                         void *workspace, size_t workspace_bytes, void *hip_stream) {
+    if (M == 0) return PQ2_OK;
+    if (!a || !ascale || !w || !wscale || (!h && !gu && !hcodes) || !hcodes != !hscales)
+        return PQ2_ERR_NULL;
+    const pq2_status st = check_mx4(M, F, K, true);
+    if (st != PQ2_OK) return st;
+    if (hcodes && F % PQ2_MX4_BLOCK != 0) return PQ2_ERR_SHAPE;
+    if (!known_format(h_format) || act < PQ2_GATE_SILU || act > PQ2_GATE_GELU_TANH)
+        return PQ2_ERR_ARG;
+    const uintptr_t ha = h_format == PQ2_ACT_F32 ? 4 : 2;
+    if (!aligned(a, 16) || !aligned(w, 16) || !aligned(ascale, 4) || !aligned(wscale, 4) ||
+        !aligned(h, ha) || !aligned(gu, ha) || !aligned(hcodes, 16) || !aligned(workspace, 16))
+        return PQ2_ERR_ALIGN;
+    const pq2::Mx4Args args{a, ascale, w, wscale, h, h_format, act, hcodes, hscales, gu, M, F, K};
+    return from_hip(pq2::launch_mx4_gemm(args, true, workspace, workspace ? workspace_bytes : 0,
+                                         static_cast<hipStream_t>(hip_stream)));
+}
+
+size_t pq2_mx4_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int format) {
+    if (M < 1 || check_mx4(M, N, K, false) != PQ2_OK || !known_format(format)) return 0;
+    return pq2::mx4_grad_workspace_bytes(M, N, K, format, false, false);
+}
+
+pq2_status pq2_mx4_gemm_grad(const void *dy, const uint8_t *w, const uint8_t *wscale, void *dx,
+                             int format, int64_t M, int64_t N, int64_t K, void *workspace,
+                             size_t workspace_bytes, void *hip_stream) {
+    if (M == 0) return PQ2_OK;
+    if (!dy || !w || !wscale || !dx) return PQ2_ERR_NULL;
+    const pq2_status st = check_mx4(M, N, K, false);
+    if (st != PQ2_OK) return st;
+    if (!known_format(format)) return PQ2_ERR_ARG;
+    if (!aligned(dy, 16) || !aligned(w, 16) || !aligned(wscale, 4) ||
+        !aligned(dx, format == PQ2_ACT_F32 ? 4 : 2) || !aligned(workspace, 16))
+        return PQ2_ERR_ALIGN;
+    const size_t bytes = workspace ? workspace_bytes : 0;
+    if (bytes < pq2::mx4_grad_least_bytes(M, N, format, false, false)) return PQ2_ERR_SCRATCH;
+    const pq2::Mx4GradArgs args{dy, w, wscale, dx, format, nullptr, nullptr, 0, M, N, K};
+    return from_hip(pq2::launch_mx4_grad(args, workspace, bytes, static_cast<hipStream_t>(hip_stream)));
+}
+
+size_t pq2_mx4_gated_grad_workspace_bytes(int64_t M, int64_t F, int64_t K, int format,
+                                          int keeps_dgu) {
+    if (M < 1 || check_mx4(M, F, K, true) != PQ2_OK || !known_format(format)) return 0;
+    return pq2::mx4_grad_workspace_bytes(M, 2 * F, K, format, true, keeps_dgu != 0);
+}
+
+pq2_status pq2_mx4_gated_grad(const void *dh, const void *gu, int act, const uint8_t *w,
+                              const uint8_t *wscale, void *dgu, void *dx, int format, int64_t M,
+                              int64_t F, int64_t K, void *workspace, size_t workspace_bytes,
+                              void *hip_stream) {
+    if (M == 0) return PQ2_OK;
+    if (!dh || !gu || !w || !wscale || !dx) return PQ2_ERR_NULL;
+    const pq2_status st = check_mx4(M, F, K, true);
+    if (st != PQ2_OK) return st;
+    if (!known_format(format) || act < PQ2_GATE_SILU || act > PQ2_GATE_GELU_TANH)
+        return PQ2_ERR_ARG;
+    if (!aligned(dh, 16) || !aligned(gu, 16) || !aligned(dgu, 16) || !aligned(w, 16) ||
+        !aligned(wscale, 4) || !aligned(dx, format == PQ2_ACT_F32 ? 4 : 2) || !aligned(workspace, 16))
+        return PQ2_ERR_ALIGN;
+    const size_t bytes = workspace ? workspace_bytes : 0;
+    if (bytes < pq2::mx4_grad_least_bytes(M, 2 * F, format, true, dgu != nullptr))
+        return PQ2_ERR_SCRATCH;
+    const pq2::Mx4GradArgs args{dh, w, wscale, dx, format, gu, dgu, act, M, 2 * F, K};
+    return from_hip(pq2::launch_mx4_grad(args, workspace, bytes, static_cast<hipStream_t>(hip_stream)));
 }
 
 pq2_status pq2_gemm_group_dots(const int8_t *q, const int32_t *t, const uint8_t *codes,

@@ -49,11 +49,14 @@
  *  PQ2_ERR_ARG   an invalid path selector (pq2_gemm_group_dots), a shape
  *                and workspace no fused kernel of pq2_linear runs, an unknown
  *                format (pq2_quantize_act_16, pq2_norm_quantize,
- *                pq2_gemm_grouped, pq2_lora_add), or an eps or alpha that
+ *                pq2_gemm_grouped, pq2_lora_add, pq2_mx4_*) or activation
+ *                (pq2_mx4_gated, pq2_mx4_gated_grad), or an eps or alpha that
  *                pq2_norm_quantize does not take;
  *  PQ2_ERR_SCRATCH (pq2_gemm_noalloc) the small-batch plan's split-K partial
  *                sums need more than PQ2_NOALLOC_SCRATCH_BYTES; (pq2_lora_add)
  *                the workspace holds fewer than M * R floats;
+ *                (pq2_mx4_gemm_grad, pq2_mx4_gated_grad) it holds less than the
+ *                gradient's parts take;
  *  PQ2_ERR_HIP   a kernel launch was rejected by the HIP runtime.
  * Nothing is enqueued when a status other than PQ2_OK is returned, except for
  * PQ2_ERR_HIP. A fault during execution surfaces at the caller's next
@@ -345,6 +348,128 @@ pq2_status pq2_lora_add(const void *x, int x_format, const void *a, const void *
  * one). Pure host query.
  */
 size_t pq2_lora_workspace_bytes(int64_t M, int64_t K, int64_t R);
+
+/*
+ * Microscaled 4-bit floating point (MX4), a second format for matrices that
+ * ternary codes do not hold, with the same split: a quantiser, a product, and
+ * what a feed-forward block puts between two products; and the gradients that
+ * adapters and layers below frozen MX4 weights are trained with.
+ *
+ * A block of 32 consecutive values of a row has one scale byte b and 32 codes:
+ *  codes   uint8 [M][K/2]; value k of a row is bits 4(k%2) .. 4(k%2)+3 of byte
+ *          k/2. Bit 3 is the sign, codes 0 .. 7 are 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *          Base 16-byte aligned.
+ *  scales  uint8 [M][K/32]; byte b stands for 2^(b - 127), 255 for not a number
+ *          (then so is every value of the block).
+ *
+ * pq2_mx4_quantize: b = max(floor(log2 max|x|) - 2 + 127, 0) over a block, 0 for
+ * a block of zeros; codes are x / 2^(b - 127) rounded to the nearest value, ties
+ * to the even code, beyond 6 to 6, the sign kept. A block that holds an infinity
+ * or NaN gets b = 255 and codes 0. pq2_mx4_dequantize is the inverse; values
+ * are exact in float32 and bfloat16 up to their range (scales the quantiser
+ * writes stay within it), rounded to nearest even in float16.
+ *   x        [M][K] of x_format (PQ2_ACT_F32, PQ2_ACT_BF16, PQ2_ACT_F16; else
+ *            PQ2_ERR_ARG), 16-byte aligned;
+ *   scales   any alignment. PQ2_ERR_SHAPE: K not a multiple of 32 in 32 ..
+ *            PQ2_MAX_K, M above PQ2_MAX_DIM, M*K above PQ2_MAX_ELEMS.
+ * Every MX4 entry returns PQ2_OK for M = 0 and does nothing.
+ */
+#define PQ2_MX4_BLOCK 32
+pq2_status pq2_mx4_quantize(const void *x, int x_format, uint8_t *codes, uint8_t *scales,
+                            int64_t M, int64_t K, void *hip_stream);
+pq2_status pq2_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, void *x, int x_format,
+                              int64_t M, int64_t K, void *hip_stream);
+
+/*
+ * y[m][n] = sum_k a[m][k] w[n][k] of two MX4 matrices: products and scales are
+ * exact, sums float32 (in a fixed order: repeated calls give identical y), y is
+ * rounded once.
+ *   a, ascale  [M][K/2], [M][K/32]; w, wscale [N][K/2], [N][K/32]: codes 16-byte,
+ *              scales 4-byte aligned;
+ *   y          [M][N] of y_format (PQ2_ACT_F32, 4-byte aligned, PQ2_ACT_BF16 or
+ *              PQ2_ACT_F16, 2-byte; else PQ2_ERR_ARG);
+ *   workspace  pq2_mx4_workspace_bytes(M, N, K, 0) bytes, 16-byte aligned, of
+ *              which the fastest plan keeps partial sums; NULL or less takes a
+ *              plan that needs no more. As for pq2_gemm, calls that may overlap
+ *              need workspaces of their own.
+ * PQ2_ERR_SHAPE: N outside 1 .. PQ2_MX4_MAX_N, K not a multiple of
+ * PQ2_MX4_STEP in PQ2_MX4_STEP .. PQ2_MX4_MAX_K, M above PQ2_MAX_DIM, M*N or M*K
+ * above PQ2_MAX_ELEMS.
+ */
+#define PQ2_MX4_STEP 128
+#define PQ2_MX4_MAX_N (1LL << 21)
+#define PQ2_MX4_MAX_K (1LL << 21)
+size_t pq2_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K, int gated);
+pq2_status pq2_mx4_gemm(const uint8_t *a, const uint8_t *ascale, const uint8_t *w,
+                        const uint8_t *wscale, void *y, int y_format, int64_t M, int64_t N,
+                        int64_t K, void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/*
+ * The gated feed-forward block: both projections, the activation and the product
+ * in one call,
+ *   g = a Wg^T,   u = a Wu^T,   h = act(g) * u,
+ * with w, wscale holding Wg's F rows and then Wu's ([2F][K/2], [2F][K/32]; the
+ * stacked layout of a gate_up projection). g, u and h are float32 until they
+ * are stored; any of the outputs may be NULL, but not all:
+ *   act      PQ2_GATE_SILU g / (1 + e^-g); PQ2_GATE_GELU g Phi(g), Phi the
+ *            normal distribution function; PQ2_GATE_GELU_TANH its tanh form,
+ *            g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 (else PQ2_ERR_ARG);
+ *   h, gu    [M][F], and [M][2F] (g's columns, then u's: what the backward pass
+ *            reads), both of h_format;
+ *   hcodes, hscales  h quantised as by pq2_mx4_quantize from its float32 values
+ *            ([M][F/2], 16-byte aligned, [M][F/32]; F a multiple of 32), the next
+ *            product's input; both or none;
+ *   workspace  pq2_mx4_workspace_bytes(M, F, K, 1) bytes, as for pq2_mx4_gemm.
+ * PQ2_ERR_SHAPE: the limits of pq2_mx4_gemm for 2F, and 2*F*K above
+ * PQ2_MX4_MAX_GATED.
+ */
+#define PQ2_GATE_SILU 0
+#define PQ2_GATE_GELU 1
+#define PQ2_GATE_GELU_TANH 2
+#define PQ2_MX4_MAX_GATED (1LL << 35)
+pq2_status pq2_mx4_gated(const uint8_t *a, const uint8_t *ascale, const uint8_t *w,
+                         const uint8_t *wscale, int act, void *h, void *gu, int h_format,
+                         uint8_t *hcodes, uint8_t *hscales, int64_t M, int64_t F, int64_t K,
+                         void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/*
+ * The gradient of pq2_mx4_gemm's input, dx[m][k] = sum_n dy[m][n] w[n][k], with
+ * respect to the values that a's codes stand for (a quantiser in front passes
+ * it on unchanged). The weights are frozen: they have no gradient. dy enters the
+ * products unrounded, sums are float32 in a fixed order, dx is rounded once.
+ *   dy, dx   [M][N], 16-byte aligned, and [M][K], both of `format`;
+ *   workspace  16-byte aligned; pq2_mx4_grad_workspace_bytes(M, N, K, format)
+ *            bytes run the fastest plan. Without partial sums the least is none
+ *            for PQ2_ACT_BF16 with N a multiple of 8; else dy's bfloat16 parts
+ *            (PQ2_ACT_BF16 one, PQ2_ACT_F16 two, PQ2_ACT_F32 three) of
+ *            M * (N rounded up to 64) elements each, rounded up to 256 bytes
+ *            (less: PQ2_ERR_SCRATCH).
+ * PQ2_ERR_SHAPE as for pq2_mx4_gemm.
+ */
+size_t pq2_mx4_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int format);
+pq2_status pq2_mx4_gemm_grad(const void *dy, const uint8_t *w, const uint8_t *wscale, void *dx,
+                             int format, int64_t M, int64_t N, int64_t K, void *workspace,
+                             size_t workspace_bytes, void *hip_stream);
+
+/*
+ * The gated block's backward pass, from the g and u that pq2_mx4_gated stored:
+ *   dg = dh * u * act'(g),   du = dh * act(g),   dx = dg Wg + du Wu.
+ * dg and du are rounded to `format`, where a projection's adapter reads them,
+ * and multiply the weights as rounded.
+ *   dh, gu, dgu  [M][F], [M][2F], [M][2F], 16-byte aligned; dx [M][K]; all of
+ *            `format`. dgu may be gu itself, or NULL (then the workspace holds
+ *            it where the products read it in place);
+ *   workspace  pq2_mx4_gated_grad_workspace_bytes(M, F, K, format, dgu != NULL)
+ *            bytes run the fastest plan; the least is that of pq2_mx4_gemm_grad
+ *            with N = 2F, and without dgu at least one part.
+ * PQ2_ERR_SHAPE as for pq2_mx4_gated; PQ2_ERR_ARG: an unknown act or format.
+ */
+size_t pq2_mx4_gated_grad_workspace_bytes(int64_t M, int64_t F, int64_t K, int format,
+                                          int keeps_dgu);
+pq2_status pq2_mx4_gated_grad(const void *dh, const void *gu, int act, const uint8_t *w,
+                              const uint8_t *wscale, void *dgu, void *dx, int format, int64_t M,
+                              int64_t F, int64_t K, void *workspace, size_t workspace_bytes,
+                              void *hip_stream);
 
 /*
  * Quantise and multiply without the separate quantiser launch, for decode
