@@ -74,12 +74,14 @@ __device__ __forceinline__ uint32_t mx_encode2(uint32_t word, float a, float b, 
 }
 
 // a b^T over 128 values: lane l holds 32 consecutive values of row l % 16,
-// block l / 16, and their scale in its word's low byte; result i is that of a's
-// row 4 (l / 16) + i and b's row l % 16.
+// block l / 16, and their scale in byte BYTE of its word; result i is that of
+// a's row 4 (l / 16) + i and b's row l % 16.
+template <int BYTE = 0>
 __device__ __forceinline__ v4f32 mfma_mx4(v4i a, v4i b, v4f32 c, uint32_t sa, uint32_t sb) {
     const v8i wa = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
     const v8i wb = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, wb, c, 4, 4, 0, (int)sa, 0, (int)sb);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, wb, c, 4, 4, BYTE, (int)sa, BYTE,
+                                                           (int)sb);
 }
 
 // Activations of the gated block (PQ2_GATE_*).

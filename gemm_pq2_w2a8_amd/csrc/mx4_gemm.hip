@@ -19,32 +19,6 @@
 namespace pq2 {
 namespace {
 
-// ---------------------------------------------------------------- tiles
-//
-// A block owns BN weight rows x BM tokens, NWN x NWM waves of WN x WM
-// instruction tiles of 16 x 16. Weights are the instruction's first operand, so
-// a lane's four results are consecutive columns of y. K advances in stages of
-// 256 (two instructions), copied into a ring of two LDS slots by 16-byte buffer
-// -> LDS copies, a whole 128-byte line of a row per eight lanes; the copies of
-// stage s + 1 fly while stage s is multiplied. Inside a row the 16-byte unit c
-// lies at place c ^ swizzle(row), so the reads of 16 rows' unit c are free of
-// bank conflicts. Scales travel four instructions (16 bytes a row) at a time in
-// two slots of their own.
-// Rows past the end lie outside the buffer resources: they read zeros.
-template <int WN_, int WM_, int NWN_, int NWM_>
-struct MxTile {
-    static constexpr int WN = WN_, WM = WM_, NWN = NWN_, NWM = NWM_;
-    static constexpr int W = NWN * NWM, T = kWave * W;
-    static constexpr int BN = 16 * WN * NWN, BM = 16 * WM * NWM;
-    static constexpr int kStageBytes = (BN + BM) * 128;
-    static constexpr int kScaleBytes = (BN + BM) * 16;
-    static constexpr int kLdsBytes = 2 * kStageBytes + 2 * kScaleBytes;
-    static constexpr int kCopiesN = BN / 8 / W, kCopiesM = BM / 8 / W;   // per wave and stage
-    static_assert(BN % (8 * W) == 0 && BM % (8 * W) == 0 && BN % 64 == 0 && BM % 64 == 0, "copies");
-};
-
-__device__ __forceinline__ int mx_swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
-
 // Results of a block of 32 gated columns and one token: h[p][i] is column 16 p
 // + 4 (lane / 16) + i. Quantised into the token's codes and scale byte.
 __device__ __forceinline__ void store_quantised(const v4f32 (&h)[2], uint8_t *codes, uint8_t *scale,
@@ -93,6 +67,98 @@ __device__ __forceinline__ void store4(void *y, int fmt, int64_t at, v4f32 v, in
 __device__ __forceinline__ bool aligned4(const void *y, int fmt, int64_t n) {
     return (n & 3) == 0 && (reinterpret_cast<uintptr_t>(y) & (fmt == kF32 ? 15 : 7)) == 0;
 }
+
+// The end of a product: acc[i][j] are four consecutive rows of w (from 4 (lane /
+// 16) on) of instruction tile i against token m + 16 j. Plain: tile i's columns
+// of y start at n + 16 i. Gated: tiles alternate between gate and up, tiles 2 p
+// and 2 p + 1 make the columns from n + 16 p on, and NI is a multiple of four,
+// so that blocks of 32 columns are whole.
+template <int NI, int WM, bool GATED>
+__device__ __forceinline__ void finish(const Mx4Args &a, const v4f32 (&acc)[NI][WM], int64_t n,
+                                       int64_t m, int lane) {
+    const int lg = lane >> 4;
+    const bool wide = aligned4(a.y, a.y_format, a.N);
+    if constexpr (!GATED) {
+#pragma unroll
+        for (int j = 0; j < WM; ++j) {
+            const int64_t t = m + 16 * j;
+            if (t >= a.M) continue;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int64_t c = n + 16 * i + 4 * lg;
+                const int left = (int)(a.N - c < 4 ? a.N - c : 4);
+                if (left > 0) store4(a.y, a.y_format, t * a.N + c, acc[i][j], left, wide && left == 4);
+            }
+        }
+    } else {
+        static_assert(NI % 4 == 0, "whole blocks of 32 columns");
+        const bool wide_gu = aligned4(a.gu, a.y_format, a.N);
+        auto run = [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < WM; ++j) {
+                const int64_t t = m + 16 * j;
+                const bool live = t < a.M;
+#pragma unroll
+                for (int b = 0; b < NI / 4; ++b) {
+                    v4f32 h[2];
+                    const int64_t nb = n + 32 * b;                 // the block of 32 columns
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const v4f32 g = acc[4 * b + 2 * p][j], u = acc[4 * b + 2 * p + 1][j];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) h[p][i] = gate_act<act.value>(g[i]) * u[i];
+                        const int64_t c = nb + 16 * p + 4 * lg;
+                        const int left = (int)(a.N - c < 4 ? a.N - c : 4);
+                        if (live && left > 0) {
+                            if (a.y) store4(a.y, a.y_format, t * a.N + c, h[p], left, wide && left == 4);
+                            if (a.gu) {
+                                const bool whole = wide_gu && left == 4;
+                                store4(a.gu, a.y_format, 2 * t * a.N + c, g, left, whole);
+                                store4(a.gu, a.y_format, (2 * t + 1) * a.N + c, u, left, whole);
+                            }
+                        }
+                    }
+                    if (a.hq)
+                        store_quantised(h, a.hq + (t * a.N + nb) / 2, a.hs + (t * a.N + nb) / 32,
+                                        live && nb < a.N, lane);
+                    __builtin_amdgcn_sched_barrier(0);   // one block's registers at a time
+                }
+            }
+        };
+        if (a.act == kSilu)
+            run(std::integral_constant<int, kSilu>());
+        else if (a.act == kGelu)
+            run(std::integral_constant<int, kGelu>());
+        else
+            run(std::integral_constant<int, kGeluTanh>());
+    }
+}
+
+// ---------------------------------------------------------------- tiles
+//
+// A block owns BN weight rows x BM tokens, NWN x NWM waves of WN x WM
+// instruction tiles of 16 x 16. Weights are the instruction's first operand, so
+// a lane's four results are consecutive columns of y. K advances in stages of
+// 256 (two instructions), copied into a ring of two LDS slots by 16-byte buffer
+// -> LDS copies, a whole 128-byte line of a row per eight lanes; the copies of
+// stage s + 1 fly while stage s is multiplied. Inside a row the 16-byte unit c
+// lies at place c ^ swizzle(row), so the reads of 16 rows' unit c are free of
+// bank conflicts. Scales travel four instructions (16 bytes a row) at a time in
+// two slots of their own.
+// Rows past the end lie outside the buffer resources: they read zeros.
+template <int WN_, int WM_, int NWN_, int NWM_>
+struct MxTile {
+    static constexpr int WN = WN_, WM = WM_, NWN = NWN_, NWM = NWM_;
+    static constexpr int W = NWN * NWM, T = kWave * W;
+    static constexpr int BN = 16 * WN * NWN, BM = 16 * WM * NWM;
+    static constexpr int kStageBytes = (BN + BM) * 128;
+    static constexpr int kScaleBytes = (BN + BM) * 16;
+    static constexpr int kLdsBytes = 2 * kStageBytes + 2 * kScaleBytes;
+    static constexpr int kCopiesN = BN / 8 / W, kCopiesM = BM / 8 / W;   // per wave and stage
+    static_assert(BN % (8 * W) == 0 && BM % (8 * W) == 0 && BN % 64 == 0 && BM % 64 == 0, "copies");
+};
+
+__device__ __forceinline__ int mx_swizzle(int row) { return row & 6; }
 
 // SPAN: rows of scales are copied 16 bytes at a time (K a multiple of 512 and
 // 16-byte bases); else 4 bytes at a time.
@@ -234,62 +300,278 @@ __global__ __launch_bounds__(L::T) void mx4_tile_kernel(Mx4Args a, int tiles_n, 
         }
     }
 
-    const int64_t mt = m0 + 16 * WM * wm + r;
-    if constexpr (!GATED) {
-        const bool wide = aligned4(a.y, a.y_format, a.N);
+    finish<WN, WM, GATED>(a, acc, n0 + (GATED ? 8 : 16) * WN * wn, m0 + 16 * WM * wm + r, lane);
+}
+
+// ---------------------------------------------------------------- wide tiles
+//
+// 256 weight rows x 256 tokens, eight waves (two a SIMD) of 128 x 64. Stages of
+// 256 along K in two slots of 64 KB, scales of four steps (512) in one of 8 KB.
+// A step is one instruction's 128. What a step multiplies was read from LDS
+// during the step before: tokens into the other of two register sets, weights
+// and their scales rolling, each tile's registers taking the next step's as soon
+// as its four products are issued. After a stage's last read a barrier frees its
+// slot; the copies of the next stage but one are dealt over the products that
+// follow.
+// Each copy has a resource of its own, the eight rows that it fills as far as
+// they exist, so that one lane offset serves all of them.
+// TODO figures
+struct MxWide {
+    static constexpr int W = 8, T = 512, BN = 256, BM = 256, WN = 8, WM = 4, NWN = 2;
+    static constexpr int kStageBytes = (BN + BM) * 128;
+    static constexpr int kScaleBytes = (BN + BM) * 16;
+    static constexpr int kLdsBytes = 2 * kStageBytes + kScaleBytes;
+    static constexpr int kPart = BN * BM;                // floats of a split tile's partial sums
+};
+
+// Tiles of a launch: the first `full` are computed whole, the K range of each of
+// the others is dealt to `ways` blocks, whose sums lie in part [tiles - full][ways]
+// [MxWide::kPart] in the lanes' own order.
+struct MxPlan {
+    int tiles_n, tiles_m, full, ways;
+    float *part;
+};
+
+// Tile t: runs of four tiles down, so that what an XCD's contiguous run of tiles
+// reads at a time is about as high as wide.
+__device__ __forceinline__ void wide_tile(const MxPlan &p, int t, int &tn, int &tm) {
+    constexpr int kDown = 4;
+    const int group = t / (kDown * p.tiles_n), in = t % (kDown * p.tiles_n);
+    const int left = p.tiles_m - group * kDown;
+    const int high = left < kDown ? left : kDown;
+    tm = group * kDown + in % high;
+    tn = in / high;
+}
+
+template <bool GATED, bool SPAN>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void mx4_wide_kernel(Mx4Args a, MxPlan plan) {
+    typedef MxWide L;
+    constexpr int WN = L::WN, WM = L::WM, W = L::W;
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    uint8_t *const sc = smem + 2 * L::kStageBytes;
+    const int tid = threadIdx.x;
+    const int lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave % L::NWN, wm = wave / L::NWN;
+    const int r = lane & 15, lg = lane >> 4;
+
+    // whole tiles first; each XCD takes a contiguous run of either kind
+    const int whole = (plan.full + 7) / 8 * 8;
+    const bool split = (int)blockIdx.x >= whole;
+    const int b = split ? blockIdx.x - whole : blockIdx.x;
+    const int count = split ? (plan.tiles_n * plan.tiles_m - plan.full) * plan.ways : plan.full;
+    const int item = (b & 7) * ((count + 7) / 8) + (b >> 3);
+    if (item >= count) return;
+    const int tile = split ? plan.full + item / plan.ways : item;
+    int tn, tm;
+    wide_tile(plan, tile, tn, tm);
+    // (divisions leave uniform results in vector registers)
+    const int64_t m0 = (int64_t)__builtin_amdgcn_readfirstlane(tm) * L::BM;
+    const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane(tn) * (GATED ? L::BN / 2 : L::BN);
+
+    const int kb = (int)(a.K / 2), sb = (int)(a.K / kMxBlock);   // bytes of a row
+    const int all = (int)((a.K / 128 + 3) / 4);                  // runs of four steps
+    const int way = split ? item % plan.ways : 0, ways = split ? plan.ways : 1;
+    const int q0 = __builtin_amdgcn_readfirstlane((int)((uint32_t)all * way / ways));
+    const int q1 = __builtin_amdgcn_readfirstlane((int)((uint32_t)all * (way + 1) / ways));
+    const int steps = q1 == all ? (int)(a.K / 128) : 4 * q1;     // the end of this block's steps
+    const int rows_n = (int)(a.N - n0 < L::BN ? a.N - n0 : L::BN);
+    const int rows_m = (int)(a.M - m0 < L::BM ? a.M - m0 : L::BM);
+
+    // copy k < 4 of a wave: weight rows 64 k + 8 wave .. of the tile, else tokens'.
+    // In the gated block runs of 16 tile rows alternate between gate and up.
+    const bool up = GATED && ((wave >> 1) & 1);
+    const int first_n = GATED ? 16 * (wave >> 2) + 8 * (wave & 1) : 8 * wave, first_m = 8 * wave;
+    const uint8_t *const base_n = a.w + (n0 + (up ? a.N : 0) + first_n) * kb;
+    const uint8_t *const base_m = a.a + (m0 + first_m) * kb;
+    auto bytes = [&](int rows) __attribute__((always_inline)) {
+        return __builtin_amdgcn_readfirstlane((rows < 0 ? 0 : rows > 8 ? 8 : rows) * kb);
+    };
+    constexpr int kNext = GATED ? 32 : 64;           // weight rows between two copies
+    const int bytes_n[4] = {bytes(rows_n - first_n), bytes(rows_n - first_n - kNext),
+                            bytes(rows_n - first_n - 2 * kNext), bytes(rows_n - first_n - 3 * kNext)};
+    const int bytes_m[4] = {bytes(rows_m - first_m), bytes(rows_m - first_m - 64),
+                            bytes(rows_m - first_m - 128), bytes(rows_m - first_m - 192)};
+    const int sub = lane >> 3, unit = (lane & 7) ^ mx_swizzle(sub);
+    const int off = sub * kb + 16 * unit;
+    int stage_off = kCopyOob;                        // of the stage being copied
+    auto open_stage = [&](int s) __attribute__((always_inline)) {
+        stage_off = 2 * s + (unit >> 2) < steps ? off : kCopyOob;
+    };
+    auto copy = [&](int s, int k) __attribute__((always_inline)) {
+        const __amdgpu_buffer_rsrc_t rs = k < 4 ? make_rsrc(base_n + (int64_t)k * kNext * kb, bytes_n[k & 3])
+                                                : make_rsrc(base_m + (int64_t)(k & 3) * 64 * kb, bytes_m[k & 3]);
+        copy16_to_lds_at(rs, smem + (s & 1) * L::kStageBytes + (k * W + wave) * 1024, stage_off, 128 * s);
+    };
+    // scale rows of the tile: the weights' 256, then the tokens'
+    auto scale_off = [&](int row) __attribute__((always_inline)) {
+        if (row < L::BN) {
+            const int src = GATED ? 16 * (row >> 5) + (row & 15) : row;
+            return src < rows_n ? src * sb + (GATED && (row & 16) ? (int)(a.N * sb) : 0) : kCopyOob;
+        }
+        return row - L::BN < rows_m ? (row - L::BN) * sb : kCopyOob;
+    };
+    const __amdgpu_buffer_rsrc_t rs_ws =
+        make_rsrc(a.ws + n0 * sb, (GATED ? a.N * sb : 0) + (int64_t)rows_n * sb);
+    const __amdgpu_buffer_rsrc_t rs_as = make_rsrc(a.as + m0 * sb, (int64_t)rows_m * sb);
+    constexpr int NS = SPAN ? 1 : 4;                 // scale copies of a wave
+    int soff[NS];
 #pragma unroll
-        for (int j = 0; j < WM; ++j) {
-            const int64_t m = mt + 16 * j;
-            if (m >= a.M) continue;
+    for (int i = 0; i < NS; ++i)
+        soff[i] = scale_off(SPAN ? 64 * wave + lane : 16 * (i * W + wave) + (lane >> 2));
+    auto copy_scales = [&](int q) __attribute__((always_inline)) {
+        if constexpr (SPAN) {
+            copy16_to_lds_at(wave < W / 2 ? rs_ws : rs_as, sc + wave * 1024, q < q1 ? soff[0] : kCopyOob, 16 * q);
+        } else {
 #pragma unroll
-            for (int i = 0; i < WN; ++i) {
-                const int64_t n = n0 + 16 * WN * wn + 16 * i + 4 * lg;
-                const int left = (int)(a.N - n < 4 ? a.N - n : 4);
-                if (left > 0) store4(a.y, a.y_format, m * a.N + n, acc[i][j], left, wide && left == 4);
+            for (int i = 0; i < NS; ++i) {
+                const int step = 4 * q + (lane & 3);
+                const int at = soff[i] != kCopyOob && step < steps ? soff[i] + 4 * step : kCopyOob;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(i < NS / 2 ? rs_ws : rs_as,
+                                                         (lds_void_t *)(sc + (i * W + wave) * 256), 4, at, 0, 0, 0);
             }
         }
-    } else {
-        const bool wide = aligned4(a.y, a.y_format, a.N);
-        const bool wide_gu = aligned4(a.gu, a.y_format, a.N);
-        auto finish = [&](auto act) __attribute__((always_inline)) {
+    };
+
+    v4f32 acc[WN][WM];
+#pragma unroll
+    for (int i = 0; i < WN; ++i)
+#pragma unroll
+        for (int j = 0; j < WM; ++j) acc[i][j] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const int row_n = 16 * WN * wn + r, row_m = L::BN + 16 * WM * wm + r;
+    v4i w[WN], x[2][WM];
+    uint32_t sw[WN], sa[WM], sa_next[WM];
+    // step u of four: stage u / 2 of two slots, half u % 2
+    const uint8_t *const at0 = smem + 128 * row_n + 16 * (lg ^ mx_swizzle(r));
+    const uint8_t *const at1 = smem + 128 * row_n + 16 * ((4 + lg) ^ mx_swizzle(r));
+    const uint8_t *const at2 = at0 + L::kStageBytes, *const at3 = at1 + L::kStageBytes;
+    const int over = 128 * (row_m - row_n);
+    const uint8_t *const xt0 = at0 + over, *const xt1 = at1 + over, *const xt2 = at2 + over, *const xt3 = at3 + over;
+    auto read_w = [&](int u, int i) __attribute__((always_inline)) {
+        const uint8_t *p = u == 0 ? at0 : u == 1 ? at1 : u == 2 ? at2 : at3;
+        w[i] = *reinterpret_cast<const v4i *>(p + 2048 * i);
+    };
+    auto read_x = [&](int u, int j) __attribute__((always_inline)) {
+        const uint8_t *p = u == 0 ? xt0 : u == 1 ? xt1 : u == 2 ? xt2 : xt3;
+        x[u & 1][j] = *reinterpret_cast<const v4i *>(p + 2048 * j);
+    };
+    // byte lg of a row's four words: the lane's scales of four steps
+    const uint32_t pick = 0x0c0c0400u + 0x0101u * lg;
+    auto read_scale = [&](int row) __attribute__((always_inline)) {
+        const v4u v = *reinterpret_cast<const v4u *>(sc + 16 * row);
+        const uint32_t lo = __builtin_amdgcn_perm(v[1], v[0], pick);
+        const uint32_t hi = __builtin_amdgcn_perm(v[3], v[2], pick);
+        return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+    };
+
+    // the slots go by the stage's parity: start on an even one
+    const int s0 = 2 * q0;
+    copy_scales(q0);
+    open_stage(s0);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) copy(s0, k);
+    open_stage(s0 + 1);
+#pragma unroll
+    for (int k = 0; k < 6; ++k) copy(s0 + 1, k);
+    wait_vmem<6>();
+    ring_barrier();
+#pragma unroll
+    for (int i = 0; i < WN; ++i) read_w(0, i);
+#pragma unroll
+    for (int j = 0; j < WM; ++j) read_x(0, j);
+#pragma unroll
+    for (int i = 0; i < WN; ++i) sw[i] = read_scale(row_n + 16 * i);
+#pragma unroll
+    for (int j = 0; j < WM; ++j) sa[j] = read_scale(row_m + 16 * j);
+
+    constexpr int kLead = 2;                         // tiles multiplied before a step's barrier
+    for (int q = q0; q < q1; ++q) {
+        auto step = [&](auto number) __attribute__((always_inline)) {
+            constexpr int U = decltype(number)::value, V = (U + 1) & 3;
+            auto products = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+                for (int j = 0; j < WM; ++j)
+                    acc[i][j] = mfma_mx4<U>(w[i], x[U & 1][j], acc[i][j], sw[i], sa[j]);
+            };
+            auto next = [&](int i) __attribute__((always_inline)) {
+                read_w(V, i);
+                if (U == 3) sw[i] = read_scale(row_n + 16 * i);
+            };
+#pragma unroll
+            for (int i = 0; i < kLead; ++i) {
+                products(i);
+                if ((U & 1) == 0) copy(2 * q + 1 + U / 2, 6 + i);
+            }
+            if (U & 1) {
+                __builtin_amdgcn_sched_barrier(0);
+                wait_vmem<0>();                      // the next stage, and at U = 3 its scales
+                ring_barrier();                      // for all waves; this stage is read
+                if (U == 1) copy_scales(q + 1);
+                open_stage(2 * q + U / 2 + 2);
+            }
+#pragma unroll
+            for (int j = 0; j < WM; ++j) read_x(V, j);
+            if (U == 3) {
+#pragma unroll
+                for (int j = 0; j < WM; ++j) sa_next[j] = read_scale(row_m + 16 * j);
+            }
+#pragma unroll
+            for (int i = 0; i < kLead; ++i) next(i);
+#pragma unroll
+            for (int i = kLead; i < WN; ++i) {
+                products(i);
+                next(i);
+                if (U & 1) copy(2 * q + U / 2 + 2, i - kLead);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        step(std::integral_constant<int, 0>());
+        step(std::integral_constant<int, 1>());
+        step(std::integral_constant<int, 2>());
+        step(std::integral_constant<int, 3>());
+#pragma unroll
+        for (int j = 0; j < WM; ++j) sa[j] = sa_next[j];
+    }
+    wait_vmem<0>();                                  // no copy may land after the block ends
+
+    if (split) {
+        float *const to = plan.part + (int64_t)item * L::kPart + 4 * tid;
+#pragma unroll
+        for (int i = 0; i < WN; ++i)
+#pragma unroll
+            for (int j = 0; j < WM; ++j)
+                *reinterpret_cast<v4f32 *>(to + (i * WM + j) * (4 * L::T)) = acc[i][j];
+        return;
+    }
+    finish<WN, WM, GATED>(a, acc, n0 + (GATED ? 8 : 16) * WN * wn, m0 + 16 * WM * wm + r, lane);
+}
+
+// The split tiles' sums, added in the order of K, and their end: a block per
+// four of a tile's rows of instruction tiles.
+template <bool GATED>
+__global__ __launch_bounds__(512) void mx4_wide_sum_kernel(Mx4Args a, MxPlan plan) {
+    typedef MxWide L;
+    constexpr int NI = 4, WM = L::WM, kCuts = L::WN / NI;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
+    const int index = (int)blockIdx.x / kCuts, cut = (int)blockIdx.x % kCuts;
+    int tn, tm;
+    wide_tile(plan, plan.full + index, tn, tm);
+    v4f32 acc[NI][WM];
+    for (int way = 0; way < plan.ways; ++way) {
+        const float *from = plan.part + ((int64_t)index * plan.ways + way) * L::kPart + 4 * tid;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
             for (int j = 0; j < WM; ++j) {
-                const int64_t m = mt + 16 * j;
-                const bool live = m < a.M;
-#pragma unroll
-                for (int b = 0; b < WN / 4; ++b) {
-                    v4f32 h[2];
-                    const int64_t n = n0 + 8 * WN * wn + 32 * b;   // the block of 32 columns
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const v4f32 g = acc[4 * b + 2 * p][j], u = acc[4 * b + 2 * p + 1][j];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) h[p][i] = gate_act<act.value>(g[i]) * u[i];
-                        const int64_t c = n + 16 * p + 4 * lg;
-                        const int left = (int)(a.N - c < 4 ? a.N - c : 4);
-                        if (live && left > 0) {
-                            if (a.y) store4(a.y, a.y_format, m * a.N + c, h[p], left, wide && left == 4);
-                            if (a.gu) {
-                                const bool whole = wide_gu && left == 4;
-                                store4(a.gu, a.y_format, 2 * m * a.N + c, g, left, whole);
-                                store4(a.gu, a.y_format, (2 * m + 1) * a.N + c, u, left, whole);
-                            }
-                        }
-                    }
-                    if (a.hq)
-                        store_quantised(h, a.hq + (m * a.N + n) / 2, a.hs + (m * a.N + n) / 32,
-                                        live && n < a.N, lane);
-                    __builtin_amdgcn_sched_barrier(0);   // one block's registers at a time
-                }
+                const v4f32 v = *reinterpret_cast<const v4f32 *>(from + ((cut * NI + i) * WM + j) * (4 * L::T));
+                acc[i][j] = way ? acc[i][j] + v : v;
             }
-        };
-        if (a.act == kSilu)
-            finish(std::integral_constant<int, kSilu>());
-        else if (a.act == kGelu)
-            finish(std::integral_constant<int, kGelu>());
-        else
-            finish(std::integral_constant<int, kGeluTanh>());
     }
+    const int wn = wave % L::NWN, wm = wave / L::NWN;
+    const int64_t n0 = (int64_t)tn * (GATED ? L::BN / 2 : L::BN) + (GATED ? 8 : 16) * (L::WN * wn + NI * cut);
+    finish<NI, WM, GATED>(a, acc, n0, (int64_t)tm * L::BM + 16 * WM * wm + (lane & 15), lane);
 }
 
 template <class L, bool GATED>
@@ -307,16 +589,70 @@ hipError_t run_tiles(const Mx4Args &a, hipStream_t stream) {
     return span ? go(mx4_tile_kernel<L, GATED, true>) : go(mx4_tile_kernel<L, GATED, false>);
 }
 
+// Tiles left over after whole rounds of the compute units are split along K.
+MxPlan wide_plan(int64_t M, int64_t N, int64_t K, bool gated, size_t bytes) {
+    MxPlan p;
+    const int64_t rows = gated ? 2 * N : N;
+    p.tiles_n = (int)((rows + MxWide::BN - 1) / MxWide::BN);
+    p.tiles_m = (int)((M + MxWide::BM - 1) / MxWide::BM);
+    p.part = nullptr;
+    const int cus = device_cus() > 0 ? device_cus() : 256;
+    const int64_t tiles = (int64_t)p.tiles_n * p.tiles_m, rest = tiles % cus;
+    const int64_t runs = (K + 511) / 512;
+    p.full = (int)tiles;
+    p.ways = 1;
+    if (rest == 0) return p;
+    // in run times of a block (about 0.9 us): whole, or split with each block's
+    // sums written and read again (about 8 runs' time) and a second launch
+    int64_t best = runs;
+    for (int w = 2; w <= 16 && w <= runs; ++w) {
+        if ((size_t)(rest * w) * MxWide::kPart * sizeof(float) > bytes) break;
+        const int64_t cost = ((rest * w + cus - 1) / cus) * ((runs + w - 1) / w + 8) + 6;
+        if (cost < best) {
+            best = cost;
+            p.ways = w;
+            p.full = (int)(tiles - rest);
+        }
+    }
+    return p;
+}
+
+template <bool GATED>
+hipError_t run_wide(const Mx4Args &a, void *work, size_t bytes, hipStream_t stream) {
+    MxPlan p = wide_plan(a.M, a.N, a.K, GATED, work ? bytes : 0);
+    p.part = static_cast<float *>(work);
+    const int rest = p.tiles_n * p.tiles_m - p.full;
+    const bool span = a.K % 512 == 0 &&
+                      ((reinterpret_cast<uintptr_t>(a.as) | reinterpret_cast<uintptr_t>(a.ws)) & 15) == 0;
+    const dim3 grid((unsigned)((p.full + 7) / 8 * 8 + (rest * p.ways + 7) / 8 * 8));
+    if (span)
+        hipLaunchKernelGGL((mx4_wide_kernel<GATED, true>), grid, dim3(MxWide::T), MxWide::kLdsBytes, stream, a, p);
+    else
+        hipLaunchKernelGGL((mx4_wide_kernel<GATED, false>), grid, dim3(MxWide::T), MxWide::kLdsBytes, stream, a, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || rest == 0) return e;
+    hipLaunchKernelGGL(mx4_wide_sum_kernel<GATED>, dim3((unsigned)(rest * (MxWide::WN / 4))), dim3(MxWide::T), 0,
+                       stream, a, p);
+    return hipGetLastError();
+}
+
+bool takes_wide(int64_t M, int64_t N, bool gated) {
+    return (((gated ? 2 * N : N) + 255) / 256) * ((M + 255) / 256) >= 192;
+}
+
 }  // namespace
 
-size_t mx4_gemm_workspace_bytes(int64_t, int64_t, int64_t, bool) { return 0; }
+size_t mx4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
+    if (!takes_wide(M, N, gated)) return 0;
+    const MxPlan p = wide_plan(M, N, K, gated, SIZE_MAX);
+    return p.ways > 1 ? (size_t)(p.tiles_n * (int64_t)p.tiles_m - p.full) * p.ways * MxWide::kPart * sizeof(float) : 0;
+}
 
-hipError_t launch_mx4_gemm(const Mx4Args &a, bool gated, void *, size_t, hipStream_t stream) {
-    typedef MxTile<8, 4, 2, 4> Big;
+hipError_t launch_mx4_gemm(const Mx4Args &a, bool gated, void *work, size_t work_bytes,
+                           hipStream_t stream) {
     typedef MxTile<4, 1, 1, 4> Small;
-    const int64_t rows = gated ? 2 * a.N : a.N;
-    const int64_t big = ((rows + 255) / 256) * ((a.M + 255) / 256);
-    if (big >= 192) return gated ? run_tiles<Big, true>(a, stream) : run_tiles<Big, false>(a, stream);
+    if (takes_wide(a.M, a.N, gated))
+        return gated ? run_wide<true>(a, work, work_bytes, stream) : run_wide<false>(a, work, work_bytes, stream);
     return gated ? run_tiles<Small, true>(a, stream) : run_tiles<Small, false>(a, stream);
 }
 

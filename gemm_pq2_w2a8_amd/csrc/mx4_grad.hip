@@ -121,7 +121,7 @@ struct GradTile {
 };
 
 __device__ __forceinline__ int grad_turn(int n) { return (n & 3) | (((n >> 3) & 1) << 2); }
-__device__ __forceinline__ int grad_swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+__device__ __forceinline__ int grad_swizzle(int row) { return row & 6; }
 
 __device__ __forceinline__ uint32_t expand2(uint32_t word, float scale, int byte) {
     switch (byte) {
