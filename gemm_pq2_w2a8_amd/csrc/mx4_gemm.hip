@@ -75,7 +75,7 @@ __device__ __forceinline__ bool aligned4(const void *y, int fmt, int64_t n) {
 // so that blocks of 32 columns are whole.
 template <int NI, int WM, bool GATED>
 __device__ __forceinline__ void finish(const Mx4Args &a, const v4f32 (&acc)[NI][WM], int64_t n,
-                                       int64_t m, int lane) {
+                                       int64_t m, int64_t end, int lane) {
     const int lg = lane >> 4;
     const bool wide = aligned4(a.y, a.y_format, a.N);
     if constexpr (!GATED) {
@@ -86,12 +86,12 @@ __device__ __forceinline__ void finish(const Mx4Args &a, const v4f32 (&acc)[NI][
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 const int64_t c = n + 16 * i + 4 * lg;
-                const int left = (int)(a.N - c < 4 ? a.N - c : 4);
+                const int left = (int)(end - c < 4 ? end - c : 4);
                 if (left > 0) store4(a.y, a.y_format, t * a.N + c, acc[i][j], left, wide && left == 4);
             }
         }
     } else {
-        static_assert(NI % 4 == 0, "whole blocks of 32 columns");
+        constexpr int P = NI < 4 ? NI / 2 : 2;               // pairs of tiles at a time
         const bool wide_gu = aligned4(a.gu, a.y_format, a.N);
         auto run = [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
@@ -99,16 +99,16 @@ __device__ __forceinline__ void finish(const Mx4Args &a, const v4f32 (&acc)[NI][
                 const int64_t t = m + 16 * j;
                 const bool live = t < a.M;
 #pragma unroll
-                for (int b = 0; b < NI / 4; ++b) {
-                    v4f32 h[2];
-                    const int64_t nb = n + 32 * b;                 // the block of 32 columns
+                for (int b = 0; b < NI / (2 * P); ++b) {
+                    v4f32 h[P];
+                    const int64_t nb = n + 16 * P * b;
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const v4f32 g = acc[4 * b + 2 * p][j], u = acc[4 * b + 2 * p + 1][j];
+                    for (int p = 0; p < P; ++p) {
+                        const v4f32 g = acc[2 * (P * b + p)][j], u = acc[2 * (P * b + p) + 1][j];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) h[p][i] = gate_act<act.value>(g[i]) * u[i];
                         const int64_t c = nb + 16 * p + 4 * lg;
-                        const int left = (int)(a.N - c < 4 ? a.N - c : 4);
+                        const int left = (int)(end - c < 4 ? end - c : 4);
                         if (live && left > 0) {
                             if (a.y) store4(a.y, a.y_format, t * a.N + c, h[p], left, wide && left == 4);
                             if (a.gu) {
@@ -118,9 +118,11 @@ __device__ __forceinline__ void finish(const Mx4Args &a, const v4f32 (&acc)[NI][
                             }
                         }
                     }
-                    if (a.hq)
-                        store_quantised(h, a.hq + (t * a.N + nb) / 2, a.hs + (t * a.N + nb) / 32,
-                                        live && nb < a.N, lane);
+                    if constexpr (P == 2) {
+                        if (a.hq)
+                            store_quantised(h, a.hq + (t * a.N + nb) / 2, a.hs + (t * a.N + nb) / 32,
+                                            live && nb < end, lane);
+                    }
                     __builtin_amdgcn_sched_barrier(0);   // one block's registers at a time
                 }
             }
@@ -300,7 +302,7 @@ __global__ __launch_bounds__(L::T) void mx4_tile_kernel(Mx4Args a, int tiles_n, 
         }
     }
 
-    finish<WN, WM, GATED>(a, acc, n0 + (GATED ? 8 : 16) * WN * wn, m0 + 16 * WM * wm + r, lane);
+    finish<WN, WM, GATED>(a, acc, n0 + (GATED ? 8 : 16) * WN * wn, m0 + 16 * WM * wm + r, a.N, lane);
 }
 
 // ---------------------------------------------------------------- wide tiles
@@ -545,7 +547,7 @@ void mx4_wide_kernel(Mx4Args a, MxPlan plan) {
                 *reinterpret_cast<v4f32 *>(to + (i * WM + j) * (4 * L::T)) = acc[i][j];
         return;
     }
-    finish<WN, WM, GATED>(a, acc, n0 + (GATED ? 8 : 16) * WN * wn, m0 + 16 * WM * wm + r, lane);
+    finish<WN, WM, GATED>(a, acc, n0 + (GATED ? 8 : 16) * WN * wn, m0 + 16 * WM * wm + r, a.N, lane);
 }
 
 // The split tiles' sums, added in the order of K, and their end: a block per
@@ -571,7 +573,152 @@ __global__ __launch_bounds__(512) void mx4_wide_sum_kernel(Mx4Args a, MxPlan pla
     }
     const int wn = wave % L::NWN, wm = wave / L::NWN;
     const int64_t n0 = (int64_t)tn * (GATED ? L::BN / 2 : L::BN) + (GATED ? 8 : 16) * (L::WN * wn + NI * cut);
-    finish<NI, WM, GATED>(a, acc, n0, (int64_t)tm * L::BM + 16 * WM * wm + (lane & 15), lane);
+    finish<NI, WM, GATED>(a, acc, n0, (int64_t)tm * L::BM + 16 * WM * wm + (lane & 15), a.N, lane);
+}
+
+// ---------------------------------------------------------------- few tokens
+//
+// Up to 16 TT tokens a block: bound by the weights' bytes. A block takes `rows`
+// weight rows (gated: that many of gate and of up), a multiple of four chosen so
+// that the blocks fill the compute units evenly, and its waves share the runs of
+// 512 along K: their sums meet in LDS and are added in the order of K. A wave
+// copies a run's codes, of the weights and of the tokens, into a piece of LDS of
+// its own, 256 contiguous bytes a row and four rows a copy (loaded straight into
+// the instruction's registers, 64 bytes a row, every line is requested twice),
+// and waits for no other wave; the waves of a unit keep about 100 KB in flight.
+// The 16-byte unit c of row r lies at place c ^ (r % 16): reads of 16 rows are
+// free of bank conflicts.
+// An instruction's rows do not mix: tiles' rows past `rows`, whose reads are
+// clamped to the last one, and tokens past M make results that are not stored.
+// Rows past the end of an array lie outside its resource and read zeros.
+// TODO figures
+struct MxThin {
+    int rows;                         // of a block
+    int tokens4;                      // copies that hold a block's tokens, four each
+};
+
+template <int NI, int TT, bool GATED>
+__global__ __launch_bounds__(1024) void mx4_thin_kernel(Mx4Args a, MxThin plan) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int waves = blockDim.x >> 6;
+    const int r = lane & 15, lg = lane >> 4;
+    constexpr int kHalves = GATED ? 2 : 1, kTiles = NI / kHalves;
+    const int64_t n0 = (int64_t)blockIdx.x * plan.rows, m0 = (int64_t)blockIdx.y * (16 * TT);
+    const int kb = (int)(a.K / 2), sb = (int)(a.K / kMxBlock);
+    const int steps = (int)(a.K / 128), runs = (steps + 3) / 4;
+    const int q0 = __builtin_amdgcn_readfirstlane((int)((uint32_t)runs * wave / waves));
+    const int q1 = __builtin_amdgcn_readfirstlane((int)((uint32_t)runs * (wave + 1) / waves));
+    const int rows_n = (int)(a.N - n0 < plan.rows ? a.N - n0 : plan.rows);
+    const int rows_m = (int)(a.M - m0 < 16 * TT ? a.M - m0 : 16 * TT);
+    uint8_t *const mine = smem + wave * 256 * (kHalves * plan.rows + 4 * plan.tokens4);
+    uint8_t *const mine_x = mine + 256 * kHalves * plan.rows;
+
+    v4f32 acc[NI][TT];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < TT; ++j) acc[i][j] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+    // where the lane's row of tile i lies (gated: gate, up, gate, ...), and its token's
+    const uint8_t *from[NI], *from_x[TT];
+    int turn[NI], turn_x[TT];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int row = 16 * (i / kHalves) + r, in = row < plan.rows ? row : plan.rows - 1;
+        from[i] = mine + 256 * ((i % kHalves) * plan.rows + in);
+        turn[i] = in & 15;
+    }
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+        const int t = 16 * j + r, in = t < 4 * plan.tokens4 ? t : 4 * plan.tokens4 - 1;
+        from_x[j] = mine_x + 256 * in;
+        turn_x[j] = in & 15;
+    }
+    const uint32_t pick = 0x0c0c0400u + 0x0101u * lg;
+    auto own = [&](v4u v) __attribute__((always_inline)) {      // byte lg of the row's four words
+        const uint32_t lo = __builtin_amdgcn_perm(v[1], v[0], pick);
+        const uint32_t hi = __builtin_amdgcn_perm(v[3], v[2], pick);
+        return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+    };
+    // rows 4 p .. 4 p + 3 of an array's `rows` rows into `to`
+    auto copies = [&](const uint8_t *base, int rows, int pieces, uint8_t *to, int q) __attribute__((always_inline)) {
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, (int64_t)rows * kb);
+        for (int p = 0; p < pieces; ++p) {
+            const int row = 4 * p + lg, unit = r ^ (row & 15);
+            copy16_to_lds(rs, to + p * 1024,
+                          4 * q + (unit >> 2) < steps && row < rows ? row * kb + 16 * unit + 256 * q : kCopyOob);
+        }
+    };
+    for (int q = q0; q < q1; ++q) {
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+            copies(a.w + (n0 + h * a.N) * kb, rows_n, plan.rows / 4, mine + 256 * h * plan.rows, q);
+        copies(a.a + m0 * kb, rows_m, plan.tokens4, mine_x, q);
+        v4u sw[NI], sx[TT];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int row = 16 * (i / kHalves) + r;
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.ws + (n0 + (i % kHalves) * a.N) * sb, (int64_t)rows_n * sb);
+            sw[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(
+                rs, row < rows_n ? row * sb + 16 * q : kCopyOob, 0, 0));
+        }
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.as + m0 * sb, (int64_t)rows_m * sb);
+#pragma unroll
+        for (int j = 0; j < TT; ++j)
+            sx[j] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(
+                rs, 16 * j + r < rows_m ? (16 * j + r) * sb + 16 * q : kCopyOob, 0, 0));
+        wait_vmem<0>();
+        asm volatile("" ::: "memory");                           // no LDS read moves up
+        uint32_t ow[NI], ox[TT];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) ow[i] = own(sw[i]);
+#pragma unroll
+        for (int j = 0; j < TT; ++j) ox[j] = own(sx[j]);
+        // a step past K would take other rows' scales: it is left out
+        auto step = [&](auto u) __attribute__((always_inline)) {
+            if (4 * q + u.value >= steps) return;
+            v4i w[NI], x[TT];
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                w[i] = *reinterpret_cast<const v4i *>(from[i] + 16 * ((4 * u.value + lg) ^ turn[i]));
+#pragma unroll
+            for (int j = 0; j < TT; ++j)
+                x[j] = *reinterpret_cast<const v4i *>(from_x[j] + 16 * ((4 * u.value + lg) ^ turn_x[j]));
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int j = 0; j < TT; ++j)
+                    acc[i][j] = mfma_mx4<u.value>(w[i], x[j], acc[i][j], ow[i], ox[j]);
+        };
+        step(std::integral_constant<int, 0>());
+        step(std::integral_constant<int, 1>());
+        step(std::integral_constant<int, 2>());
+        step(std::integral_constant<int, 3>());
+        // the piece is read before the next run's copies into it
+        __builtin_amdgcn_s_waitcnt(0xC07F);                      // lgkmcnt(0)
+        asm volatile("" ::: "memory");
+    }
+    __syncthreads();
+    v4f32 *const sums = reinterpret_cast<v4f32 *>(smem);         // [waves][NI][TT][64]
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < TT; ++j) sums[((wave * NI + i) * TT + j) * kWave + lane] = acc[i][j];
+    __syncthreads();
+    // a wave ends one tile (gated: all of them, which a block of 32 columns may
+    // span) of one token tile at a time
+    constexpr int kEnds = GATED ? 1 : NI, kEach = NI / kEnds;
+    for (int e = wave; e < kEnds * TT; e += waves) {
+        const int i0 = e / TT, j = e % TT;
+        v4f32 v[kEach][1];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) v[i][0] = sums[((i0 + i) * TT + j) * kWave + lane];
+        for (int o = 1; o < waves; ++o)
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) v[i][0] += sums[((o * NI + i0 + i) * TT + j) * kWave + lane];
+        finish<kEach, 1, GATED>(a, v, n0 + 16 * i0, m0 + 16 * j + r, n0 + rows_n, lane);
+    }
 }
 
 template <class L, bool GATED>
@@ -636,6 +783,51 @@ hipError_t run_wide(const Mx4Args &a, void *work, size_t bytes, hipStream_t stre
     return hipGetLastError();
 }
 
+template <int NI, int TT, bool GATED>
+hipError_t launch_thin(const Mx4Args &a, int rows, hipStream_t stream) {
+    const int64_t blocks = (a.N + rows - 1) / rows, tokens = (a.M + 16 * TT - 1) / (16 * TT);
+    MxThin plan;
+    plan.rows = rows;
+    plan.tokens4 = (int)((a.M < 16 * TT ? a.M : 16 * TT) + 3) / 4;
+    // as many waves as LDS holds (two blocks a unit unless each has its own),
+    // the runs dealt evenly
+    const int64_t bytes = 256 * ((GATED ? 2 : 1) * rows + 4 * plan.tokens4);
+    const int64_t sums = NI * TT * 1024, piece = bytes > sums ? bytes : sums;
+    const int64_t runs = (a.K + 511) / 512;
+    int64_t most = (blocks * tokens > 256 ? 80 * 1024 : 160 * 1024) / piece;
+    most = most > 16 ? 16 : most;
+    const int64_t each = (runs + most - 1) / most;
+    const int waves = (int)((runs + each - 1) / each);
+    hipLaunchKernelGGL((mx4_thin_kernel<NI, TT, GATED>), dim3((unsigned)blocks, (unsigned)tokens),
+                       dim3((unsigned)(kWave * waves)), (size_t)(waves * piece), stream, a, plan);
+    return hipGetLastError();
+}
+
+// Rows of a block: those with which the busiest of the compute units reads the
+// fewest, each block counted as four more. Quantised columns go by whole blocks.
+int thin_rows(int64_t N, bool blocks32) {
+    const int64_t cus = device_cus() > 0 ? device_cus() : 256;
+    int best = 32;
+    int64_t least = INT64_MAX;
+    for (int rows = blocks32 ? 32 : 4; rows <= 32; rows += 4) {
+        const int64_t blocks = (N + rows - 1) / rows;
+        const int64_t cost = (blocks + cus - 1) / cus * (rows + 4);
+        if (cost < least) {
+            least = cost;
+            best = rows;
+        }
+    }
+    return best;
+}
+
+template <int TT>
+hipError_t run_thin(const Mx4Args &a, bool gated, hipStream_t stream) {
+    const int rows = thin_rows(a.N, gated && a.hq);
+    if (!gated)
+        return rows <= 16 ? launch_thin<1, TT, false>(a, rows, stream) : launch_thin<2, TT, false>(a, rows, stream);
+    return rows <= 16 ? launch_thin<2, TT, true>(a, rows, stream) : launch_thin<4, TT, true>(a, rows, stream);
+}
+
 bool takes_wide(int64_t M, int64_t N, bool gated) {
     return (((gated ? 2 * N : N) + 255) / 256) * ((M + 255) / 256) >= 192;
 }
@@ -653,6 +845,8 @@ hipError_t launch_mx4_gemm(const Mx4Args &a, bool gated, void *work, size_t work
     typedef MxTile<4, 1, 1, 4> Small;
     if (takes_wide(a.M, a.N, gated))
         return gated ? run_wide<true>(a, work, work_bytes, stream) : run_wide<false>(a, work, work_bytes, stream);
+    if (a.M <= 16) return run_thin<1>(a, gated, stream);
+    if (a.M <= 32) return run_thin<2>(a, gated, stream);
     return gated ? run_tiles<Small, true>(a, stream) : run_tiles<Small, false>(a, stream);
 }
 
