@@ -136,6 +136,106 @@ __device__ __forceinline__ void finish(const Mx4Args &a, const v4f32 (&acc)[NI][
     }
 }
 
+// ---------------------------------------------------------------- work of a block
+//
+// Tiles of a launch: the first `full` are computed whole, the K range of each of
+// the others is dealt to `ways` blocks, whose float32 sums lie in part [tiles -
+// full][ways][tile] in the lanes' own order until a second launch adds them in
+// the order of K. K goes by runs of 512, four instructions.
+struct MxPlan {
+    int tiles_n, tiles_m, full, ways;
+    float *part;
+};
+
+// Tile t: runs of four tiles down, so that what an XCD's contiguous run of tiles
+// reads at a time is about as high as wide.
+__device__ __forceinline__ void tile_at(const MxPlan &p, int t, int &tn, int &tm) {
+    constexpr int kDown = 4;
+    const int group = t / (kDown * p.tiles_n), in = t % (kDown * p.tiles_n);
+    const int left = p.tiles_m - group * kDown;
+    const int high = left < kDown ? left : kDown;
+    // (divisions leave uniform results in vector registers)
+    tm = __builtin_amdgcn_readfirstlane(group * kDown + in % high);
+    tn = __builtin_amdgcn_readfirstlane(in / high);
+}
+
+struct MxShare {
+    bool live, split;
+    int item;                         // of a split tile: its share's place in part
+    int64_t m0, n0;                   // first token, first column (gated: of h)
+    int q0, q1, steps;                // runs of this block, and where its steps end
+};
+
+// Whole tiles come first; each XCD takes a contiguous run of either kind.
+template <class L, bool GATED>
+__device__ __forceinline__ MxShare share_of(const Mx4Args &a, const MxPlan &p) {
+    MxShare s;
+    const int whole = (p.full + 7) / 8 * 8;
+    s.split = (int)blockIdx.x >= whole;
+    const int b = s.split ? blockIdx.x - whole : blockIdx.x;
+    const int count = s.split ? (p.tiles_n * p.tiles_m - p.full) * p.ways : p.full;
+    s.item = (b & 7) * ((count + 7) / 8) + (b >> 3);
+    s.live = s.item < count;
+    if (!s.live) return s;
+    const int ways = s.split ? p.ways : 1, way = s.split ? s.item % p.ways : 0;
+    int tn, tm;
+    tile_at(p, s.split ? p.full + s.item / p.ways : s.item, tn, tm);
+    s.m0 = (int64_t)tm * L::BM;
+    s.n0 = (int64_t)tn * (GATED ? L::BN / 2 : L::BN);
+    const int all = (int)((a.K / 128 + 3) / 4);
+    s.q0 = __builtin_amdgcn_readfirstlane((int)((uint32_t)all * way / ways));
+    s.q1 = __builtin_amdgcn_readfirstlane((int)((uint32_t)all * (way + 1) / ways));
+    s.steps = s.q1 == all ? (int)(a.K / 128) : 4 * s.q1;
+    return s;
+}
+
+// The end of a block's work: the tile's results, or a split tile's sums. Waves
+// past the last token have none.
+template <class L, bool GATED>
+__device__ __forceinline__ void end_share(const Mx4Args &a, const MxPlan &p, const MxShare &s,
+                                          const v4f32 (&acc)[L::WN][L::WM], int wave, int lane) {
+    const int wn = wave % L::NWN, wm = wave / L::NWN;
+    const int64_t m = s.m0 + 16 * L::WM * wm;
+    if (!s.split) {
+        finish<L::WN, L::WM, GATED>(a, acc, s.n0 + (GATED ? 8 : 16) * L::WN * wn, m + (lane & 15), a.N, lane);
+        return;
+    }
+    if (m >= a.M) return;
+    float *const to = p.part + (int64_t)s.item * (L::BN * L::BM) + 4 * (wave * kWave + lane);
+#pragma unroll
+    for (int i = 0; i < L::WN; ++i)
+#pragma unroll
+        for (int j = 0; j < L::WM; ++j)
+            *reinterpret_cast<v4f32 *>(to + (i * L::WM + j) * (4 * L::T)) = acc[i][j];
+}
+
+// The split tiles' sums and their end: a block for every four instruction tiles
+// of a wave's rows.
+template <class L, bool GATED>
+__global__ __launch_bounds__(L::T) void mx4_sum_kernel(Mx4Args a, MxPlan p) {
+    constexpr int NI = 4, WM = L::WM, kCuts = L::WN / NI;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
+    const int index = (int)blockIdx.x / kCuts, cut = (int)blockIdx.x % kCuts;
+    const int wn = wave % L::NWN, wm = wave / L::NWN;
+    int tn, tm;
+    tile_at(p, p.full + index, tn, tm);
+    const int64_t m = (int64_t)tm * L::BM + 16 * WM * wm;
+    if (m >= a.M) return;
+    v4f32 acc[NI][WM];
+    for (int way = 0; way < p.ways; ++way) {
+        const float *from = p.part + ((int64_t)index * p.ways + way) * (L::BN * L::BM) + 4 * tid;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int j = 0; j < WM; ++j) {
+                const v4f32 v = *reinterpret_cast<const v4f32 *>(from + ((cut * NI + i) * WM + j) * (4 * L::T));
+                acc[i][j] = way ? acc[i][j] + v : v;
+            }
+    }
+    const int64_t n = (int64_t)tn * (GATED ? L::BN / 2 : L::BN) + (GATED ? 8 : 16) * (L::WN * wn + NI * cut);
+    finish<NI, WM, GATED>(a, acc, n, m + (lane & 15), a.N, lane);
+}
+
 // ---------------------------------------------------------------- tiles
 //
 // A block owns BN weight rows x BM tokens, NWN x NWM waves of WN x WM
@@ -157,6 +257,9 @@ struct MxTile {
     static constexpr int kScaleBytes = (BN + BM) * 16;
     static constexpr int kLdsBytes = 2 * kStageBytes + 2 * kScaleBytes;
     static constexpr int kCopiesN = BN / 8 / W, kCopiesM = BM / 8 / W;   // per wave and stage
+    static constexpr int kBlocks = 160 * 1024 / kLdsBytes;               // a compute unit holds
+    static constexpr int kRun = BN == 64 ? 1050 : 1550, kMore = BN == 64 ? 1050 : 750,
+                         kEnds = BN == 64 ? 1500 : 3000;                 // plan_tiles's times, ns
     static_assert(BN % (8 * W) == 0 && BM % (8 * W) == 0 && BN % 64 == 0 && BM % 64 == 0, "copies");
 };
 
@@ -165,7 +268,7 @@ __device__ __forceinline__ int mx_swizzle(int row) { return row & 6; }
 // SPAN: rows of scales are copied 16 bytes at a time (K a multiple of 512 and
 // 16-byte bases); else 4 bytes at a time.
 template <class L, bool GATED, bool SPAN>
-__global__ __launch_bounds__(L::T) void mx4_tile_kernel(Mx4Args a, int tiles_n, int tiles) {
+__global__ __launch_bounds__(L::T) void mx4_tile_kernel(Mx4Args a, MxPlan plan) {
     constexpr int WN = L::WN, WM = L::WM, W = L::W;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int tid = threadIdx.x;
@@ -174,15 +277,11 @@ __global__ __launch_bounds__(L::T) void mx4_tile_kernel(Mx4Args a, int tiles_n, 
     const int wn = wave % L::NWN, wm = wave / L::NWN;
     const int r = lane & 15, lg = lane >> 4;
 
-    // each XCD takes a contiguous run of tiles
-    const int per = (tiles + 7) / 8;
-    const int tile = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
-    if (tile >= tiles) return;
-    const int64_t m0 = (int64_t)(tile / tiles_n) * L::BM;
-    const int64_t n0 = (int64_t)(tile % tiles_n) * (GATED ? L::BN / 2 : L::BN);
-
+    const MxShare share = share_of<L, GATED>(a, plan);
+    if (!share.live) return;
+    const int64_t m0 = share.m0, n0 = share.n0;
     const int kb = (int)(a.K / 2), sb = (int)(a.K / kMxBlock);   // bytes of a row
-    const int steps = (int)(a.K / 128), stages = (steps + 1) / 2;
+    const int steps = share.steps, stages = (steps + 1) / 2;     // where they end
     const int rows_n = (int)(a.N - n0 < L::BN ? a.N - n0 : L::BN);
     const int rows_m = (int)(a.M - m0 < L::BM ? a.M - m0 : L::BM);
 
@@ -268,9 +367,9 @@ __global__ __launch_bounds__(L::T) void mx4_tile_kernel(Mx4Args a, int tiles_n, 
         for (int j = 0; j < WM; ++j) acc[i][j] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
 
     const int row_n = 16 * WN * wn + r, row_m = L::BN + 16 * WM * wm + r;
-    issue_scales(0);
-    issue_stage(0);
-    for (int s = 0; s < stages; ++s) {
+    issue_scales(share.q0);
+    issue_stage(2 * share.q0);
+    for (int s = 2 * share.q0; s < stages; ++s) {
         wait_vmem<0>();                         // this wave's copies of stage s
         ring_barrier();                         // everyone's; and stage s - 1 is read
         if (s + 1 < stages) issue_stage(s + 1);
@@ -302,7 +401,7 @@ __global__ __launch_bounds__(L::T) void mx4_tile_kernel(Mx4Args a, int tiles_n, 
         }
     }
 
-    finish<WN, WM, GATED>(a, acc, n0 + (GATED ? 8 : 16) * WN * wn, m0 + 16 * WM * wm + r, a.N, lane);
+    end_share<L, GATED>(a, plan, share, acc, wave, lane);
 }
 
 // ---------------------------------------------------------------- wide tiles
@@ -323,27 +422,8 @@ struct MxWide {
     static constexpr int kStageBytes = (BN + BM) * 128;
     static constexpr int kScaleBytes = (BN + BM) * 16;
     static constexpr int kLdsBytes = 2 * kStageBytes + kScaleBytes;
-    static constexpr int kPart = BN * BM;                // floats of a split tile's partial sums
+    static constexpr int kBlocks = 1, kRun = 2300, kMore = 1700, kEnds = 6000;
 };
-
-// Tiles of a launch: the first `full` are computed whole, the K range of each of
-// the others is dealt to `ways` blocks, whose sums lie in part [tiles - full][ways]
-// [MxWide::kPart] in the lanes' own order.
-struct MxPlan {
-    int tiles_n, tiles_m, full, ways;
-    float *part;
-};
-
-// Tile t: runs of four tiles down, so that what an XCD's contiguous run of tiles
-// reads at a time is about as high as wide.
-__device__ __forceinline__ void wide_tile(const MxPlan &p, int t, int &tn, int &tm) {
-    constexpr int kDown = 4;
-    const int group = t / (kDown * p.tiles_n), in = t % (kDown * p.tiles_n);
-    const int left = p.tiles_m - group * kDown;
-    const int high = left < kDown ? left : kDown;
-    tm = group * kDown + in % high;
-    tn = in / high;
-}
 
 template <bool GATED, bool SPAN>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
@@ -358,26 +438,11 @@ void mx4_wide_kernel(Mx4Args a, MxPlan plan) {
     const int wn = wave % L::NWN, wm = wave / L::NWN;
     const int r = lane & 15, lg = lane >> 4;
 
-    // whole tiles first; each XCD takes a contiguous run of either kind
-    const int whole = (plan.full + 7) / 8 * 8;
-    const bool split = (int)blockIdx.x >= whole;
-    const int b = split ? blockIdx.x - whole : blockIdx.x;
-    const int count = split ? (plan.tiles_n * plan.tiles_m - plan.full) * plan.ways : plan.full;
-    const int item = (b & 7) * ((count + 7) / 8) + (b >> 3);
-    if (item >= count) return;
-    const int tile = split ? plan.full + item / plan.ways : item;
-    int tn, tm;
-    wide_tile(plan, tile, tn, tm);
-    // (divisions leave uniform results in vector registers)
-    const int64_t m0 = (int64_t)__builtin_amdgcn_readfirstlane(tm) * L::BM;
-    const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane(tn) * (GATED ? L::BN / 2 : L::BN);
-
+    const MxShare share = share_of<L, GATED>(a, plan);
+    if (!share.live) return;
+    const int64_t m0 = share.m0, n0 = share.n0;
     const int kb = (int)(a.K / 2), sb = (int)(a.K / kMxBlock);   // bytes of a row
-    const int all = (int)((a.K / 128 + 3) / 4);                  // runs of four steps
-    const int way = split ? item % plan.ways : 0, ways = split ? plan.ways : 1;
-    const int q0 = __builtin_amdgcn_readfirstlane((int)((uint32_t)all * way / ways));
-    const int q1 = __builtin_amdgcn_readfirstlane((int)((uint32_t)all * (way + 1) / ways));
-    const int steps = q1 == all ? (int)(a.K / 128) : 4 * q1;     // the end of this block's steps
+    const int q0 = share.q0, q1 = share.q1, steps = share.steps;
     const int rows_n = (int)(a.N - n0 < L::BN ? a.N - n0 : L::BN);
     const int rows_m = (int)(a.M - m0 < L::BM ? a.M - m0 : L::BM);
 
@@ -538,42 +603,7 @@ void mx4_wide_kernel(Mx4Args a, MxPlan plan) {
     }
     wait_vmem<0>();                                  // no copy may land after the block ends
 
-    if (split) {
-        float *const to = plan.part + (int64_t)item * L::kPart + 4 * tid;
-#pragma unroll
-        for (int i = 0; i < WN; ++i)
-#pragma unroll
-            for (int j = 0; j < WM; ++j)
-                *reinterpret_cast<v4f32 *>(to + (i * WM + j) * (4 * L::T)) = acc[i][j];
-        return;
-    }
-    finish<WN, WM, GATED>(a, acc, n0 + (GATED ? 8 : 16) * WN * wn, m0 + 16 * WM * wm + r, a.N, lane);
-}
-
-// The split tiles' sums, added in the order of K, and their end: a block per
-// four of a tile's rows of instruction tiles.
-template <bool GATED>
-__global__ __launch_bounds__(512) void mx4_wide_sum_kernel(Mx4Args a, MxPlan plan) {
-    typedef MxWide L;
-    constexpr int NI = 4, WM = L::WM, kCuts = L::WN / NI;
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
-    const int index = (int)blockIdx.x / kCuts, cut = (int)blockIdx.x % kCuts;
-    int tn, tm;
-    wide_tile(plan, plan.full + index, tn, tm);
-    v4f32 acc[NI][WM];
-    for (int way = 0; way < plan.ways; ++way) {
-        const float *from = plan.part + ((int64_t)index * plan.ways + way) * L::kPart + 4 * tid;
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-            for (int j = 0; j < WM; ++j) {
-                const v4f32 v = *reinterpret_cast<const v4f32 *>(from + ((cut * NI + i) * WM + j) * (4 * L::T));
-                acc[i][j] = way ? acc[i][j] + v : v;
-            }
-    }
-    const int wn = wave % L::NWN, wm = wave / L::NWN;
-    const int64_t n0 = (int64_t)tn * (GATED ? L::BN / 2 : L::BN) + (GATED ? 8 : 16) * (L::WN * wn + NI * cut);
-    finish<NI, WM, GATED>(a, acc, n0, (int64_t)tm * L::BM + 16 * WM * wm + (lane & 15), a.N, lane);
+    end_share<L, GATED>(a, plan, share, acc, wave, lane);
 }
 
 // ---------------------------------------------------------------- few tokens
@@ -604,7 +634,7 @@ __global__ __launch_bounds__(1024) void mx4_thin_kernel(Mx4Args a, MxThin plan) 
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int waves = blockDim.x >> 6;
     const int r = lane & 15, lg = lane >> 4;
-    constexpr int kHalves = GATED ? 2 : 1, kTiles = NI / kHalves;
+    constexpr int kHalves = GATED ? 2 : 1;
     const int64_t n0 = (int64_t)blockIdx.x * plan.rows, m0 = (int64_t)blockIdx.y * (16 * TT);
     const int kb = (int)(a.K / 2), sb = (int)(a.K / kMxBlock);
     const int steps = (int)(a.K / 128), runs = (steps + 3) / 4;
@@ -721,66 +751,82 @@ __global__ __launch_bounds__(1024) void mx4_thin_kernel(Mx4Args a, MxThin plan) 
     }
 }
 
-template <class L, bool GATED>
-hipError_t run_tiles(const Mx4Args &a, hipStream_t stream) {
-    constexpr int cols = GATED ? L::BN / 2 : L::BN;
-    const int64_t tn = (a.N + cols - 1) / cols, tm = (a.M + L::BM - 1) / L::BM;
-    const int64_t per = (tn * tm + 7) / 8;
-    const bool span = a.K % 512 == 0 &&
-                      ((reinterpret_cast<uintptr_t>(a.as) | reinterpret_cast<uintptr_t>(a.ws)) & 15) == 0;
-    const auto go = [&](auto kernel) -> hipError_t {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)(8 * per)), dim3(L::T), L::kLdsBytes, stream, a,
-                           (int)tn, (int)(tn * tm));
-        return hipGetLastError();
-    };
-    return span ? go(mx4_tile_kernel<L, GATED, true>) : go(mx4_tile_kernel<L, GATED, false>);
-}
+// The plan of a tile for a shape. Tiles left over after whole rounds of the
+// compute units (each holds L::kBlocks) are split along K where that is faster
+// by this count in nanoseconds: a block takes L::kRun for a run alone on the
+// card and L::kMore longer with all places taken, L::kEnds for its start and end;
+// a split tile's sums are written and read again at about 4 TB/s in a second
+// launch. (Measured at 33 to 4096 tokens, N x K 5120 x 17408, 17408 x 5120, 6144 x
+// 5120, 17408 x 1024 and 1411 x 896, each tile in 1 to 16 ways: the count takes
+// the fastest or one within a tenth of it.)
+struct MxCost {
+    MxPlan plan;
+    int64_t ns;
+};
 
-// Tiles left over after whole rounds of the compute units are split along K.
-MxPlan wide_plan(int64_t M, int64_t N, int64_t K, bool gated, size_t bytes) {
-    MxPlan p;
+template <class L>
+MxCost plan_tiles(int64_t M, int64_t N, int64_t K, bool gated, size_t bytes) {
+    MxCost c;
+    MxPlan &p = c.plan;
     const int64_t rows = gated ? 2 * N : N;
-    p.tiles_n = (int)((rows + MxWide::BN - 1) / MxWide::BN);
-    p.tiles_m = (int)((M + MxWide::BM - 1) / MxWide::BM);
+    p.tiles_n = (int)((rows + L::BN - 1) / L::BN);
+    p.tiles_m = (int)((M + L::BM - 1) / L::BM);
     p.part = nullptr;
-    const int cus = device_cus() > 0 ? device_cus() : 256;
-    const int64_t tiles = (int64_t)p.tiles_n * p.tiles_m, rest = tiles % cus;
-    const int64_t runs = (K + 511) / 512;
-    p.full = (int)tiles;
     p.ways = 1;
-    if (rest == 0) return p;
-    // in run times of a block (about 0.9 us): whole, or split with each block's
-    // sums written and read again (about 8 runs' time) and a second launch
-    int64_t best = runs;
+    const int64_t cus = device_cus() > 0 ? device_cus() : 256, slots = cus * L::kBlocks;
+    const int64_t tiles = (int64_t)p.tiles_n * p.tiles_m, rest = tiles % slots, runs = (K + 511) / 512;
+    p.full = (int)tiles;
+    const int64_t part = (int64_t)L::BN * L::BM * sizeof(float);
+    auto rounds = [&](int64_t blocks, int64_t each) {
+        const int64_t full = blocks / slots, left = blocks % slots;
+        return full * (each * (L::kRun + L::kMore) + L::kEnds) +
+               (left ? each * (L::kRun + L::kMore * left / slots) + L::kEnds : 0);
+    };
+    const int64_t whole = rounds(tiles - rest, runs);
+    c.ns = rounds(tiles, runs);
+    const int64_t most = M < L::BM ? (M + 15) / 16 * 16 : L::BM;    // tokens whose sums are kept
     for (int w = 2; w <= 16 && w <= runs; ++w) {
-        if ((size_t)(rest * w) * MxWide::kPart * sizeof(float) > bytes) break;
-        const int64_t cost = ((rest * w + cus - 1) / cus) * ((runs + w - 1) / w + 8) + 6;
-        if (cost < best) {
-            best = cost;
+        if ((size_t)(rest * w * part) > bytes) break;
+        const int64_t sums = rest * w * (part * most / L::BM) * 2 / 4000 + 3000;
+        const int64_t ns = whole + rounds(rest * w, (runs + w - 1) / w) + sums;
+        if (rest && ns < c.ns) {
+            c.ns = ns;
             p.ways = w;
             p.full = (int)(tiles - rest);
         }
     }
-    return p;
+    return c;
 }
 
-template <bool GATED>
-hipError_t run_wide(const Mx4Args &a, void *work, size_t bytes, hipStream_t stream) {
-    MxPlan p = wide_plan(a.M, a.N, a.K, GATED, work ? bytes : 0);
+template <class L, bool GATED>
+hipError_t launch_tiles(const Mx4Args &a, MxPlan p, void *work, hipStream_t stream) {
     p.part = static_cast<float *>(work);
     const int rest = p.tiles_n * p.tiles_m - p.full;
     const bool span = a.K % 512 == 0 &&
                       ((reinterpret_cast<uintptr_t>(a.as) | reinterpret_cast<uintptr_t>(a.ws)) & 15) == 0;
-    const dim3 grid((unsigned)((p.full + 7) / 8 * 8 + (rest * p.ways + 7) / 8 * 8));
-    if (span)
-        hipLaunchKernelGGL((mx4_wide_kernel<GATED, true>), grid, dim3(MxWide::T), MxWide::kLdsBytes, stream, a, p);
+    const dim3 grid((unsigned)((p.full + 7) / 8 * 8 + (rest * p.ways + 7) / 8 * 8)), block(L::T);
+    const auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, block, L::kLdsBytes, stream, a, p);
+        return hipGetLastError();
+    };
+    hipError_t e;
+    if constexpr (std::is_same<L, MxWide>::value)
+        e = span ? go(mx4_wide_kernel<GATED, true>) : go(mx4_wide_kernel<GATED, false>);
     else
-        hipLaunchKernelGGL((mx4_wide_kernel<GATED, false>), grid, dim3(MxWide::T), MxWide::kLdsBytes, stream, a, p);
-    const hipError_t e = hipGetLastError();
+        e = span ? go(mx4_tile_kernel<L, GATED, true>) : go(mx4_tile_kernel<L, GATED, false>);
     if (e != hipSuccess || rest == 0) return e;
-    hipLaunchKernelGGL(mx4_wide_sum_kernel<GATED>, dim3((unsigned)(rest * (MxWide::WN / 4))), dim3(MxWide::T), 0,
-                       stream, a, p);
+    hipLaunchKernelGGL((mx4_sum_kernel<L, GATED>), dim3((unsigned)(rest * (L::WN / 4))), block, 0, stream, a, p);
     return hipGetLastError();
+}
+
+template <class L>
+hipError_t run_tiles(const Mx4Args &a, bool gated, const MxPlan &p, void *work, hipStream_t stream) {
+    return gated ? launch_tiles<L, true>(a, p, work, stream) : launch_tiles<L, false>(a, p, work, stream);
+}
+
+template <class L>
+size_t part_bytes(const MxPlan &p) {
+    return p.ways > 1 ? (size_t)((int64_t)p.tiles_n * p.tiles_m - p.full) * p.ways * (L::BN * L::BM) * sizeof(float) : 0;
 }
 
 template <int NI, int TT, bool GATED>
@@ -828,26 +874,47 @@ hipError_t run_thin(const Mx4Args &a, bool gated, hipStream_t stream) {
     return rows <= 16 ? launch_thin<2, TT, true>(a, rows, stream) : launch_thin<4, TT, true>(a, rows, stream);
 }
 
-bool takes_wide(int64_t M, int64_t N, bool gated) {
-    return (((gated ? 2 * N : N) + 255) / 256) * ((M + 255) / 256) >= 192;
+typedef MxTile<4, 1, 1, 4> MxSmall;    // 64 x 64
+typedef MxTile<4, 4, 2, 2> MxMid;      // 128 x 128
+
+// The tile for a shape: the least of plan_tiles's counts.
+enum class MxKind { kSmall, kMid, kWide };
+MxKind choose_tile(int64_t M, int64_t N, int64_t K, bool gated, size_t bytes, MxPlan &plan) {
+    const MxCost s = plan_tiles<MxSmall>(M, N, K, gated, bytes), m = plan_tiles<MxMid>(M, N, K, gated, bytes),
+                 w = plan_tiles<MxWide>(M, N, K, gated, bytes);
+    const MxKind kind = w.ns <= s.ns && w.ns <= m.ns ? MxKind::kWide : m.ns <= s.ns ? MxKind::kMid : MxKind::kSmall;
+    plan = kind == MxKind::kWide ? w.plan : kind == MxKind::kMid ? m.plan : s.plan;
+    return kind;
+}
+
+// Up to 16 tokens, and up to 32 where 64 x 64 tiles are few: a gated block of 17408
+// columns takes 24.0 us this way at 32 tokens and 21 in tiles, 5120 x 17408 13.5
+// and 20.
+bool takes_thin(int64_t M, int64_t N, bool gated) {
+    return M <= 16 || (M <= 32 && (gated ? 2 * N : N) < 64 * 512);
 }
 
 }  // namespace
 
 size_t mx4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
-    if (!takes_wide(M, N, gated)) return 0;
-    const MxPlan p = wide_plan(M, N, K, gated, SIZE_MAX);
-    return p.ways > 1 ? (size_t)(p.tiles_n * (int64_t)p.tiles_m - p.full) * p.ways * MxWide::kPart * sizeof(float) : 0;
+    if (takes_thin(M, N, gated)) return 0;
+    MxPlan p;
+    switch (choose_tile(M, N, K, gated, SIZE_MAX, p)) {
+        case MxKind::kSmall: return part_bytes<MxSmall>(p);
+        case MxKind::kMid: return part_bytes<MxMid>(p);
+        default: return part_bytes<MxWide>(p);
+    }
 }
 
 hipError_t launch_mx4_gemm(const Mx4Args &a, bool gated, void *work, size_t work_bytes,
                            hipStream_t stream) {
-    typedef MxTile<4, 1, 1, 4> Small;
-    if (takes_wide(a.M, a.N, gated))
-        return gated ? run_wide<true>(a, work, work_bytes, stream) : run_wide<false>(a, work, work_bytes, stream);
-    if (a.M <= 16) return run_thin<1>(a, gated, stream);
-    if (a.M <= 32) return run_thin<2>(a, gated, stream);
-    return gated ? run_tiles<Small, true>(a, stream) : run_tiles<Small, false>(a, stream);
+    if (takes_thin(a.M, a.N, gated)) return a.M <= 16 ? run_thin<1>(a, gated, stream) : run_thin<2>(a, gated, stream);
+    MxPlan p;
+    switch (choose_tile(a.M, a.N, a.K, gated, work ? work_bytes : 0, p)) {
+        case MxKind::kSmall: return run_tiles<MxSmall>(a, gated, p, work, stream);
+        case MxKind::kMid: return run_tiles<MxMid>(a, gated, p, work, stream);
+        default: return run_tiles<MxWide>(a, gated, p, work, stream);
+    }
 }
 
 }  // namespace pq2
