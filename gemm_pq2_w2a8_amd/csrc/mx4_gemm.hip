@@ -14,7 +14,7 @@
 
 #include "mx4_device.hpp"
 #include "mx4_launch.hpp"
-#include "pq2_launch.hpp"
+#include "mx4_plan.hpp"
 
 namespace pq2 {
 namespace {
@@ -63,9 +63,35 @@ __device__ __forceinline__ void store4(void *y, int fmt, int64_t at, v4f32 v, in
         if (i < left) store_fmt(y, fmt, at + i, v[i]);
 }
 
-// Whether every run of four columns from a multiple of four on is aligned.
+// Whether every run of four columns from a multiple of four on is aligned, and of
+// eight.
 __device__ __forceinline__ bool aligned4(const void *y, int fmt, int64_t n) {
     return (n & 3) == 0 && (reinterpret_cast<uintptr_t>(y) & (fmt == kF32 ? 15 : 7)) == 0;
+}
+__device__ __forceinline__ bool aligned8(const void *y, int64_t n) {
+    return (n & 7) == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0;
+}
+
+// 32 columns of one row from element `at` on, which is a multiple of 16 columns
+// into it: a lane's four of the first 16 and of the second. 16-bit rows exchange
+// every other 16 lanes' second halves, so that a lane has eight columns in a row
+// and the four lanes of a token write 64 contiguous bytes at once (eight bytes a
+// lane, 32 contiguous, took the gated batch of 2048 x 17408 with g and u 305 us
+// instead of 279). `left`: columns that exist; live: the lane's row does.
+__device__ __forceinline__ void store_pair(void *y, int fmt, int64_t at, v4f32 a, v4f32 b, int64_t left,
+                                           bool live, int lg, bool four, bool eight) {
+    if (fmt != kF32 && eight && left >= 32) {
+        const auto lo = __builtin_amdgcn_permlane16_swap(pack16(fmt, a[0], a[1]), pack16(fmt, b[0], b[1]), false, false);
+        const auto hi = __builtin_amdgcn_permlane16_swap(pack16(fmt, a[2], a[3]), pack16(fmt, b[2], b[3]), false, false);
+        const v4u v = {lo[0], hi[0], lo[1], hi[1]};
+        if (live) *reinterpret_cast<v4u *>(static_cast<uint16_t *>(y) + at + 16 * (lg & 1) + 8 * (lg >> 1)) = v;
+        return;
+    }
+    if (!live) return;
+    const int la = (int)(left - 4 * lg < 4 ? left - 4 * lg : 4);
+    if (la > 0) store4(y, fmt, at + 4 * lg, a, la, four && la == 4);
+    const int lb = (int)(left - 16 - 4 * lg < 4 ? left - 16 - 4 * lg : 4);
+    if (lb > 0) store4(y, fmt, at + 16 + 4 * lg, b, lb, four && lb == 4);
 }
 
 // The end of a product: acc[i][j] are four consecutive rows of w (from 4 (lane /
@@ -79,20 +105,27 @@ __device__ __forceinline__ void finish(const Mx4Args &a, const v4f32 (&acc)[NI][
     const int lg = lane >> 4;
     const bool wide = aligned4(a.y, a.y_format, a.N);
     if constexpr (!GATED) {
+        const bool eight = aligned8(a.y, a.N);
 #pragma unroll
         for (int j = 0; j < WM; ++j) {
             const int64_t t = m + 16 * j;
-            if (t >= a.M) continue;
+            if constexpr (NI % 2 == 0) {
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int64_t c = n + 16 * i + 4 * lg;
+                for (int i = 0; i < NI; i += 2) {
+                    const int64_t c = n + 16 * i;
+                    store_pair(a.y, a.y_format, t * a.N + c, acc[i][j], acc[i + 1][j], end - c, t < a.M, lg,
+                               wide, eight);
+                }
+            } else {
+                const int64_t c = n + 4 * lg;
                 const int left = (int)(end - c < 4 ? end - c : 4);
-                if (left > 0) store4(a.y, a.y_format, t * a.N + c, acc[i][j], left, wide && left == 4);
+                if (t < a.M && left > 0) store4(a.y, a.y_format, t * a.N + c, acc[0][j], left, wide && left == 4);
             }
         }
     } else {
         constexpr int P = NI < 4 ? NI / 2 : 2;               // pairs of tiles at a time
         const bool wide_gu = aligned4(a.gu, a.y_format, a.N);
+        const bool eight = aligned8(a.y, a.N), eight_gu = aligned8(a.gu, a.N);
         auto run = [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
             for (int j = 0; j < WM; ++j) {
@@ -100,28 +133,26 @@ __device__ __forceinline__ void finish(const Mx4Args &a, const v4f32 (&acc)[NI][
                 const bool live = t < a.M;
 #pragma unroll
                 for (int b = 0; b < NI / (2 * P); ++b) {
-                    v4f32 h[P];
-                    const int64_t nb = n + 16 * P * b;
+                    v4f32 g[2], u[2], h[2];
+                    const int64_t c = n + 16 * P * b;
 #pragma unroll
-                    for (int p = 0; p < P; ++p) {
-                        const v4f32 g = acc[2 * (P * b + p)][j], u = acc[2 * (P * b + p) + 1][j];
+                    for (int p = 0; p < 2; ++p) {
+                        const int q = p < P ? p : 0;                // one pair: its columns end after 16
+                        g[p] = acc[2 * (P * b + q)][j];
+                        u[p] = acc[2 * (P * b + q) + 1][j];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) h[p][i] = gate_act<act.value>(g[i]) * u[i];
-                        const int64_t c = nb + 16 * p + 4 * lg;
-                        const int left = (int)(end - c < 4 ? end - c : 4);
-                        if (live && left > 0) {
-                            if (a.y) store4(a.y, a.y_format, t * a.N + c, h[p], left, wide && left == 4);
-                            if (a.gu) {
-                                const bool whole = wide_gu && left == 4;
-                                store4(a.gu, a.y_format, 2 * t * a.N + c, g, left, whole);
-                                store4(a.gu, a.y_format, (2 * t + 1) * a.N + c, u, left, whole);
-                            }
-                        }
+                        for (int i = 0; i < 4; ++i) h[p][i] = p < P ? gate_act<act.value>(g[p][i]) * u[p][i] : 0.0f;
+                    }
+                    const int64_t left = P == 2 || end - c < 16 ? end - c : 16;
+                    if (a.y) store_pair(a.y, a.y_format, t * a.N + c, h[0], h[1], left, live, lg, wide, eight);
+                    if (a.gu) {
+                        store_pair(a.gu, a.y_format, 2 * t * a.N + c, g[0], g[1], left, live, lg, wide_gu, eight_gu);
+                        store_pair(a.gu, a.y_format, (2 * t + 1) * a.N + c, u[0], u[1], left, live, lg, wide_gu, eight_gu);
                     }
                     if constexpr (P == 2) {
                         if (a.hq)
-                            store_quantised(h, a.hq + (t * a.N + nb) / 2, a.hs + (t * a.N + nb) / 32,
-                                            live && nb < end, lane);
+                            store_quantised(h, a.hq + (t * a.N + c) / 2, a.hs + (t * a.N + c) / 32,
+                                            live && c < end, lane);
                     }
                     __builtin_amdgcn_sched_barrier(0);   // one block's registers at a time
                 }
@@ -136,57 +167,10 @@ __device__ __forceinline__ void finish(const Mx4Args &a, const v4f32 (&acc)[NI][
     }
 }
 
-// ---------------------------------------------------------------- work of a block
-//
-// Tiles of a launch: the first `full` are computed whole, the K range of each of
-// the others is dealt to `ways` blocks, whose float32 sums lie in part [tiles -
-// full][ways][tile] in the lanes' own order until a second launch adds them in
-// the order of K. K goes by runs of 512, four instructions.
-struct MxPlan {
-    int tiles_n, tiles_m, full, ways;
-    float *part;
-};
-
-// Tile t: runs of four tiles down, so that what an XCD's contiguous run of tiles
-// reads at a time is about as high as wide.
-__device__ __forceinline__ void tile_at(const MxPlan &p, int t, int &tn, int &tm) {
-    constexpr int kDown = 4;
-    const int group = t / (kDown * p.tiles_n), in = t % (kDown * p.tiles_n);
-    const int left = p.tiles_m - group * kDown;
-    const int high = left < kDown ? left : kDown;
-    // (divisions leave uniform results in vector registers)
-    tm = __builtin_amdgcn_readfirstlane(group * kDown + in % high);
-    tn = __builtin_amdgcn_readfirstlane(in / high);
-}
-
-struct MxShare {
-    bool live, split;
-    int item;                         // of a split tile: its share's place in part
-    int64_t m0, n0;                   // first token, first column (gated: of h)
-    int q0, q1, steps;                // runs of this block, and where its steps end
-};
-
-// Whole tiles come first; each XCD takes a contiguous run of either kind.
+// First column of a tile (gated: of h).
 template <class L, bool GATED>
-__device__ __forceinline__ MxShare share_of(const Mx4Args &a, const MxPlan &p) {
-    MxShare s;
-    const int whole = (p.full + 7) / 8 * 8;
-    s.split = (int)blockIdx.x >= whole;
-    const int b = s.split ? blockIdx.x - whole : blockIdx.x;
-    const int count = s.split ? (p.tiles_n * p.tiles_m - p.full) * p.ways : p.full;
-    s.item = (b & 7) * ((count + 7) / 8) + (b >> 3);
-    s.live = s.item < count;
-    if (!s.live) return s;
-    const int ways = s.split ? p.ways : 1, way = s.split ? s.item % p.ways : 0;
-    int tn, tm;
-    tile_at(p, s.split ? p.full + s.item / p.ways : s.item, tn, tm);
-    s.m0 = (int64_t)tm * L::BM;
-    s.n0 = (int64_t)tn * (GATED ? L::BN / 2 : L::BN);
-    const int all = (int)((a.K / 128 + 3) / 4);
-    s.q0 = __builtin_amdgcn_readfirstlane((int)((uint32_t)all * way / ways));
-    s.q1 = __builtin_amdgcn_readfirstlane((int)((uint32_t)all * (way + 1) / ways));
-    s.steps = s.q1 == all ? (int)(a.K / 128) : 4 * s.q1;
-    return s;
+__device__ __forceinline__ int64_t first_column(int tn) {
+    return (int64_t)tn * (GATED ? L::BN / 2 : L::BN);
 }
 
 // The end of a block's work: the tile's results, or a split tile's sums. Waves
@@ -195,18 +179,12 @@ template <class L, bool GATED>
 __device__ __forceinline__ void end_share(const Mx4Args &a, const MxPlan &p, const MxShare &s,
                                           const v4f32 (&acc)[L::WN][L::WM], int wave, int lane) {
     const int wn = wave % L::NWN, wm = wave / L::NWN;
-    const int64_t m = s.m0 + 16 * L::WM * wm;
+    const int64_t m = (int64_t)s.tm * L::BM + 16 * L::WM * wm;
     if (!s.split) {
-        finish<L::WN, L::WM, GATED>(a, acc, s.n0 + (GATED ? 8 : 16) * L::WN * wn, m + (lane & 15), a.N, lane);
+        finish<L::WN, L::WM, GATED>(a, acc, first_column<L, GATED>(s.tn) + (GATED ? 8 : 16) * L::WN * wn, m + (lane & 15), a.N, lane);
         return;
     }
-    if (m >= a.M) return;
-    float *const to = p.part + (int64_t)s.item * (L::BN * L::BM) + 4 * (wave * kWave + lane);
-#pragma unroll
-    for (int i = 0; i < L::WN; ++i)
-#pragma unroll
-        for (int j = 0; j < L::WM; ++j)
-            *reinterpret_cast<v4f32 *>(to + (i * L::WM + j) * (4 * L::T)) = acc[i][j];
+    if (m < a.M) store_share<L::WN, L::WM, L::T>(p, s.item, wave * kWave + lane, acc);
 }
 
 // The split tiles' sums and their end: a block for every four instruction tiles
@@ -222,17 +200,8 @@ __global__ __launch_bounds__(L::T) void mx4_sum_kernel(Mx4Args a, MxPlan p) {
     const int64_t m = (int64_t)tm * L::BM + 16 * WM * wm;
     if (m >= a.M) return;
     v4f32 acc[NI][WM];
-    for (int way = 0; way < p.ways; ++way) {
-        const float *from = p.part + ((int64_t)index * p.ways + way) * (L::BN * L::BM) + 4 * tid;
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-            for (int j = 0; j < WM; ++j) {
-                const v4f32 v = *reinterpret_cast<const v4f32 *>(from + ((cut * NI + i) * WM + j) * (4 * L::T));
-                acc[i][j] = way ? acc[i][j] + v : v;
-            }
-    }
-    const int64_t n = (int64_t)tn * (GATED ? L::BN / 2 : L::BN) + (GATED ? 8 : 16) * (L::WN * wn + NI * cut);
+    sum_shares<NI, L::WN, WM, L::T>(p, index, NI * cut, tid, acc);
+    const int64_t n = first_column<L, GATED>(tn) + (GATED ? 8 : 16) * (L::WN * wn + NI * cut);
     finish<NI, WM, GATED>(a, acc, n, m + (lane & 15), a.N, lane);
 }
 
@@ -277,11 +246,12 @@ __global__ __launch_bounds__(L::T) void mx4_tile_kernel(Mx4Args a, MxPlan plan) 
     const int wn = wave % L::NWN, wm = wave / L::NWN;
     const int r = lane & 15, lg = lane >> 4;
 
-    const MxShare share = share_of<L, GATED>(a, plan);
+    const MxShare share = share_of(plan);
     if (!share.live) return;
-    const int64_t m0 = share.m0, n0 = share.n0;
+    const int64_t m0 = (int64_t)share.tm * L::BM, n0 = first_column<L, GATED>(share.tn);
     const int kb = (int)(a.K / 2), sb = (int)(a.K / kMxBlock);   // bytes of a row
-    const int steps = share.steps, stages = (steps + 1) / 2;     // where they end
+    // where the block's steps end: a run is four
+    const int steps = share.q1 == plan.runs ? (int)(a.K / 128) : 4 * share.q1, stages = (steps + 1) / 2;
     const int rows_n = (int)(a.N - n0 < L::BN ? a.N - n0 : L::BN);
     const int rows_m = (int)(a.M - m0 < L::BM ? a.M - m0 : L::BM);
 
@@ -438,11 +408,12 @@ void mx4_wide_kernel(Mx4Args a, MxPlan plan) {
     const int wn = wave % L::NWN, wm = wave / L::NWN;
     const int r = lane & 15, lg = lane >> 4;
 
-    const MxShare share = share_of<L, GATED>(a, plan);
+    const MxShare share = share_of(plan);
     if (!share.live) return;
-    const int64_t m0 = share.m0, n0 = share.n0;
+    const int64_t m0 = (int64_t)share.tm * L::BM, n0 = first_column<L, GATED>(share.tn);
     const int kb = (int)(a.K / 2), sb = (int)(a.K / kMxBlock);   // bytes of a row
-    const int q0 = share.q0, q1 = share.q1, steps = share.steps;
+    const int q0 = share.q0, q1 = share.q1;
+    const int steps = q1 == plan.runs ? (int)(a.K / 128) : 4 * q1;   // where the block's end
     const int rows_n = (int)(a.N - n0 < L::BN ? a.N - n0 : L::BN);
     const int rows_m = (int)(a.M - m0 < L::BM ? a.M - m0 : L::BM);
 
@@ -751,60 +722,13 @@ __global__ __launch_bounds__(1024) void mx4_thin_kernel(Mx4Args a, MxThin plan) 
     }
 }
 
-// The plan of a tile for a shape. Tiles left over after whole rounds of the
-// compute units (each holds L::kBlocks) are split along K where that is faster
-// by this count in nanoseconds: a block takes L::kRun for a run alone on the
-// card and L::kMore longer with all places taken, L::kEnds for its start and end;
-// a split tile's sums are written and read again at about 4 TB/s in a second
-// launch. (Measured at 33 to 4096 tokens, N x K 5120 x 17408, 17408 x 5120, 6144 x
-// 5120, 17408 x 1024 and 1411 x 896, each tile in 1 to 16 ways: the count takes
-// the fastest or one within a tenth of it.)
-struct MxCost {
-    MxPlan plan;
-    int64_t ns;
-};
-
-template <class L>
-MxCost plan_tiles(int64_t M, int64_t N, int64_t K, bool gated, size_t bytes) {
-    MxCost c;
-    MxPlan &p = c.plan;
-    const int64_t rows = gated ? 2 * N : N;
-    p.tiles_n = (int)((rows + L::BN - 1) / L::BN);
-    p.tiles_m = (int)((M + L::BM - 1) / L::BM);
-    p.part = nullptr;
-    p.ways = 1;
-    const int64_t cus = device_cus() > 0 ? device_cus() : 256, slots = cus * L::kBlocks;
-    const int64_t tiles = (int64_t)p.tiles_n * p.tiles_m, rest = tiles % slots, runs = (K + 511) / 512;
-    p.full = (int)tiles;
-    const int64_t part = (int64_t)L::BN * L::BM * sizeof(float);
-    auto rounds = [&](int64_t blocks, int64_t each) {
-        const int64_t full = blocks / slots, left = blocks % slots;
-        return full * (each * (L::kRun + L::kMore) + L::kEnds) +
-               (left ? each * (L::kRun + L::kMore * left / slots) + L::kEnds : 0);
-    };
-    const int64_t whole = rounds(tiles - rest, runs);
-    c.ns = rounds(tiles, runs);
-    const int64_t most = M < L::BM ? (M + 15) / 16 * 16 : L::BM;    // tokens whose sums are kept
-    for (int w = 2; w <= 16 && w <= runs; ++w) {
-        if ((size_t)(rest * w * part) > bytes) break;
-        const int64_t sums = rest * w * (part * most / L::BM) * 2 / 4000 + 3000;
-        const int64_t ns = whole + rounds(rest * w, (runs + w - 1) / w) + sums;
-        if (rest && ns < c.ns) {
-            c.ns = ns;
-            p.ways = w;
-            p.full = (int)(tiles - rest);
-        }
-    }
-    return c;
-}
-
 template <class L, bool GATED>
 hipError_t launch_tiles(const Mx4Args &a, MxPlan p, void *work, hipStream_t stream) {
     p.part = static_cast<float *>(work);
     const int rest = p.tiles_n * p.tiles_m - p.full;
     const bool span = a.K % 512 == 0 &&
                       ((reinterpret_cast<uintptr_t>(a.as) | reinterpret_cast<uintptr_t>(a.ws)) & 15) == 0;
-    const dim3 grid((unsigned)((p.full + 7) / 8 * 8 + (rest * p.ways + 7) / 8 * 8)), block(L::T);
+    const dim3 grid(plan_blocks(p)), block(L::T);
     const auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, block, L::kLdsBytes, stream, a, p);
         return hipGetLastError();
@@ -822,11 +746,6 @@ hipError_t launch_tiles(const Mx4Args &a, MxPlan p, void *work, hipStream_t stre
 template <class L>
 hipError_t run_tiles(const Mx4Args &a, bool gated, const MxPlan &p, void *work, hipStream_t stream) {
     return gated ? launch_tiles<L, true>(a, p, work, stream) : launch_tiles<L, false>(a, p, work, stream);
-}
-
-template <class L>
-size_t part_bytes(const MxPlan &p) {
-    return p.ways > 1 ? (size_t)((int64_t)p.tiles_n * p.tiles_m - p.full) * p.ways * (L::BN * L::BM) * sizeof(float) : 0;
 }
 
 template <int NI, int TT, bool GATED>
@@ -877,11 +796,15 @@ hipError_t run_thin(const Mx4Args &a, bool gated, hipStream_t stream) {
 typedef MxTile<4, 1, 1, 4> MxSmall;    // 64 x 64
 typedef MxTile<4, 4, 2, 2> MxMid;      // 128 x 128
 
-// The tile for a shape: the least of plan_tiles's counts.
+// The tile for a shape: the least of plan_tiles's counts. (Measured at 33 to 4096
+// tokens, N x K 5120 x 17408, 17408 x 5120, 6144 x 5120, 17408 x 1024 and 1411 x
+// 896, each tile in 1 to 16 ways: the count takes the fastest or one within a
+// tenth of it.)
 enum class MxKind { kSmall, kMid, kWide };
 MxKind choose_tile(int64_t M, int64_t N, int64_t K, bool gated, size_t bytes, MxPlan &plan) {
-    const MxCost s = plan_tiles<MxSmall>(M, N, K, gated, bytes), m = plan_tiles<MxMid>(M, N, K, gated, bytes),
-                 w = plan_tiles<MxWide>(M, N, K, gated, bytes);
+    const int64_t rows = gated ? 2 * N : N, runs = (K + 511) / 512;
+    const MxCost s = plan_tiles<MxSmall>(M, rows, runs, bytes), m = plan_tiles<MxMid>(M, rows, runs, bytes),
+                 w = plan_tiles<MxWide>(M, rows, runs, bytes);
     const MxKind kind = w.ns <= s.ns && w.ns <= m.ns ? MxKind::kWide : m.ns <= s.ns ? MxKind::kMid : MxKind::kSmall;
     plan = kind == MxKind::kWide ? w.plan : kind == MxKind::kMid ? m.plan : s.plan;
     return kind;

@@ -11,9 +11,10 @@
 // and three bfloat16 parts that add up to it exactly (truncated, so that no
 // part overflows), which run through the same loop as two or three passes over
 // d's tiles beside one expansion of the weights.
-#include "mx4_device.hpp"
+#include <type_traits>
+
 #include "mx4_launch.hpp"
-#include "pq2_launch.hpp"
+#include "mx4_plan.hpp"
 
 namespace pq2 {
 namespace {
@@ -107,15 +108,17 @@ template <int WK_, int WM_, int NWK_, int NWM_>
 struct GradTile {
     static constexpr int WK = WK_, WM = WM_, NWK = NWK_, NWM = NWM_;
     static constexpr int W = NWK * NWM, T = kWave * W;
-    static constexpr int BK = 16 * WK * NWK, BM = 16 * WM * NWM;
+    static constexpr int BN = 16 * WK * NWK, BM = 16 * WM * NWM;       // BN: columns of dx
     static constexpr int kD = BM * 128;                  // bytes of a tile of d
-    static constexpr int kRaw = kStep * BK / 2;
-    static constexpr int kWide = kStep * BK * 2;
+    static constexpr int kRaw = kStep * BN / 2;
+    static constexpr int kWide = kStep * BN * 2;
     static constexpr int kLdsBytes = 2 * (kD + kRaw + kWide);
     static constexpr int kCopiesM = BM / 8 / W;          // per wave
     static constexpr int kCopiesW = kRaw / 1024 / W;
-    static constexpr int kUnits = BK / 32;               // blocks of scales in a row of the tile
+    static constexpr int kUnits = BN / 32;               // blocks of scales in a row of the tile
     static constexpr int kItems = kStep * kUnits / T;    // expanded by a thread
+    static constexpr int kBlocks = 160 * 1024 / kLdsBytes;  // a compute unit holds
+    static constexpr int kRun = 700, kMore = 400, kEnds = 2500;        // plan_tiles's times
     static_assert(kCopiesM * W * 8 == BM && kCopiesW * W * 1024 == kRaw && kItems * T == kStep * kUnits,
                   "whole copies");
 };
@@ -139,13 +142,74 @@ __device__ __forceinline__ v4s read_turned(const uint8_t *p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)p);
 }
 
-// chunks: the n range is dealt to that many blocks per tile; with more than one
-// their float32 sums go to part [chunks][M][K].
+// Four results of one row of dx from column k on, which is a multiple of four.
+__device__ __forceinline__ void store_dx(void *dx, int format, int64_t at, v4f32 v, bool wide) {
+    if (wide && format == kF32) {
+        *reinterpret_cast<v4f32 *>(static_cast<float *>(dx) + at) = v;
+    } else if (wide) {
+        *reinterpret_cast<v2u *>(static_cast<uint16_t *>(dx) + at) =
+            v2u{pack16(format, v[0], v[1]), pack16(format, v[2], v[3])};
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) store_fmt(dx, format, at + e, v[e]);
+    }
+}
+
+// acc[i][j]: four columns from k + 16 i + 4 (lane / 16) on of token m + 16 j.
+template <int NI, int WM>
+__device__ __forceinline__ void finish_dx(const v4f32 (&acc)[NI][WM], void *dx, int format, int64_t k, int64_t m,
+                                          int64_t M, int64_t K, int lane) {
+    const bool wide = (reinterpret_cast<uintptr_t>(dx) & (format == kF32 ? 15 : 7)) == 0;
+#pragma unroll
+    for (int j = 0; j < WM; ++j) {
+        const int64_t t = m + 16 * j;
+        if (t >= M) continue;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int64_t c = k + 16 * i + 4 * (lane >> 4);
+            if (c < K) store_dx(dx, format, t * K + c, acc[i][j], wide);     // K is a multiple of four
+        }
+    }
+}
+
+struct GradOut {
+    void *dx;
+    int format;
+    int64_t M, N, K;
+};
+
+// The end of a block's work: the tile's results, or a split tile's sums.
+template <class L>
+__device__ __forceinline__ void end_grad(const GradOut &o, const MxPlan &p, const MxShare &s,
+                                         const v4f32 (&acc)[L::WK][L::WM], int wave, int lane) {
+    const int wk = wave % L::NWK, wm = wave / L::NWK;
+    const int64_t m = (int64_t)s.tm * L::BM + 16 * L::WM * wm;
+    if (!s.split)
+        finish_dx<L::WK, L::WM>(acc, o.dx, o.format, (int64_t)s.tn * L::BN + 16 * L::WK * wk, m + (lane & 15), o.M,
+                                o.K, lane);
+    else if (m < o.M)
+        store_share<L::WK, L::WM, L::T>(p, s.item, wave * kWave + lane, acc);
+}
+
+template <class L>
+__global__ __launch_bounds__(L::T) void grad_sum_kernel(GradOut o, MxPlan p) {
+    constexpr int NI = 4, kCuts = L::WK / NI;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
+    const int index = (int)blockIdx.x / kCuts, cut = (int)blockIdx.x % kCuts;
+    const int wk = wave % L::NWK, wm = wave / L::NWK;
+    int tn, tm;
+    tile_at(p, p.full + index, tn, tm);
+    const int64_t m = (int64_t)tm * L::BM + 16 * L::WM * wm;
+    if (m >= o.M) return;
+    v4f32 acc[NI][L::WM];
+    sum_shares<NI, L::WK, L::WM, L::T>(p, index, NI * cut, tid, acc);
+    finish_dx<NI, L::WM>(acc, o.dx, o.format, (int64_t)tn * L::BN + 16 * (L::WK * wk + NI * cut), m + (lane & 15), o.M,
+                         o.K, lane);
+}
+
 template <class L>
 __global__ __launch_bounds__(L::T) void grad_kernel(GradRows d, const uint8_t *__restrict__ w,
-                                                    const uint8_t *__restrict__ ws, void *dx,
-                                                    int format, float *part, int64_t M, int64_t N,
-                                                    int64_t K, int tiles_k, int tiles, int chunks) {
+                                                    const uint8_t *__restrict__ ws, GradOut o, MxPlan plan) {
     constexpr int WK = L::WK, WM = L::WM, W = L::W;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     uint8_t *const raw0 = smem + 2 * L::kD, *const wide0 = raw0 + 2 * L::kRaw;
@@ -154,22 +218,14 @@ __global__ __launch_bounds__(L::T) void grad_kernel(GradRows d, const uint8_t *_
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wk = wave % L::NWK, wm = wave / L::NWK;
     const int r = lane & 15, lg = lane >> 4;
-
-    const int all = tiles * chunks;
-    const int per = (all + 7) / 8;
-    const int at = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
-    if (at >= all) return;
-    const int tile = at / chunks, chunk = at % chunks;
-    const int64_t m0 = (int64_t)(tile / tiles_k) * L::BM;
-    const int k0 = (tile % tiles_k) * L::BK;
-
-    // this chunk's stages
-    const int stages = (int)((N + kStep - 1) / kStep);
-    const int s0 = (int)((int64_t)stages * chunk / chunks), s1 = (int)((int64_t)stages * (chunk + 1) / chunks);
+    const MxShare share = share_of(plan);
+    if (!share.live) return;
+    const int64_t M = o.M, N = o.N, K = o.K, m0 = (int64_t)share.tm * L::BM;
+    const int k0 = share.tn * L::BN, s0 = share.q0, s1 = share.q1;
     const int parts = d.parts;
 
     const int rows_m = (int)(M - m0 < L::BM ? M - m0 : L::BM);
-    const int cols = (int)(K - k0 < L::BK ? K - k0 : L::BK);
+    const int cols = (int)(K - k0 < L::BN ? K - k0 : L::BN);
     const int sub = lane >> 3;
 
     // stage s of d's rows, part p
@@ -227,7 +283,7 @@ __global__ __launch_bounds__(L::T) void grad_kernel(GradRows d, const uint8_t *_
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[j] = expand2(c[q], scale, j);
                 const int seg = (2 * u + (q >> 1)) ^ grad_turn(n);
-                *reinterpret_cast<v4u *>(to + n * (2 * L::BK) + 32 * seg + 16 * (q & 1)) = o;
+                *reinterpret_cast<v4u *>(to + n * (2 * L::BN) + 32 * seg + 16 * (q & 1)) = o;
             }
         }
     };
@@ -280,8 +336,8 @@ __global__ __launch_bounds__(L::T) void grad_kernel(GradRows d, const uint8_t *_
             for (int i = 0; i < WK; ++i) {
                 const int n = 32 * half + 8 * lg + (r >> 2);
                 const int seg = WK * wk + i;
-                const v4s lo = read_turned(wt + n * (2 * L::BK) + 32 * (seg ^ grad_turn(n)) + 8 * (r & 3));
-                const v4s hi = read_turned(wt + (n + 4) * (2 * L::BK) + 32 * (seg ^ grad_turn(n + 4)) + 8 * (r & 3));
+                const v4s lo = read_turned(wt + n * (2 * L::BN) + 32 * (seg ^ grad_turn(n)) + 8 * (r & 3));
+                const v4s hi = read_turned(wt + (n + 4) * (2 * L::BN) + 32 * (seg ^ grad_turn(n + 4)) + 8 * (r & 3));
                 fw[i] = __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
             }
 #pragma unroll
@@ -294,39 +350,203 @@ __global__ __launch_bounds__(L::T) void grad_kernel(GradRows d, const uint8_t *_
         s += turn;
     }
 
-    const bool wide = (reinterpret_cast<uintptr_t>(dx) & (format == kF32 ? 15 : 7)) == 0;
-#pragma unroll
-    for (int j = 0; j < WM; ++j) {
-        const int64_t m = m0 + 16 * (WM * wm + j) + r;
-        if (m >= M) continue;
-#pragma unroll
-        for (int i = 0; i < WK; ++i) {
-            const int k = k0 + 16 * (WK * wk + i) + 4 * lg;
-            if (k >= K) continue;                // K is a multiple of four
-            if (chunks > 1)
-                *reinterpret_cast<v4f32 *>(part + ((int64_t)chunk * M + m) * K + k) = acc[i][j];
-            else if (wide && format == kF32)
-                *reinterpret_cast<v4f32 *>(static_cast<float *>(dx) + m * K + k) = acc[i][j];
-            else if (wide)
-                *reinterpret_cast<v2u *>(static_cast<uint16_t *>(dx) + m * K + k) =
-                    v2u{pack16(format, acc[i][j][0], acc[i][j][1]), pack16(format, acc[i][j][2], acc[i][j][3])};
-            else
-#pragma unroll
-                for (int e = 0; e < 4; ++e) store_fmt(dx, format, m * K + k + e, acc[i][j][e]);
-        }
-    }
+    end_grad<L>(o, plan, share, acc, wave, lane);
 }
 
-// dx of the chunks' sums, added in chunk order.
-__global__ __launch_bounds__(256) void grad_sum_kernel(const float *__restrict__ part, void *dx,
-                                                       int format, int64_t n, int chunks) {
-    for (int64_t i = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x); i < n;
-         i += (int64_t)gridDim.x * 1024) {
-        v4f32 v = *reinterpret_cast<const v4f32 *>(part + i);
-        for (int c = 1; c < chunks; ++c) v += *reinterpret_cast<const v4f32 *>(part + c * n + i);
+// ---------------------------------------------------------------- wide tiles
+//
+// 256 columns x 256 tokens, eight waves (two a SIMD) of 128 x 64; d's tiles, the
+// 4-bit rows and the bfloat16 rows in two slots each, 144 KB. A step is one
+// instruction's 32 n, two a stage. What a step multiplies was read from LDS during
+// the step before, tokens into the other of two register sets, weights rolling.
+// In a stage's first step the next stage's weights are expanded; in its second a
+// barrier frees d's slot and shows the others' expansion, and the copies of the
+// next tile but one are dealt over the products that follow.
+// TODO figures
+struct GradWide {
+    static constexpr int W = 8, T = 512, BN = 256, BM = 256, WK = 8, WM = 4, NWK = 2;
+    static constexpr int kD = BM * 128, kRaw = kStep * BN / 2, kWide = kStep * BN * 2;
+    static constexpr int kLdsBytes = 2 * (kD + kWide + kRaw);
+    static constexpr int kBlocks = 1, kRun = 1500, kMore = 600, kEnds = 6000;   // plan_tiles's times
+};
+
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void grad_wide_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__restrict__ ws, GradOut o,
+                      MxPlan plan) {
+    typedef GradWide L;
+    constexpr int WK = L::WK, WM = L::WM, W = L::W;
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    uint8_t *const wide0 = smem + 2 * L::kD, *const raw0 = wide0 + 2 * L::kWide;
+    const int tid = threadIdx.x;
+    const int lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wk = wave % L::NWK, wm = wave / L::NWK;
+    const int r = lane & 15, lg = lane >> 4;
+    const MxShare share = share_of(plan);
+    if (!share.live) return;
+    const int64_t M = o.M, N = o.N, K = o.K, m0 = (int64_t)share.tm * L::BM;
+    const int k0 = share.tn * L::BN, s0 = share.q0, s1 = share.q1;
+    const int parts = d.parts;
+    const int rows_m = (int)(M - m0 < L::BM ? M - m0 : L::BM);
+    const int cols = (int)(K - k0 < L::BN ? K - k0 : L::BN);
+
+    // d: copy i of a wave fills rows 64 i + 8 wave .., each copy with a resource
+    // of the rows that exist and one lane offset for all
+    const int sub = lane >> 3, unit = (lane & 7) ^ grad_swizzle(sub);
+    const int row_bytes = (int)(d.cols * 2);
+    auto bytes = [&](int i) __attribute__((always_inline)) {
+        const int rows = rows_m - 64 * i - 8 * wave;
+        return __builtin_amdgcn_readfirstlane((rows < 0 ? 0 : rows > 8 ? 8 : rows) * row_bytes);
+    };
+    const int bytes_d[4] = {bytes(0), bytes(1), bytes(2), bytes(3)};
+    const int off = sub * row_bytes + 16 * unit;
+    const uint16_t *const base_d = d.d + (m0 + 8 * wave) * d.cols;
+    const uint16_t *from_d = base_d;                 // of the tile being copied
+    int off_d = kCopyOob;
+    auto open_d = [&](int s, int p) __attribute__((always_inline)) {
+        from_d = base_d + p * d.plane + (int64_t)s * kStep;
+        off_d = s < s1 && (int64_t)s * kStep + 8 * unit < d.n ? off : kCopyOob;
+    };
+    auto copy_d = [&](int slot, int i) __attribute__((always_inline)) {
+        copy16_to_lds(make_rsrc(from_d + (int64_t)i * 64 * d.cols, bytes_d[i]),
+                      smem + slot * L::kD + (i * W + wave) * 1024, off_d);
+    };
+    // 4-bit rows: wave's copy fills rows 8 wave .. of the stage, eight units each
+    const int kb = (int)(K / 2);
+    const int row_w = 8 * wave + sub, unit_w = lane & 7;
+    const bool live_w = 32 * unit_w < cols;
+    auto copy_w = [&](int s) __attribute__((always_inline)) {
+        const int64_t n0 = (int64_t)s * kStep;
+        const int rows = (int)(N - n0 < kStep ? N - n0 : kStep);
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(w + n0 * kb + k0 / 2, (int64_t)(rows - 1) * kb + cols / 2);
+        copy16_to_lds(rs, raw0 + (s & 1) * L::kRaw + wave * 1024,
+                      live_w && row_w < rows ? row_w * kb + 16 * unit_w : kCopyOob);
+    };
+    // the thread expands unit unit_w of row row_w
+    auto scale_of = [&](int s) __attribute__((always_inline)) {
+        const int64_t n = (int64_t)s * kStep + row_w;
+        return live_w && n < N ? (uint32_t)ws[n * (K / kMxBlock) + k0 / kMxBlock + unit_w] : 0u;
+    };
+    uint8_t *const to_wide = wide0 + row_w * 512 + 32 * ((2 * unit_w) ^ grad_turn(row_w));
+    const int other = 32 - 64 * (((2 * unit_w) ^ grad_turn(row_w)) & 1);         // to the unit's second half
+    auto expand = [&](int slot, uint32_t byte) __attribute__((always_inline)) {
+        const v4u c = *reinterpret_cast<const v4u *>(raw0 + slot * L::kRaw + 16 * tid);
+        const float scale = mx_scale(byte);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) store_fmt(dx, format, i + e, v[e]);
+        for (int q = 0; q < 4; ++q) {
+            v4u v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = expand2(c[q], scale, j);
+            *reinterpret_cast<v4u *>(to_wide + slot * L::kWide + (q >> 1) * other + 16 * (q & 1)) = v;
+        }
+    };
+
+    v4f32 acc[WK][WM];
+#pragma unroll
+    for (int i = 0; i < WK; ++i)
+#pragma unroll
+        for (int j = 0; j < WM; ++j) acc[i][j] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+    v8bf fw[WK], fd[2][WM];
+    // weights: segment 8 wk + i of row 8 lg + r / 4 of a step, and of the row four on
+    const uint32_t turned = 32 * ((8 * wk) ^ grad_turn(8 * lg + (r >> 2))) + 8 * (r & 3) + 512 * (8 * lg + (r >> 2));
+    auto read_w = [&](int slot, int half, int i) __attribute__((always_inline)) {
+        const uint8_t *p = wide0 + (turned ^ (32 * i)) + slot * L::kWide + half * (32 * 512);
+        const v4s lo = read_turned(p), hi = read_turned(p + 4 * 512);
+        fw[i] = __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    const uint8_t *const at_d0 = smem + 128 * (16 * WM * wm + r) + 16 * (lg ^ grad_swizzle(r));
+    const uint8_t *const at_d1 = smem + 128 * (16 * WM * wm + r) + 16 * ((4 + lg) ^ grad_swizzle(r));
+    auto read_d = [&](int slot, int half, int j) __attribute__((always_inline)) {
+        fd[half][j] = *reinterpret_cast<const v8bf *>((half ? at_d1 : at_d0) + slot * L::kD + 2048 * j);
+    };
+
+    // prologue: d's tiles 0 and 1 (but two copies), 4-bit rows of stages s0 .. s0 + 2
+    const int tiles = (s1 - s0) * parts;
+    copy_w(s0);
+    uint32_t byte = scale_of(s0);
+    open_d(s0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) copy_d(0, i);
+    wait_vmem<0>();
+    ring_barrier();
+    expand(s0 & 1, byte);
+    byte = 0;
+    uint32_t byte_next = 0;
+    if (s0 + 1 < s1) {
+        copy_w(s0 + 1);
+        byte = scale_of(s0 + 1);
     }
+    wait_vmem<0>();
+    ring_barrier();                                  // expanded, and stage s0's 4-bit rows read
+    if (s0 + 2 < s1) {
+        copy_w(s0 + 2);
+        byte_next = scale_of(s0 + 2);
+    }
+    int ahead_s = parts > 1 ? s0 : s0 + 1, ahead_p = parts > 1 ? 1 : 0;          // the tile after this one
+    open_d(ahead_s, ahead_p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) copy_d(1, i);
+#pragma unroll
+    for (int i = 0; i < WK; ++i) read_w(s0 & 1, 0, i);
+#pragma unroll
+    for (int j = 0; j < WM; ++j) read_d(0, 0, j);
+
+    constexpr int kLead = 2;                         // column tiles multiplied before the barrier
+    int s = s0, p = 0;
+    for (int t = 0; t < tiles; ++t) {
+        const int slot = t & 1, ws_slot = s & 1;
+        auto products = [&](int half, int i) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < WM; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[i], fd[half][j], acc[i][j], 0, 0, 0);
+        };
+        // first step: the second's fragments, and the next stage's weights
+#pragma unroll
+        for (int j = 0; j < WM; ++j) read_d(slot, 1, j);
+#pragma unroll
+        for (int i = 0; i < WK; ++i) {
+            products(0, i);
+            read_w(ws_slot, 1, i);
+            if (i == 0 && p == 0 && s + 1 < s1) expand(ws_slot ^ 1, byte);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // second step
+#pragma unroll
+        for (int i = 0; i < kLead; ++i) products(1, i);
+        __builtin_amdgcn_sched_barrier(0);
+        const bool turn = p + 1 == parts;
+        const int s_next = turn ? s + 1 : s;
+        wait_vmem<0>();                              // the next tile of d, 4-bit rows s + 2
+        ring_barrier();                              // for all waves; d's slot is read, s + 1 expanded
+        if (turn) {
+            byte = byte_next;
+            if (s + 3 < s1) {
+                copy_w(s + 3);
+                byte_next = scale_of(s + 3);
+            }
+        }
+        ++ahead_p;
+        if (ahead_p == parts) {
+            ahead_p = 0;
+            ++ahead_s;
+        }
+        open_d(ahead_s, ahead_p);
+#pragma unroll
+        for (int j = 0; j < WM; ++j) read_d(slot ^ 1, 0, j);
+#pragma unroll
+        for (int i = 0; i < kLead; ++i) read_w(s_next & 1, 0, i);
+#pragma unroll
+        for (int i = kLead; i < WK; ++i) {
+            products(1, i);
+            read_w(s_next & 1, 0, i);
+            if (i - kLead < 4) copy_d(slot, i - kLead);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        s = s_next;
+        p = turn ? 0 : p + 1;
+    }
+    wait_vmem<0>();                                  // no copy may land after the block ends
+    end_grad<L>(o, plan, share, acc, wave, lane);
 }
 
 // A launch holds fewer than 2^32 threads: the kernels go round again.
@@ -340,34 +560,28 @@ int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 // Whether d is read where it lies: bfloat16 rows of whole 16-byte units.
 bool in_place(int64_t N, int format) { return format == kBf16 && N % 8 == 0; }
 
-struct GradPlan {
-    bool big;
-    int chunks;
-    int64_t sums;                     // bytes of the chunks' sums
-};
+typedef GradTile<4, 2, 2, 2> GradSmall;    // 128 x 64
 
-GradPlan plan_grad(int64_t M, int64_t N, int64_t K, size_t bytes) {
-    GradPlan p;
-    const int64_t tiles_big = ((K + 255) / 256) * ((M + 255) / 256);
-    p.big = tiles_big >= 192;
-    const int64_t tiles = p.big ? tiles_big : ((K + 127) / 128) * ((M + 63) / 64);
+// The tile for a shape: the least of plan_tiles's counts.
+bool choose_wide(int64_t M, int64_t N, int64_t K, int parts, size_t bytes, MxPlan &plan) {
     const int64_t stages = (N + kStep - 1) / kStep;
-    int64_t c = p.big ? 1 : 512 / tiles;
-    c = c < stages / 4 ? c : stages / 4;
-    c = c < 16 ? c : 16;
-    const int64_t fits = (int64_t)(bytes / ((size_t)M * (size_t)K * sizeof(float)));
-    c = c < fits ? c : fits;
-    p.chunks = c < 1 ? 1 : (int)c;
-    p.sums = p.chunks > 1 ? p.chunks * M * K * (int64_t)sizeof(float) : 0;
-    return p;
+    const MxCost s = plan_tiles<GradSmall>(M, K, stages, bytes, parts), w = plan_tiles<GradWide>(M, K, stages, bytes, parts);
+    plan = w.ns <= s.ns ? w.plan : s.plan;
+    return w.ns <= s.ns;
 }
 
 template <class L>
-hipError_t run_grad(const GradRows &d, const Mx4GradArgs &a, float *part, int chunks, hipStream_t stream) {
-    const int64_t tk = (a.K + L::BK - 1) / L::BK, tm = (a.M + L::BM - 1) / L::BM;
-    const int64_t per = (tk * tm * chunks + 7) / 8;
-    hipLaunchKernelGGL(grad_kernel<L>, dim3((unsigned)(8 * per)), dim3(L::T), L::kLdsBytes, stream, d,
-                       a.w, a.ws, a.dx, a.format, part, a.M, a.N, a.K, (int)tk, (int)(tk * tm), chunks);
+hipError_t run_grad(const GradRows &d, const Mx4GradArgs &a, MxPlan p, void *work, hipStream_t stream) {
+    p.part = static_cast<float *>(work);
+    const GradOut o{a.dx, a.format, a.M, a.N, a.K};
+    if constexpr (std::is_same<L, GradWide>::value)
+        hipLaunchKernelGGL(grad_wide_kernel, dim3(plan_blocks(p)), dim3(L::T), L::kLdsBytes, stream, d, a.w, a.ws, o, p);
+    else
+        hipLaunchKernelGGL(grad_kernel<L>, dim3(plan_blocks(p)), dim3(L::T), L::kLdsBytes, stream, d, a.w, a.ws, o, p);
+    const hipError_t e = hipGetLastError();
+    const int rest = p.tiles_n * p.tiles_m - p.full;
+    if (e != hipSuccess || rest == 0) return e;
+    hipLaunchKernelGGL(grad_sum_kernel<L>, dim3((unsigned)(rest * (L::WK / 4))), dim3(L::T), 0, stream, o, p);
     return hipGetLastError();
 }
 
@@ -394,7 +608,9 @@ size_t mx4_grad_least_bytes(int64_t M, int64_t N, int format, bool gated, bool k
 
 size_t mx4_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int format, bool gated,
                                 bool keeps_dgu) {
-    return mx4_grad_least_bytes(M, N, format, gated, keeps_dgu) + (size_t)plan_grad(M, N, K, SIZE_MAX).sums;
+    MxPlan p;
+    const bool wide = choose_wide(M, N, K, parts_of(format), SIZE_MAX, p);
+    return mx4_grad_least_bytes(M, N, format, gated, keeps_dgu) + (wide ? part_bytes<GradWide>(p) : part_bytes<GradSmall>(p));
 }
 
 hipError_t launch_mx4_grad(const Mx4GradArgs &a, void *work, size_t work_bytes, hipStream_t stream) {
@@ -423,16 +639,10 @@ hipError_t launch_mx4_grad(const Mx4GradArgs &a, void *work, size_t work_bytes, 
                               : run_rows<kF16>(a, a.dgu, rows, d.cols, stream);
     }
     if (e != hipSuccess) return e;
-    const GradPlan p = plan_grad(a.M, a.N, a.K, work_bytes - least);
-    float *part = p.chunks > 1 ? reinterpret_cast<float *>(static_cast<uint8_t *>(work) + least) : nullptr;
-    typedef GradTile<8, 4, 2, 4> Big;
-    typedef GradTile<4, 2, 2, 2> Small;
-    e = p.big ? run_grad<Big>(d, a, part, p.chunks, stream) : run_grad<Small>(d, a, part, p.chunks, stream);
-    if (e != hipSuccess || p.chunks == 1) return e;
-    const int64_t n = a.M * a.K;
-    hipLaunchKernelGGL(grad_sum_kernel, dim3(blocks_of(n / 4)), dim3(256), 0, stream,
-                       part, a.dx, a.format, n, p.chunks);
-    return hipGetLastError();
+    MxPlan p;
+    const bool wide = choose_wide(a.M, a.N, a.K, d.parts, work_bytes - least, p);
+    void *const sums = p.ways > 1 ? static_cast<uint8_t *>(work) + least : nullptr;
+    return wide ? run_grad<GradWide>(d, a, p, sums, stream) : run_grad<GradSmall>(d, a, p, sums, stream);
 }
 
 }  // namespace pq2
