@@ -11,8 +11,6 @@
 // and three bfloat16 parts that add up to it exactly (truncated, so that no
 // part overflows), which run through the same loop as two or three passes over
 // d's tiles beside one expansion of the weights.
-#include <type_traits>
-
 #include "mx4_launch.hpp"
 #include "mx4_plan.hpp"
 
@@ -96,31 +94,37 @@ __global__ __launch_bounds__(256) void grad_rows_kernel(const void *dy, const vo
 
 // ---------------------------------------------------------------- product
 //
-// A block owns BK columns of dx x BM tokens. Stage s covers 64 n: d's tile (one
-// part) and the weights' 4-bit rows come by buffer -> LDS copies, and while
-// stage s is multiplied the weights of stage s + 1 are expanded into the other
-// of two bfloat16 tiles, rows n of BK values. The instruction wants, for a
-// column k, eight consecutive n: the transposing LDS read takes them out of
-// four rows at a time. The 32-byte segment of 16 columns seg of row n lies at
-// place seg ^ turn(n), so that the four (and eight) rows of such a read are in
-// different banks.
+// A block owns BN columns of dx x BM tokens, NWK x NWM waves of WK x WM
+// instruction tiles. A stage is 64 n of one part of d: d's tile and the weights
+// as bfloat16, rows n of BN values, in two LDS slots each. Both come through
+// registers, loaded a stage before they are stored: a thread expands 32 values
+// under one scale (sixteen conversions) while others multiply. (Buffer -> LDS
+// copies do not go with the transposing LDS reads: the compiler waits for every
+// copy in flight before such a read; 4096 x 5120 x 17408 in 1009 us instead of
+// TODO.) The instruction wants, for a column k, eight consecutive n: the
+// transposing read takes them out of four rows at a time. The 32-byte segment seg
+// of row n lies at place seg ^ turn(n), so that the four (and eight) rows of such a
+// read are in different banks.
+// A step is one instruction's 32 n, two a stage. What a step multiplies was read
+// from LDS during the step before, tokens into the other of two register sets,
+// weights rolling, each tile's registers taking the next step's as soon as its
+// products are issued. In the first step of a stage the next stage's tile is
+// stored and the one after requested; a barrier in the second shows it to all.
+// TODO figures
 template <int WK_, int WM_, int NWK_, int NWM_>
 struct GradTile {
     static constexpr int WK = WK_, WM = WM_, NWK = NWK_, NWM = NWM_;
     static constexpr int W = NWK * NWM, T = kWave * W;
-    static constexpr int BN = 16 * WK * NWK, BM = 16 * WM * NWM;       // BN: columns of dx
+    static constexpr int BN = 16 * WK * NWK, BM = 16 * WM * NWM;
     static constexpr int kD = BM * 128;                  // bytes of a tile of d
-    static constexpr int kRaw = kStep * BN / 2;
     static constexpr int kWide = kStep * BN * 2;
-    static constexpr int kLdsBytes = 2 * (kD + kRaw + kWide);
-    static constexpr int kCopiesM = BM / 8 / W;          // per wave
-    static constexpr int kCopiesW = kRaw / 1024 / W;
+    static constexpr int kLdsBytes = 2 * (kD + kWide);
+    static constexpr int kRows = BM / 8 / W;             // 16-byte pieces of d's tile a thread moves
     static constexpr int kUnits = BN / 32;               // blocks of scales in a row of the tile
-    static constexpr int kItems = kStep * kUnits / T;    // expanded by a thread
-    static constexpr int kBlocks = 160 * 1024 / kLdsBytes;  // a compute unit holds
-    static constexpr int kRun = 700, kMore = 400, kEnds = 2500;        // plan_tiles's times
-    static_assert(kCopiesM * W * 8 == BM && kCopiesW * W * 1024 == kRaw && kItems * T == kStep * kUnits,
-                  "whole copies");
+    static constexpr int kBlocks = BN == 256 ? 1 : 3;    // a compute unit holds
+    static constexpr int kRun = BN == 256 ? 1500 : 700, kMore = BN == 256 ? 600 : 400,
+                         kEnds = BN == 256 ? 6000 : 2500;               // plan_tiles's times
+    static_assert(kRows * W * 8 == BM && kStep * kUnits == T, "a thread expands one block");
 };
 
 __device__ __forceinline__ int grad_turn(int n) { return (n & 3) | (((n >> 3) & 1) << 2); }
@@ -208,175 +212,11 @@ __global__ __launch_bounds__(L::T) void grad_sum_kernel(GradOut o, MxPlan p) {
 }
 
 template <class L>
-__global__ __launch_bounds__(L::T) void grad_kernel(GradRows d, const uint8_t *__restrict__ w,
-                                                    const uint8_t *__restrict__ ws, GradOut o, MxPlan plan) {
-    constexpr int WK = L::WK, WM = L::WM, W = L::W;
+__global__ __launch_bounds__(L::T) __attribute__((amdgpu_waves_per_eu(2)))
+void grad_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__restrict__ ws, GradOut o, MxPlan plan) {
+    constexpr int WK = L::WK, WM = L::WM, W = L::W, NR = L::kRows;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    uint8_t *const raw0 = smem + 2 * L::kD, *const wide0 = raw0 + 2 * L::kRaw;
-    const int tid = threadIdx.x;
-    const int lane = tid & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wk = wave % L::NWK, wm = wave / L::NWK;
-    const int r = lane & 15, lg = lane >> 4;
-    const MxShare share = share_of(plan);
-    if (!share.live) return;
-    const int64_t M = o.M, N = o.N, K = o.K, m0 = (int64_t)share.tm * L::BM;
-    const int k0 = share.tn * L::BN, s0 = share.q0, s1 = share.q1;
-    const int parts = d.parts;
-
-    const int rows_m = (int)(M - m0 < L::BM ? M - m0 : L::BM);
-    const int cols = (int)(K - k0 < L::BN ? K - k0 : L::BN);
-    const int sub = lane >> 3;
-
-    // stage s of d's rows, part p
-    auto issue_d = [&](int s, int p, int slot) __attribute__((always_inline)) {
-        const __amdgpu_buffer_rsrc_t rs =
-            make_rsrc(d.d + p * d.plane + m0 * d.cols + (int64_t)s * kStep,
-                      ((int64_t)(rows_m - 1) * d.cols + kStep) * 2);
-        uint8_t *to = smem + slot * L::kD;
-        const int64_t left = d.n - (int64_t)s * kStep;           // columns that exist from here on
-#pragma unroll
-        for (int i = 0; i < L::kCopiesM; ++i) {
-            const int row = 8 * (i * W + wave) + sub;
-            const int unit = (lane & 7) ^ grad_swizzle(row);
-            const bool live = row < rows_m && 8 * unit < left;
-            copy16_to_lds(rs, to + (i * W + wave) * 1024,
-                          live ? (int)(row * d.cols * 2) + 16 * unit : kCopyOob);
-        }
-    };
-    // 4-bit rows n of stage s, unit u (32 columns) of row n at place u
-    auto issue_w = [&](int s) __attribute__((always_inline)) {
-        const int64_t n0 = (int64_t)s * kStep;
-        const int rows = (int)(N - n0 < kStep ? N - n0 : kStep);
-        const __amdgpu_buffer_rsrc_t rs = make_rsrc(w + (n0 * K + k0) / 2, ((int64_t)(rows - 1) * K + cols) / 2);
-        uint8_t *to = raw0 + (s & 1) * L::kRaw;
-#pragma unroll
-        for (int i = 0; i < L::kCopiesW; ++i) {
-            const int item = (i * W + wave) * 64 + lane;
-            const int row = item / L::kUnits, u = item % L::kUnits;
-            const bool live = row < rows && 32 * u < cols;
-            copy16_to_lds(rs, to + (i * W + wave) * 1024, live ? (int)(row * (K / 2)) + 16 * u : kCopyOob);
-        }
-    };
-    uint32_t scale_byte[L::kItems];
-    auto load_scales = [&](int s) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < L::kItems; ++i) {
-            const int item = i * L::T + tid;
-            const int64_t n = (int64_t)s * kStep + item / L::kUnits;
-            const int u = item % L::kUnits;
-            scale_byte[i] = n < N && 32 * u < cols ? ws[n * (K / kMxBlock) + k0 / kMxBlock + u] : 0u;
-        }
-    };
-    auto expand = [&](int s) __attribute__((always_inline)) {
-        const uint8_t *from = raw0 + (s & 1) * L::kRaw;
-        uint8_t *to = wide0 + (s & 1) * L::kWide;
-#pragma unroll
-        for (int i = 0; i < L::kItems; ++i) {
-            const int item = i * L::T + tid;
-            const int n = item / L::kUnits, u = item % L::kUnits;
-            const v4u c = *reinterpret_cast<const v4u *>(from + 16 * item);
-            const float scale = mx_scale(scale_byte[i]);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                v4u o;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[j] = expand2(c[q], scale, j);
-                const int seg = (2 * u + (q >> 1)) ^ grad_turn(n);
-                *reinterpret_cast<v4u *>(to + n * (2 * L::BN) + 32 * seg + 16 * (q & 1)) = o;
-            }
-        }
-    };
-
-    v4f32 acc[WK][WM];
-#pragma unroll
-    for (int i = 0; i < WK; ++i)
-#pragma unroll
-        for (int j = 0; j < WM; ++j) acc[i][j] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
-
-    if (s0 < s1) {
-        issue_w(s0);
-        load_scales(s0);
-        issue_d(s0, 0, 0);
-        wait_vmem<0>();
-        ring_barrier();
-        expand(s0);
-        if (s0 + 1 < s1) {
-            issue_w(s0 + 1);
-            load_scales(s0 + 1);
-        }
-    }
-    for (int s = s0, p = 0, slot = 0; s < s1; slot ^= 1) {
-        wait_vmem<0>();
-        ring_barrier();                  // d's tile, the 4-bit rows s + 1, the bfloat16 rows s
-        const bool turn = p + 1 == parts;
-        if (!turn)
-            issue_d(s, p + 1, slot ^ 1);
-        else if (s + 1 < s1)
-            issue_d(s + 1, 0, slot ^ 1);
-        if (p == 0 && s + 1 < s1) {
-            // the 4-bit rows' other slot was read a stage ago
-            expand(s + 1);
-            if (s + 2 < s1) {
-                issue_w(s + 2);
-                load_scales(s + 2);
-            }
-        }
-        const uint8_t *dt = smem + slot * L::kD;
-        const uint8_t *wt = wide0 + (s & 1) * L::kWide;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            v8bf fw[WK], fd[WM];
-#pragma unroll
-            for (int j = 0; j < WM; ++j) {
-                const int row = 16 * (WM * wm + j) + r;
-                fd[j] = *reinterpret_cast<const v8bf *>(dt + 128 * row + 16 * ((4 * half + lg) ^ grad_swizzle(r)));
-            }
-#pragma unroll
-            for (int i = 0; i < WK; ++i) {
-                const int n = 32 * half + 8 * lg + (r >> 2);
-                const int seg = WK * wk + i;
-                const v4s lo = read_turned(wt + n * (2 * L::BN) + 32 * (seg ^ grad_turn(n)) + 8 * (r & 3));
-                const v4s hi = read_turned(wt + (n + 4) * (2 * L::BN) + 32 * (seg ^ grad_turn(n + 4)) + 8 * (r & 3));
-                fw[i] = __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-            }
-#pragma unroll
-            for (int i = 0; i < WK; ++i)
-#pragma unroll
-                for (int j = 0; j < WM; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[i], fd[j], acc[i][j], 0, 0, 0);
-        }
-        p = turn ? 0 : p + 1;
-        s += turn;
-    }
-
-    end_grad<L>(o, plan, share, acc, wave, lane);
-}
-
-// ---------------------------------------------------------------- wide tiles
-//
-// 256 columns x 256 tokens, eight waves (two a SIMD) of 128 x 64; d's tiles, the
-// 4-bit rows and the bfloat16 rows in two slots each, 144 KB. A step is one
-// instruction's 32 n, two a stage. What a step multiplies was read from LDS during
-// the step before, tokens into the other of two register sets, weights rolling.
-// In a stage's first step the next stage's weights are expanded; in its second a
-// barrier frees d's slot and shows the others' expansion, and the copies of the
-// next tile but one are dealt over the products that follow.
-// TODO figures
-struct GradWide {
-    static constexpr int W = 8, T = 512, BN = 256, BM = 256, WK = 8, WM = 4, NWK = 2;
-    static constexpr int kD = BM * 128, kRaw = kStep * BN / 2, kWide = kStep * BN * 2;
-    static constexpr int kLdsBytes = 2 * (kD + kWide + kRaw);
-    static constexpr int kBlocks = 1, kRun = 1500, kMore = 600, kEnds = 6000;   // plan_tiles's times
-};
-
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
-void grad_wide_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__restrict__ ws, GradOut o,
-                      MxPlan plan) {
-    typedef GradWide L;
-    constexpr int WK = L::WK, WM = L::WM, W = L::W;
-    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    uint8_t *const wide0 = smem + 2 * L::kD, *const raw0 = wide0 + 2 * L::kWide;
+    uint8_t *const wide0 = smem + 2 * L::kD;
     const int tid = threadIdx.x;
     const int lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -390,53 +230,60 @@ void grad_wide_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *
     const int rows_m = (int)(M - m0 < L::BM ? M - m0 : L::BM);
     const int cols = (int)(K - k0 < L::BN ? K - k0 : L::BN);
 
-    // d: copy i of a wave fills rows 64 i + 8 wave .., each copy with a resource
-    // of the rows that exist and one lane offset for all
+    // d: piece i of a wave is rows 8 (i W + wave) .., each with a resource of the
+    // rows that exist and one lane offset for all
     const int sub = lane >> 3, unit = (lane & 7) ^ grad_swizzle(sub);
     const int row_bytes = (int)(d.cols * 2);
-    auto bytes = [&](int i) __attribute__((always_inline)) {
-        const int rows = rows_m - 64 * i - 8 * wave;
-        return __builtin_amdgcn_readfirstlane((rows < 0 ? 0 : rows > 8 ? 8 : rows) * row_bytes);
-    };
-    const int bytes_d[4] = {bytes(0), bytes(1), bytes(2), bytes(3)};
+    int bytes_d[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const int rows = rows_m - 8 * (i * W + wave);
+        bytes_d[i] = __builtin_amdgcn_readfirstlane((rows < 0 ? 0 : rows > 8 ? 8 : rows) * row_bytes);
+    }
     const int off = sub * row_bytes + 16 * unit;
     const uint16_t *const base_d = d.d + (m0 + 8 * wave) * d.cols;
-    const uint16_t *from_d = base_d;                 // of the tile being copied
-    int off_d = kCopyOob;
-    auto open_d = [&](int s, int p) __attribute__((always_inline)) {
-        from_d = base_d + p * d.plane + (int64_t)s * kStep;
-        off_d = s < s1 && (int64_t)s * kStep + 8 * unit < d.n ? off : kCopyOob;
+    v4u held[NR];                                    // the tile of d after the next
+    auto load_d = [&](int s, int p) __attribute__((always_inline)) {
+        const uint16_t *from = base_d + p * d.plane + (int64_t)s * kStep;
+        const int at = s < s1 && (int64_t)s * kStep + 8 * unit < d.n ? off : kCopyOob;
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+            held[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(
+                make_rsrc(from + (int64_t)i * (8 * W) * d.cols, bytes_d[i]), at, 0, 0));
     };
-    auto copy_d = [&](int slot, int i) __attribute__((always_inline)) {
-        copy16_to_lds(make_rsrc(from_d + (int64_t)i * 64 * d.cols, bytes_d[i]),
-                      smem + slot * L::kD + (i * W + wave) * 1024, off_d);
+    auto store_d = [&](int slot) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+            *reinterpret_cast<v4u *>(smem + slot * L::kD + (i * W + wave) * 1024 + 16 * lane) = held[i];
     };
-    // 4-bit rows: wave's copy fills rows 8 wave .. of the stage, eight units each
-    const int kb = (int)(K / 2);
-    const int row_w = 8 * wave + sub, unit_w = lane & 7;
+    // weights: the thread expands block unit_w of row row_w of a stage
+    const int kb = (int)(K / 2), row_w = tid / L::kUnits, unit_w = tid % L::kUnits;
     const bool live_w = 32 * unit_w < cols;
-    auto copy_w = [&](int s) __attribute__((always_inline)) {
+    v4u codes;
+    uint32_t byte;
+    auto load_w = [&](int s) __attribute__((always_inline)) {
         const int64_t n0 = (int64_t)s * kStep;
-        const int rows = (int)(N - n0 < kStep ? N - n0 : kStep);
-        const __amdgpu_buffer_rsrc_t rs = make_rsrc(w + n0 * kb + k0 / 2, (int64_t)(rows - 1) * kb + cols / 2);
-        copy16_to_lds(rs, raw0 + (s & 1) * L::kRaw + wave * 1024,
-                      live_w && row_w < rows ? row_w * kb + 16 * unit_w : kCopyOob);
+        const int rows = s < s1 ? (int)(N - n0 < kStep ? N - n0 : kStep) : 0;
+        const bool live = live_w && row_w < rows;
+        const int64_t first = rows ? n0 : 0;
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(w + first * kb + k0 / 2, rows ? (int64_t)(rows - 1) * kb + cols / 2 : 0);
+        codes = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(
+            rs, live ? row_w * kb + 16 * unit_w : kCopyOob, 0, 0));
+        const int sb = kb / 16;
+        const __amdgpu_buffer_rsrc_t rss =
+            make_rsrc(ws + first * sb + k0 / kMxBlock, rows ? (int64_t)(rows - 1) * sb + cols / kMxBlock : 0);
+        byte = __builtin_amdgcn_raw_buffer_load_b8(rss, live ? row_w * sb + unit_w : kCopyOob, 0, 0);
     };
-    // the thread expands unit unit_w of row row_w
-    auto scale_of = [&](int s) __attribute__((always_inline)) {
-        const int64_t n = (int64_t)s * kStep + row_w;
-        return live_w && n < N ? (uint32_t)ws[n * (K / kMxBlock) + k0 / kMxBlock + unit_w] : 0u;
-    };
-    uint8_t *const to_wide = wide0 + row_w * 512 + 32 * ((2 * unit_w) ^ grad_turn(row_w));
-    const int other = 32 - 64 * (((2 * unit_w) ^ grad_turn(row_w)) & 1);         // to the unit's second half
-    auto expand = [&](int slot, uint32_t byte) __attribute__((always_inline)) {
-        const v4u c = *reinterpret_cast<const v4u *>(raw0 + slot * L::kRaw + 16 * tid);
-        const float scale = mx_scale(byte);
+    const int place_w = (2 * unit_w) ^ grad_turn(row_w);
+    uint8_t *const to_wide = wide0 + row_w * (2 * L::BN) + 32 * place_w;
+    const int other = 32 - 64 * (place_w & 1);       // to the block's second half
+    auto expand = [&](int slot) __attribute__((always_inline)) {
+        const float scale = mx_scale(byte & 0xffu);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             v4u v;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = expand2(c[q], scale, j);
+            for (int j = 0; j < 4; ++j) v[j] = expand2(codes[q], scale, j);
             *reinterpret_cast<v4u *>(to_wide + slot * L::kWide + (q >> 1) * other + 16 * (q & 1)) = v;
         }
     };
@@ -447,11 +294,13 @@ void grad_wide_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *
 #pragma unroll
         for (int j = 0; j < WM; ++j) acc[i][j] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
     v8bf fw[WK], fd[2][WM];
-    // weights: segment 8 wk + i of row 8 lg + r / 4 of a step, and of the row four on
-    const uint32_t turned = 32 * ((8 * wk) ^ grad_turn(8 * lg + (r >> 2))) + 8 * (r & 3) + 512 * (8 * lg + (r >> 2));
+    // weights: segment WK wk + i of row 8 lg + r / 4 of a step, and of the row four
+    // on; WK wk + i and i differ in bits that turn() leaves alone or by an XOR too
+    const int row_t = 8 * lg + (r >> 2);
+    const uint32_t turned = 32 * ((WK * wk) ^ grad_turn(row_t)) + 8 * (r & 3) + 2 * L::BN * row_t;
     auto read_w = [&](int slot, int half, int i) __attribute__((always_inline)) {
-        const uint8_t *p = wide0 + (turned ^ (32 * i)) + slot * L::kWide + half * (32 * 512);
-        const v4s lo = read_turned(p), hi = read_turned(p + 4 * 512);
+        const uint8_t *p = wide0 + (turned ^ (32 * i)) + slot * L::kWide + half * (64 * L::BN);
+        const v4s lo = read_turned(p), hi = read_turned(p + 8 * L::BN);
         fw[i] = __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     };
     const uint8_t *const at_d0 = smem + 128 * (16 * WM * wm + r) + 16 * (lg ^ grad_swizzle(r));
@@ -460,92 +309,71 @@ void grad_wide_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *
         fd[half][j] = *reinterpret_cast<const v8bf *>((half ? at_d1 : at_d0) + slot * L::kD + 2048 * j);
     };
 
-    // prologue: d's tiles 0 and 1 (but two copies), 4-bit rows of stages s0 .. s0 + 2
-    const int tiles = (s1 - s0) * parts;
-    copy_w(s0);
-    uint32_t byte = scale_of(s0);
-    open_d(s0, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) copy_d(0, i);
-    wait_vmem<0>();
+    load_d(s0, 0);
+    load_w(s0);
+    store_d(0);
+    expand(s0 & 1);
+    int ahead_s = parts > 1 ? s0 : s0 + 1, ahead_p = parts > 1 ? 1 : 0;          // the tile that is held
+    load_d(ahead_s, ahead_p);
+    load_w(s0 + 1);
     ring_barrier();
-    expand(s0 & 1, byte);
-    byte = 0;
-    uint32_t byte_next = 0;
-    if (s0 + 1 < s1) {
-        copy_w(s0 + 1);
-        byte = scale_of(s0 + 1);
-    }
-    wait_vmem<0>();
-    ring_barrier();                                  // expanded, and stage s0's 4-bit rows read
-    if (s0 + 2 < s1) {
-        copy_w(s0 + 2);
-        byte_next = scale_of(s0 + 2);
-    }
-    int ahead_s = parts > 1 ? s0 : s0 + 1, ahead_p = parts > 1 ? 1 : 0;          // the tile after this one
-    open_d(ahead_s, ahead_p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) copy_d(1, i);
 #pragma unroll
     for (int i = 0; i < WK; ++i) read_w(s0 & 1, 0, i);
 #pragma unroll
     for (int j = 0; j < WM; ++j) read_d(0, 0, j);
 
-    constexpr int kLead = 2;                         // column tiles multiplied before the barrier
+    constexpr int kLead = WK / 4;                    // column tiles multiplied before the barrier
     int s = s0, p = 0;
-    for (int t = 0; t < tiles; ++t) {
-        const int slot = t & 1, ws_slot = s & 1;
+    for (int t = 0; s < s1; ++t) {
+        const int slot = t & 1, slot_w = s & 1;
         auto products = [&](int half, int i) __attribute__((always_inline)) {
 #pragma unroll
             for (int j = 0; j < WM; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[i], fd[half][j], acc[i][j], 0, 0, 0);
         };
-        // first step: the second's fragments, and the next stage's weights
+        // first step
 #pragma unroll
         for (int j = 0; j < WM; ++j) read_d(slot, 1, j);
 #pragma unroll
         for (int i = 0; i < WK; ++i) {
             products(0, i);
-            read_w(ws_slot, 1, i);
-            if (i == 0 && p == 0 && s + 1 < s1) expand(ws_slot ^ 1, byte);
+            read_w(slot_w, 1, i);
+            if (i == WK / 2 - 1) {
+                __builtin_amdgcn_sched_barrier(0);
+                store_d(slot ^ 1);
+                ++ahead_p;
+                if (ahead_p == parts) {
+                    ahead_p = 0;
+                    ++ahead_s;
+                }
+                load_d(ahead_s, ahead_p);
+                if (p == 0) {
+                    expand(slot_w ^ 1);
+                    load_w(s + 2);
+                }
+            }
         }
         __builtin_amdgcn_sched_barrier(0);
         // second step
 #pragma unroll
         for (int i = 0; i < kLead; ++i) products(1, i);
         __builtin_amdgcn_sched_barrier(0);
+        ring_barrier();                              // the next tile is there, this one is read
         const bool turn = p + 1 == parts;
-        const int s_next = turn ? s + 1 : s;
-        wait_vmem<0>();                              // the next tile of d, 4-bit rows s + 2
-        ring_barrier();                              // for all waves; d's slot is read, s + 1 expanded
-        if (turn) {
-            byte = byte_next;
-            if (s + 3 < s1) {
-                copy_w(s + 3);
-                byte_next = scale_of(s + 3);
-            }
-        }
-        ++ahead_p;
-        if (ahead_p == parts) {
-            ahead_p = 0;
-            ++ahead_s;
-        }
-        open_d(ahead_s, ahead_p);
+        const int next_w = (turn ? s + 1 : s) & 1;
 #pragma unroll
         for (int j = 0; j < WM; ++j) read_d(slot ^ 1, 0, j);
 #pragma unroll
-        for (int i = 0; i < kLead; ++i) read_w(s_next & 1, 0, i);
+        for (int i = 0; i < kLead; ++i) read_w(next_w, 0, i);
 #pragma unroll
         for (int i = kLead; i < WK; ++i) {
             products(1, i);
-            read_w(s_next & 1, 0, i);
-            if (i - kLead < 4) copy_d(slot, i - kLead);
+            read_w(next_w, 0, i);
         }
         __builtin_amdgcn_sched_barrier(0);
-        s = s_next;
+        s += turn;
         p = turn ? 0 : p + 1;
     }
-    wait_vmem<0>();                                  // no copy may land after the block ends
     end_grad<L>(o, plan, share, acc, wave, lane);
 }
 
@@ -560,6 +388,7 @@ int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 // Whether d is read where it lies: bfloat16 rows of whole 16-byte units.
 bool in_place(int64_t N, int format) { return format == kBf16 && N % 8 == 0; }
 
+typedef GradTile<8, 4, 2, 4> GradWide;     // 256 x 256
 typedef GradTile<4, 2, 2, 2> GradSmall;    // 128 x 64
 
 // The tile for a shape: the least of plan_tiles's counts.
@@ -574,10 +403,7 @@ template <class L>
 hipError_t run_grad(const GradRows &d, const Mx4GradArgs &a, MxPlan p, void *work, hipStream_t stream) {
     p.part = static_cast<float *>(work);
     const GradOut o{a.dx, a.format, a.M, a.N, a.K};
-    if constexpr (std::is_same<L, GradWide>::value)
-        hipLaunchKernelGGL(grad_wide_kernel, dim3(plan_blocks(p)), dim3(L::T), L::kLdsBytes, stream, d, a.w, a.ws, o, p);
-    else
-        hipLaunchKernelGGL(grad_kernel<L>, dim3(plan_blocks(p)), dim3(L::T), L::kLdsBytes, stream, d, a.w, a.ws, o, p);
+    hipLaunchKernelGGL(grad_kernel<L>, dim3(plan_blocks(p)), dim3(L::T), L::kLdsBytes, stream, d, a.w, a.ws, o, p);
     const hipError_t e = hipGetLastError();
     const int rest = p.tiles_n * p.tiles_m - p.full;
     if (e != hipSuccess || rest == 0) return e;
