@@ -109,12 +109,13 @@ __device__ __forceinline__ float gate_act(float g) {
 }
 
 // a(g) and a'(g).
-__device__ __forceinline__ void gate_act_slope(int act, float g, float &a, float &d) {
-    if (act == kSilu) {
+template <int ACT>
+__device__ __forceinline__ void gate_act_slope(float g, float &a, float &d) {
+    if constexpr (ACT == kSilu) {
         const float s = logistic(g);
         a = g * s;
         d = s + a * (1.0f - s);
-    } else if (act == kGelu) {
+    } else if constexpr (ACT == kGelu) {
         const float c = 0.5f * erfcf(-0.70710678118654752f * g);
         a = g * c;
         d = c + g * (0.3989422804014327f * expf(-0.5f * g * g));

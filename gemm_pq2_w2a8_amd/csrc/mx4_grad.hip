@@ -11,6 +11,8 @@
 // and three bfloat16 parts that add up to it exactly (truncated, so that no
 // part overflows), which run through the same loop as two or three passes over
 // d's tiles beside one expansion of the weights.
+#include <type_traits>
+
 #include "mx4_launch.hpp"
 #include "mx4_plan.hpp"
 
@@ -46,48 +48,122 @@ __device__ __forceinline__ uint16_t take_part(float &v) {
     return (uint16_t)(top >> 16);
 }
 
-__device__ __forceinline__ void store_parts(uint16_t *out, int64_t at, int64_t plane, int parts,
-                                            float v) {
-    if (parts == 1) {
-        out[at] = bf16_rne(v);                   // a bfloat16 value: exact
-        return;
+// V columns of one row of d as its parts, from element `at` of the first on.
+template <int V>
+__device__ __forceinline__ void store_parts(uint16_t *out, int64_t at, int64_t plane, int parts, float (&v)[V]) {
+    for (int p = 0; p < parts; ++p) {
+        uint16_t h[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) h[i] = parts == 1 ? bf16_rne(v[i]) : take_part(v[i]);   // one part: exact
+        uint16_t *to = out + at + p * plane;
+        if constexpr (V == 8) {
+            v4u o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = (uint32_t)h[2 * i] | ((uint32_t)h[2 * i + 1] << 16);
+            *reinterpret_cast<v4u *>(to) = o;
+        } else {
+            *to = h[0];
+        }
     }
-    for (int p = 0; p < parts; ++p) out[at + p * plane] = take_part(v);
 }
 
-// One thread per column of d (and of its padding). GATED: per column of dh,
-// whose two columns of dgu (dgu may be gu) and of the parts it writes.
-template <int FMT, bool GATED>
+// V values of a row (V = 8: from a 16-byte address on).
+template <int FMT, int V>
+__device__ __forceinline__ void load_values(const void *x, int64_t at, float (&v)[V]) {
+    typedef typename MxType<FMT>::T T;
+    const T *from = static_cast<const T *>(x) + at;
+    if constexpr (V == 1) {
+        v[0] = widen<FMT>(*from);
+    } else if constexpr (FMT == kF32) {
+        const v4f32 lo = *reinterpret_cast<const v4f32 *>(from), hi = *reinterpret_cast<const v4f32 *>(from + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = lo[i];
+            v[4 + i] = hi[i];
+        }
+    } else {
+        const v4u two = *reinterpret_cast<const v4u *>(from);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = widen<FMT>((uint16_t)(two[i] & 0xffffu));
+            v[2 * i + 1] = widen<FMT>((uint16_t)(two[i] >> 16));
+        }
+    }
+}
+
+// Rounds v to the format, and stores it where x is given.
+template <int FMT, int V>
+__device__ __forceinline__ void round_values(void *x, int64_t at, float (&v)[V]) {
+    typedef typename MxType<FMT>::T T;
+    T t[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        t[i] = narrow<FMT>(v[i]);
+        v[i] = widen<FMT>(t[i]);
+    }
+    if (!x) return;
+    T *to = static_cast<T *>(x) + at;
+    if constexpr (V == 1) {
+        *to = t[0];
+    } else if constexpr (FMT == kF32) {
+        *reinterpret_cast<v4f32 *>(to) = v4f32{t[0], t[1], t[2], t[3]};
+        *reinterpret_cast<v4f32 *>(to + 4) = v4f32{t[4], t[5], t[6], t[7]};
+    } else {
+        v4u o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = (uint32_t)t[2 * i] | ((uint32_t)t[2 * i + 1] << 16);
+        *reinterpret_cast<v4u *>(to) = o;
+    }
+}
+
+// What multiplies the weights: d's parts, for a gated block from dh, g and u, whose
+// dgu it writes too (dgu may be gu). V columns a thread: eight where rows of F
+// columns keep 16-byte addresses (2048 x 17408 bfloat16 116 us one by one, TODO by
+// eight); the columns behind d's last, up to a whole stage, are zeros.
+template <int FMT, bool GATED, int V>
 __global__ __launch_bounds__(256) void grad_rows_kernel(const void *dy, const void *gu, void *dgu,
                                                         int act, uint16_t *out, int64_t M,
                                                         int64_t N, int64_t cols, int parts) {
-    typedef typename MxType<FMT>::T T;
     const int64_t F = GATED ? N / 2 : N;         // columns of dy
-    const int64_t width = F + (out ? cols - N : 0);
+    const int64_t width = (F + (out ? cols - N : 0)) / V;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < M * width;
          i += (int64_t)gridDim.x * 256) {
-        const int64_t m = i / width, c = i % width;
-        if (c >= F) {                                // padding
-            for (int p = 0; p < parts; ++p) out[p * M * cols + m * cols + N + (c - F)] = 0;
+        const int64_t m = i / width, c = i % width * V;
+        float v[V];
+        if (c >= F) {                            // padding
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = 0.0f;
+            store_parts<V>(out, m * cols + N + (c - F), M * cols, parts, v);
             continue;
         }
-        float v = widen<FMT>(static_cast<const T *>(dy)[m * F + c]);
+        load_values<FMT, V>(dy, m * F + c, v);
         if constexpr (GATED) {
-            const float g = widen<FMT>(static_cast<const T *>(gu)[2 * m * F + c]);
-            const float u = widen<FMT>(static_cast<const T *>(gu)[(2 * m + 1) * F + c]);
-            float a, s;
-            gate_act_slope(act, g, a, s);
-            const T dg = narrow<FMT>(v * u * s), du = narrow<FMT>(v * a);
-            if (dgu) {
-                static_cast<T *>(dgu)[2 * m * F + c] = dg;
-                static_cast<T *>(dgu)[(2 * m + 1) * F + c] = du;
-            }
+            float g[V], u[V], dg[V], du[V];
+            load_values<FMT, V>(gu, 2 * m * F + c, g);
+            load_values<FMT, V>(gu, (2 * m + 1) * F + c, u);
+            auto run = [&](auto kind) __attribute__((always_inline)) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    float a, s;
+                    gate_act_slope<kind.value>(g[e], a, s);
+                    dg[e] = v[e] * u[e] * s;
+                    du[e] = v[e] * a;
+                }
+            };
+            if (act == kSilu)
+                run(std::integral_constant<int, kSilu>());
+            else if (act == kGelu)
+                run(std::integral_constant<int, kGelu>());
+            else
+                run(std::integral_constant<int, kGeluTanh>());
+            round_values<FMT, V>(dgu, 2 * m * F + c, dg);
+            round_values<FMT, V>(dgu, (2 * m + 1) * F + c, du);
             if (out) {
-                store_parts(out, m * cols + c, M * cols, parts, widen<FMT>(dg));
-                store_parts(out, m * cols + F + c, M * cols, parts, widen<FMT>(du));
+                store_parts<V>(out, m * cols + c, M * cols, parts, dg);
+                store_parts<V>(out, m * cols + F + c, M * cols, parts, du);
             }
         } else {
-            store_parts(out, m * cols + c, M * cols, parts, v);
+            store_parts<V>(out, m * cols + c, M * cols, parts, v);
         }
     }
 }
@@ -122,8 +198,8 @@ struct GradTile {
     static constexpr int kRows = BM / 8 / W;             // 16-byte pieces of d's tile a thread moves
     static constexpr int kUnits = BN / 32;               // blocks of scales in a row of the tile
     static constexpr int kBlocks = BN == 256 ? 1 : 3;    // a compute unit holds
-    static constexpr int kRun = BN == 256 ? 1500 : 700, kMore = BN == 256 ? 600 : 400,
-                         kEnds = BN == 256 ? 6000 : 2500;               // plan_tiles's times
+    static constexpr int kRun = BN == 256 ? 1770 : 640, kMore = BN == 256 ? 80 : 540,
+                         kEnds = BN == 256 ? 5000 : 2500;               // plan_tiles's times
     static_assert(kRows * W * 8 == BM && kStep * kUnits == T, "a thread expands one block");
 };
 
@@ -274,17 +350,23 @@ void grad_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__res
             make_rsrc(ws + first * sb + k0 / kMxBlock, rows ? (int64_t)(rows - 1) * sb + cols / kMxBlock : 0);
         byte = __builtin_amdgcn_raw_buffer_load_b8(rss, live ? row_w * sb + unit_w : kCopyOob, 0, 0);
     };
-    const int place_w = (2 * unit_w) ^ grad_turn(row_w);
-    uint8_t *const to_wide = wide0 + row_w * (2 * L::BN) + 32 * place_w;
-    const int other = 32 - 64 * (place_w & 1);       // to the block's second half
+    // 16-byte piece q of the block goes to place q ^ turn of its 64 bytes in the
+    // row; the lanes write their pieces in the order q ^ order, so that eight of
+    // them fill 128 bytes at a time (in one order 32 clocks a store, so 14)
+    const int order = (unit_w >> 1) & 3, turn_w = grad_turn(row_w);
+    const uint32_t to_wide = row_w * (2 * L::BN) + 64 * (unit_w ^ (turn_w >> 1)) + 16 * (order ^ (2 * (turn_w & 1)));
     auto expand = [&](int slot) __attribute__((always_inline)) {
         const float scale = mx_scale(byte & 0xffu);
+        const bool odd = order & 1, high = order & 2;
+        const uint32_t c0 = odd ? codes[1] : codes[0], c1 = odd ? codes[0] : codes[1];
+        const uint32_t c2 = odd ? codes[3] : codes[2], c3 = odd ? codes[2] : codes[3];
+        const v4u c = {high ? c2 : c0, high ? c3 : c1, high ? c0 : c2, high ? c1 : c3};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             v4u v;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = expand2(codes[q], scale, j);
-            *reinterpret_cast<v4u *>(to_wide + slot * L::kWide + (q >> 1) * other + 16 * (q & 1)) = v;
+            for (int j = 0; j < 4; ++j) v[j] = expand2(c[q], scale, j);
+            *reinterpret_cast<v4u *>(wide0 + slot * L::kWide + (to_wide ^ (16 * q))) = v;
         }
     };
 
@@ -411,18 +493,22 @@ hipError_t run_grad(const GradRows &d, const Mx4GradArgs &a, MxPlan p, void *wor
     return hipGetLastError();
 }
 
+template <int FMT, bool GATED, int V>
+hipError_t launch_rows(const Mx4GradArgs &a, void *dgu, uint16_t *out, int64_t cols, hipStream_t stream) {
+    const int64_t F = GATED ? a.N / 2 : a.N, n = a.M * ((F + (out ? cols - a.N : 0)) / V);
+    hipLaunchKernelGGL((grad_rows_kernel<FMT, GATED, V>), dim3(blocks_of(n)), dim3(256), 0, stream, a.dy, a.gu, dgu,
+                       a.act, out, a.M, a.N, cols, parts_of(FMT));
+    return hipGetLastError();
+}
+
 template <int FMT>
 hipError_t run_rows(const Mx4GradArgs &a, void *dgu, uint16_t *out, int64_t cols, hipStream_t stream) {
-    const int64_t F = a.gu ? a.N / 2 : a.N;
-    const int64_t n = a.M * (F + (out ? cols - a.N : 0));
-    const dim3 grid(blocks_of(n)), block(256);
+    const bool eight = (a.gu ? a.N / 2 : a.N) % 8 == 0;     // bases are 16-byte aligned, cols whole stages
     if (a.gu)
-        hipLaunchKernelGGL((grad_rows_kernel<FMT, true>), grid, block, 0, stream, a.dy, a.gu, dgu,
-                           a.act, out, a.M, a.N, cols, parts_of(FMT));
-    else
-        hipLaunchKernelGGL((grad_rows_kernel<FMT, false>), grid, block, 0, stream, a.dy, nullptr,
-                           nullptr, 0, out, a.M, a.N, cols, parts_of(FMT));
-    return hipGetLastError();
+        return eight ? launch_rows<FMT, true, 8>(a, dgu, out, cols, stream)
+                     : launch_rows<FMT, true, 1>(a, dgu, out, cols, stream);
+    return eight ? launch_rows<FMT, false, 8>(a, dgu, out, cols, stream)
+                 : launch_rows<FMT, false, 1>(a, dgu, out, cols, stream);
 }
 
 }  // namespace
