@@ -513,14 +513,21 @@ def pq2_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tenso
 
 def _mx4_args(codes: torch.Tensor, scales: torch.Tensor, name: str, at: int, K: int):
     """Pointers and rows of an MX4 matrix of rows of K."""
-    rows = _mk(codes)[0]
+    rows = codes.shape[0]
     return (_ptr(codes, name, torch.uint8, (rows, K // 2), at),
             _ptr(scales, name + "scale", torch.uint8, (rows, K // MX4_BLOCK), at)), rows
 
 
 def _mx4_work(workspace, at: int, device, stream, query, *args):
     """(pointer, bytes, keep-alive) of an MX4 workspace argument, as _workspace."""
-    wp, wn, keep = _workspace(workspace, 0, 0, 0, device, stream, lambda *_: int(query(*args)))
+    if workspace is None:
+        return 0, 0, None
+    n = 0
+    if isinstance(workspace, str):
+        n = query(*args)
+        if n == 0 and workspace == "auto":
+            return 0, 0, None
+    wp, wn, keep = _workspace(workspace, 0, 0, 0, device, stream, lambda *_: n)
     if keep is not None and keep.get_device() != at:
         raise ValueError(f"workspace must be on cuda:{at}, got {keep.device}")
     return wp, wn, keep

@@ -36,7 +36,7 @@ pq2_status check_mx4_rows(int64_t M, int64_t K) {
 // MX4 products. The kernels address a tile's rows (at most 256) with 32-bit
 // offsets, and both halves of a gated block's scales with one resource.
 pq2_status check_mx4(int64_t M, int64_t N, int64_t K, bool gated) {
-    if (M < 0 || M > PQ2_MAX_DIM || N < 1 || N > (gated ? PQ2_MX4_MAX_N / 2 : PQ2_MX4_MAX_N) ||
+    if (M < 0 || M > PQ2_MX4_MAX_M || N < 1 || N > (gated ? PQ2_MX4_MAX_N / 2 : PQ2_MX4_MAX_N) ||
         K < PQ2_MX4_STEP || K % PQ2_MX4_STEP != 0 || K > PQ2_MX4_MAX_K)
         return PQ2_ERR_SHAPE;
     const int64_t rows = gated ? 2 * N : N;

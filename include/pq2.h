@@ -393,10 +393,11 @@ pq2_status pq2_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, void 
  *              plan that needs no more. As for pq2_gemm, calls that may overlap
  *              need workspaces of their own.
  * PQ2_ERR_SHAPE: N outside 1 .. PQ2_MX4_MAX_N, K not a multiple of
- * PQ2_MX4_STEP in PQ2_MX4_STEP .. PQ2_MX4_MAX_K, M above PQ2_MAX_DIM, M*N or M*K
- * above PQ2_MAX_ELEMS.
+ * PQ2_MX4_STEP in PQ2_MX4_STEP .. PQ2_MX4_MAX_K, M above PQ2_MX4_MAX_M, M*N or
+ * M*K above PQ2_MAX_ELEMS.
  */
 #define PQ2_MX4_STEP 128
+#define PQ2_MX4_MAX_M (1LL << 26)
 #define PQ2_MX4_MAX_N (1LL << 21)
 #define PQ2_MX4_MAX_K (1LL << 21)
 size_t pq2_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K, int gated);

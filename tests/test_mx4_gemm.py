@@ -52,8 +52,8 @@ def gated(a=P, s=P, w=P, ws=P, act=0, y=P, gu=None, fmt=0, hq=None, hs=None, M=1
     (dict(ws=None), ERR_NULL), (dict(y=None), ERR_NULL),
     (dict(M=-1), ERR_SHAPE), (dict(N=0), ERR_SHAPE), (dict(N=(1 << 21) + 1), ERR_SHAPE),
     (dict(K=0), ERR_SHAPE), (dict(K=64), ERR_SHAPE), (dict(K=160), ERR_SHAPE),
-    (dict(K=(1 << 21) + 128), ERR_SHAPE), (dict(M=(1 << 30) + 1), ERR_SHAPE),
-    (dict(M=1 << 30, N=2048), ERR_SHAPE), (dict(M=1 << 30, K=2048), ERR_SHAPE),
+    (dict(K=(1 << 21) + 128), ERR_SHAPE), (dict(M=(1 << 26) + 1), ERR_SHAPE),
+    (dict(M=1 << 26, N=1 << 15), ERR_SHAPE), (dict(M=1 << 26, K=1 << 15), ERR_SHAPE),
     (dict(fmt=3), ERR_ARG), (dict(fmt=-1), ERR_ARG),
     (dict(a=P + 8), ERR_ALIGN), (dict(w=P + 8), ERR_ALIGN), (dict(s=P + 2), ERR_ALIGN),
     (dict(ws=P + 1), ERR_ALIGN), (dict(y=P + 2), ERR_ALIGN), (dict(y=P + 1, fmt=1), ERR_ALIGN),
@@ -158,6 +158,38 @@ def test_gemm_exact(M, N, K):
     y = torch.empty(M, N, device="cuda")
     pq2.pq2_mx4_gemm(*a.args, *w.args, y)
     assert torch.equal(y.double(), product(a, w)[0])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K,gated", [
+    (33, 5120, 17408, False), (100, 1000, 8192, False), (130, 5120, 17408, False), (500, 5120, 17408, False),
+    (1000, 5120, 6144, False), (1000, 17408, 1152, False), (4096, 4352, 8192, False), (2000, 8704, 5120, False),
+    (40, 2048, 17408, True), (300, 8704, 5120, True), (1030, 2176, 8192, True), (4000, 2200, 5120, True)])
+def test_plans_agree(M, N, K, gated):
+    """Every tile, whole and split along K in any workspace: with all scales alike
+    nothing is rounded, so the results are the same bits; some rows against
+    float64."""
+    a, w = Matrix(M, K, M, flat=True), Matrix(2 * N if gated else N, K, N, flat=True)
+    w.scales -= 10                                   # the block's sums of order one
+    w.refresh()
+    call = pq2.pq2_mx4_gated if gated else pq2.pq2_mx4_gemm
+    y, z = (torch.full((M, N), 7.0, device="cuda") for _ in range(2))
+    call(*a.args, *w.args, y)
+    call(*a.args, *w.args, z, workspace=None)
+    assert torch.equal(y, z)
+    most = pq2.mx4_workspace_bytes(M, N, K, gated)
+    for n in {most // 2, most // 7} - {0}:
+        call(*a.args, *w.args, z, workspace=torch.full((n,), 255, dtype=torch.uint8, device="cuda"))
+        assert torch.equal(y, z)
+    some = torch.tensor(sorted({0, M // 3, M // 2, M - 2, M - 1}), device="cuda")
+    want = a.v[some] @ w.v.t()
+    if gated:
+        g, u = want[:, :N], want[:, N:]
+        v = torch.from_numpy(mx4.act("silu", g.cpu().numpy())[0]).cuda() * u
+        rel = torch.minimum((10 + 3 * g * g) * 2.0 ** -23, torch.ones_like(g))
+        check(y[some], v, rel * v.abs(), "f32")
+    else:
+        assert torch.equal(y[some].double(), want)
 
 
 @pytest.mark.gpu

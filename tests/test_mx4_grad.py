@@ -46,8 +46,8 @@ def gated_grad(dy=P, gu=P, act=0, w=P, ws=P, dgu=P, dx=P, fmt=1, M=1, N=8, K=128
     (dict(dy=None), ERR_NULL), (dict(w=None), ERR_NULL), (dict(ws=None), ERR_NULL),
     (dict(dx=None), ERR_NULL), (dict(M=-1), ERR_SHAPE), (dict(N=0), ERR_SHAPE),
     (dict(N=(1 << 21) + 1), ERR_SHAPE), (dict(K=0), ERR_SHAPE), (dict(K=192), ERR_SHAPE),
-    (dict(K=(1 << 21) + 128), ERR_SHAPE), (dict(M=(1 << 30) + 1), ERR_SHAPE),
-    (dict(M=1 << 30, N=2048), ERR_SHAPE), (dict(M=1 << 30, K=2048), ERR_SHAPE),
+    (dict(K=(1 << 21) + 128), ERR_SHAPE), (dict(M=(1 << 26) + 1), ERR_SHAPE),
+    (dict(M=1 << 26, N=1 << 15), ERR_SHAPE), (dict(M=1 << 26, K=1 << 15), ERR_SHAPE),
     (dict(fmt=3), ERR_ARG), (dict(fmt=-1), ERR_ARG), (dict(dy=P + 8), ERR_ALIGN),
     (dict(w=P + 8), ERR_ALIGN), (dict(ws=P + 2), ERR_ALIGN), (dict(dx=P + 1), ERR_ALIGN),
     (dict(dx=P + 2, fmt=0), ERR_ALIGN), (dict(work=P + 8), ERR_ALIGN),
@@ -139,6 +139,27 @@ def test_gemm_grad_exact(M, N, K, ty):
     dx = torch.empty(M, K, dtype=TYPES[ty], device="cuda")
     pq2.pq2_mx4_gemm_grad(dy, *w, dx)
     assert torch.equal(dx, (dy.double() @ decoded(*w)).float().to(TYPES[ty]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ty", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(1, 17408, 1024), (33, 5120, 17408), (300, 5120, 6144), (1000, 2048, 17408),
+                                   (2048, 2048, 8704), (4000, 1000, 5120)])
+def test_plans_agree(M, N, K, ty):
+    """Both tiles, whole and split along N in any workspace: small integers, no
+    rounding but the output's, so the same bits; some rows against float64."""
+    w = weights(N, K, 1, flat=True)
+    dy = torch.randint(-4, 5, (M, N), device="cuda").to(TYPES[ty])
+    dx, other = (torch.full((M, K), 7.0, dtype=TYPES[ty], device="cuda") for _ in range(2))
+    pq2.pq2_mx4_gemm_grad(dy, *w, dx)
+    least = 0 if ty == "bf16" and N % 8 == 0 else (PARTS[ty] * M * ((N + 63) // 64 * 64) * 2 + 255) // 256 * 256
+    most = pq2.mx4_grad_workspace_bytes(M, N, K, TYPES[ty])
+    for n in {least, (least + most) // 2, least + (most - least) // 7}:
+        work = torch.full((max(n, 16),), 255, dtype=torch.uint8, device="cuda")[:n]
+        pq2.pq2_mx4_gemm_grad(dy, *w, other, workspace=work if n else None)
+        assert torch.equal(dx, other)
+    some = sorted({0, M // 3, M // 2, M - 1})
+    assert torch.equal(dx[some], (dy[some].double() @ decoded(*w)).float().to(TYPES[ty]))
 
 
 @pytest.mark.gpu
