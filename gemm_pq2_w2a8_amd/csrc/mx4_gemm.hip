@@ -187,11 +187,11 @@ __device__ __forceinline__ void end_share(const Mx4Args &a, const MxPlan &p, con
     if (m < a.M) store_share<L::WN, L::WM, L::T>(p, s.item, wave * kWave + lane, acc);
 }
 
-// The split tiles' sums and their end: a block for every four instruction tiles
-// of a wave's rows.
+// The split tiles' sums and their end: a block for every two instruction tiles of a
+// wave's rows (gated: four, a block of 32 columns).
 template <class L, bool GATED>
 __global__ __launch_bounds__(L::T) void mx4_sum_kernel(Mx4Args a, MxPlan p) {
-    constexpr int NI = 4, WM = L::WM, kCuts = L::WN / NI;
+    constexpr int NI = GATED ? 4 : 2, WM = L::WM, kCuts = L::WN / NI;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
     const int index = (int)blockIdx.x / kCuts, cut = (int)blockIdx.x % kCuts;
     const int wn = wave % L::NWN, wm = wave / L::NWN;
@@ -739,7 +739,7 @@ hipError_t launch_tiles(const Mx4Args &a, MxPlan p, void *work, hipStream_t stre
     else
         e = span ? go(mx4_tile_kernel<L, GATED, true>) : go(mx4_tile_kernel<L, GATED, false>);
     if (e != hipSuccess || rest == 0) return e;
-    hipLaunchKernelGGL((mx4_sum_kernel<L, GATED>), dim3((unsigned)(rest * (L::WN / 4))), block, 0, stream, a, p);
+    hipLaunchKernelGGL((mx4_sum_kernel<L, GATED>), dim3((unsigned)(rest * (L::WN / (GATED ? 4 : 2)))), block, 0, stream, a, p);
     return hipGetLastError();
 }
 

@@ -273,7 +273,7 @@ __device__ __forceinline__ void end_grad(const GradOut &o, const MxPlan &p, cons
 
 template <class L>
 __global__ __launch_bounds__(L::T) void grad_sum_kernel(GradOut o, MxPlan p) {
-    constexpr int NI = 4, kCuts = L::WK / NI;
+    constexpr int NI = 1, kCuts = L::WK / NI;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
     const int index = (int)blockIdx.x / kCuts, cut = (int)blockIdx.x % kCuts;
     const int wk = wave % L::NWK, wm = wave / L::NWK;
@@ -491,7 +491,7 @@ hipError_t run_grad(const GradRows &d, const Mx4GradArgs &a, MxPlan p, void *wor
     const hipError_t e = hipGetLastError();
     const int rest = p.tiles_n * p.tiles_m - p.full;
     if (e != hipSuccess || rest == 0) return e;
-    hipLaunchKernelGGL(grad_sum_kernel<L>, dim3((unsigned)(rest * (L::WK / 4))), dim3(L::T), 0, stream, o, p);
+    hipLaunchKernelGGL(grad_sum_kernel<L>, dim3((unsigned)(rest * L::WK)), dim3(L::T), 0, stream, o, p);
     return hipGetLastError();
 }
 

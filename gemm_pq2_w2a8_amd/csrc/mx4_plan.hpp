@@ -62,19 +62,29 @@ __device__ __forceinline__ void store_share(const MxPlan &p, int item, int tid, 
         for (int j = 0; j < J; ++j) *reinterpret_cast<v4f32 *>(to + (i * J + j) * (4 * T)) = acc[i][j];
 }
 
-// Rows i0 .. i0 + NI - 1 of split tile `index`, its shares added in order.
+// Rows i0 .. i0 + NI - 1 of split tile `index`, its shares added in order, four
+// requested at a time.
 template <int NI, int I, int J, int T>
 __device__ __forceinline__ void sum_shares(const MxPlan &p, int index, int i0, int tid, v4f32 (&acc)[NI][J]) {
-    for (int way = 0; way < p.ways; ++way) {
-        const float *from = p.part + ((int64_t)index * p.ways + way) * (I * J * T * 4) + 4 * tid;
+    const float *const from = p.part + (int64_t)index * p.ways * (I * J * T * 4) + 4 * tid;
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const v4f32 v = *reinterpret_cast<const v4f32 *>(from + ((i0 + i) * J + j) * (4 * T));
-                acc[i][j] = way ? acc[i][j] + v : v;
+        for (int j = 0; j < J; ++j) {
+            const float *const at = from + ((i0 + i) * J + j) * (4 * T);
+            v4f32 sum = *reinterpret_cast<const v4f32 *>(at);
+            for (int way = 1; way < p.ways; way += 4) {
+                v4f32 v[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (way + u < p.ways)
+                        v[u] = *reinterpret_cast<const v4f32 *>(at + (int64_t)(way + u) * (I * J * T * 4));
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (way + u < p.ways) sum += v[u];
             }
-    }
+            acc[i][j] = sum;
+        }
 }
 
 // The plan of a tile L for `rows` x M results. Tiles left over after whole rounds
