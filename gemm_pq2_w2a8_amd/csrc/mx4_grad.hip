@@ -24,7 +24,7 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 
 constexpr int kStep = 64;             // n of a stage: two matrix instructions
 
-int parts_of(int format) { return format == kBf16 ? 1 : format == kF16 ? 2 : 3; }
+constexpr int parts_of(int format) { return format == kBf16 ? 1 : format == kF16 ? 2 : 3; }
 
 // ---------------------------------------------------------------- parts of d
 
@@ -49,12 +49,13 @@ __device__ __forceinline__ uint16_t take_part(float &v) {
 }
 
 // V columns of one row of d as its parts, from element `at` of the first on.
-template <int V>
-__device__ __forceinline__ void store_parts(uint16_t *out, int64_t at, int64_t plane, int parts, float (&v)[V]) {
-    for (int p = 0; p < parts; ++p) {
+template <int FMT, int V>
+__device__ __forceinline__ void store_parts(uint16_t *out, int64_t at, int64_t plane, float (&v)[V]) {
+#pragma unroll
+    for (int p = 0; p < parts_of(FMT); ++p) {
         uint16_t h[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) h[i] = parts == 1 ? bf16_rne(v[i]) : take_part(v[i]);   // one part: exact
+        for (int i = 0; i < V; ++i) h[i] = FMT == kBf16 ? bf16_rne(v[i]) : take_part(v[i]);   // one part: exact
         uint16_t *to = out + at + p * plane;
         if constexpr (V == 8) {
             v4u o;
@@ -119,21 +120,22 @@ __device__ __forceinline__ void round_values(void *x, int64_t at, float (&v)[V])
 // What multiplies the weights: d's parts, for a gated block from dh, g and u, whose
 // dgu it writes too (dgu may be gu). V columns a thread: eight where rows of F
 // columns keep 16-byte addresses (2048 x 17408 bfloat16 116 us one by one, TODO by
-// eight); the columns behind d's last, up to a whole stage, are zeros.
+// eight); the columns behind d's last, up to a whole stage, are zeros. A block is
+// 2^span threads wide, the others of its 256 take rows below.
 template <int FMT, bool GATED, int V>
 __global__ __launch_bounds__(256) void grad_rows_kernel(const void *dy, const void *gu, void *dgu,
                                                         int act, uint16_t *out, int64_t M,
-                                                        int64_t N, int64_t cols, int parts) {
+                                                        int64_t N, int64_t cols, int span) {
     const int64_t F = GATED ? N / 2 : N;         // columns of dy
-    const int64_t width = (F + (out ? cols - N : 0)) / V;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < M * width;
-         i += (int64_t)gridDim.x * 256) {
-        const int64_t m = i / width, c = i % width * V;
+    const int64_t c = (((int64_t)blockIdx.x << span) + (threadIdx.x & ((1 << span) - 1))) * V;
+    if (c >= F + (out ? cols - N : 0)) return;
+    const int64_t rows = 256 >> span;
+    for (int64_t m = (int64_t)blockIdx.y * rows + (threadIdx.x >> span); m < M; m += gridDim.y * rows) {
         float v[V];
         if (c >= F) {                            // padding
 #pragma unroll
             for (int e = 0; e < V; ++e) v[e] = 0.0f;
-            store_parts<V>(out, m * cols + N + (c - F), M * cols, parts, v);
+            store_parts<FMT, V>(out, m * cols + N + (c - F), M * cols, v);
             continue;
         }
         load_values<FMT, V>(dy, m * F + c, v);
@@ -159,11 +161,11 @@ __global__ __launch_bounds__(256) void grad_rows_kernel(const void *dy, const vo
             round_values<FMT, V>(dgu, 2 * m * F + c, dg);
             round_values<FMT, V>(dgu, (2 * m + 1) * F + c, du);
             if (out) {
-                store_parts<V>(out, m * cols + c, M * cols, parts, dg);
-                store_parts<V>(out, m * cols + F + c, M * cols, parts, du);
+                store_parts<FMT, V>(out, m * cols + c, M * cols, dg);
+                store_parts<FMT, V>(out, m * cols + F + c, M * cols, du);
             }
         } else {
-            store_parts<V>(out, m * cols + c, M * cols, parts, v);
+            store_parts<FMT, V>(out, m * cols + c, M * cols, v);
         }
     }
 }
@@ -462,11 +464,6 @@ void grad_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__res
 }
 
 // A launch holds fewer than 2^32 threads: the kernels go round again.
-unsigned blocks_of(int64_t threads) {
-    const int64_t b = (threads + 255) / 256;
-    return (unsigned)(b < (1 << 22) ? b : 1 << 22);
-}
-
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // Whether d is read where it lies: bfloat16 rows of whole 16-byte units.
@@ -497,9 +494,15 @@ hipError_t run_grad(const GradRows &d, const Mx4GradArgs &a, MxPlan p, void *wor
 
 template <int FMT, bool GATED, int V>
 hipError_t launch_rows(const Mx4GradArgs &a, void *dgu, uint16_t *out, int64_t cols, hipStream_t stream) {
-    const int64_t F = GATED ? a.N / 2 : a.N, n = a.M * ((F + (out ? cols - a.N : 0)) / V);
-    hipLaunchKernelGGL((grad_rows_kernel<FMT, GATED, V>), dim3(blocks_of(n)), dim3(256), 0, stream, a.dy, a.gu, dgu,
-                       a.act, out, a.M, a.N, cols, parts_of(FMT));
+    const int64_t F = GATED ? a.N / 2 : a.N, width = (F + (out ? cols - a.N : 0)) / V;
+    int span = 0;
+    while (span < 8 && (1 << span) < width) ++span;
+    const int64_t across = (width + (1 << span) - 1) >> span, down = (a.M + (256 >> span) - 1) / (256 >> span);
+    int64_t most = (1 << 22) / across;               // a launch holds fewer than 2^32 threads: rows go round again
+    most = most < 65535 ? most : 65535;
+    hipLaunchKernelGGL((grad_rows_kernel<FMT, GATED, V>),
+                       dim3((unsigned)across, (unsigned)(down < most ? down : most)), dim3(256), 0, stream, a.dy,
+                       a.gu, dgu, a.act, out, a.M, a.N, cols, span);
     return hipGetLastError();
 }
 
