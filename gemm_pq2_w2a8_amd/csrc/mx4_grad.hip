@@ -199,9 +199,10 @@ struct GradTile {
     static constexpr int kLdsBytes = 2 * (kD + kWide);
     static constexpr int kRows = BM / 8 / W;             // 16-byte pieces of d's tile a thread moves
     static constexpr int kUnits = BN / 32;               // blocks of scales in a row of the tile
-    static constexpr int kBlocks = BN == 256 ? 1 : 3;    // a compute unit holds
-    static constexpr int kRun = BN == 256 ? 1770 : 640, kMore = BN == 256 ? 80 : 540,
-                         kEnds = BN == 256 ? 5000 : 2500;               // plan_tiles's times
+    static constexpr bool kTwo = W == 8;                 // two waves a SIMD (wide)
+    static constexpr int kBlocks = kTwo ? 1 : 3;         // a compute unit holds
+    static constexpr int kRun = kTwo ? 1770 : 640, kMore = kTwo ? 80 : 540,
+                         kEnds = kTwo ? 5000 : 2500;               // plan_tiles's times
     static_assert(kRows * W * 8 == BM && kStep * kUnits == T, "a thread expands one block");
 };
 
@@ -422,9 +423,9 @@ void grad_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__res
         for (int i = 0; i < WK; ++i) {
             products(0, i);
             read_w(slot_w, 1, i);
-            // (the two waves of a SIMD, wave and wave + W / 2, not at once: 684 -> 645 us
-            // at 2048 x 34816 x 5120)
-            if ((i == 0 && wave < W / 2) || (i == WK / 2 && wave >= W / 2)) {
+            // wide: the two waves of a SIMD, wave and wave + W / 2, not at once (684 -> 645
+            // us at 2048 x 34816 x 5120). Small: a block has one wave on each
+            if (i == 0 ? !L::kTwo || wave < W / 2 : L::kTwo && i == WK / 2 && wave >= W / 2) {
                 __builtin_amdgcn_sched_barrier(0);
                 store_d(slot ^ 1);
                 ++ahead_p;
@@ -433,7 +434,9 @@ void grad_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__res
                     ++ahead_s;
                 }
                 load_d(ahead_s, ahead_p);
-                if (p == 0) {
+                // in a stage's first tile or in its last, as measured: wide 616 us at 4096 x
+                // 5120 x 17408 (628 in the last), small 116 at 128 x 5120 x 17408 float32 (134)
+                if (L::kTwo ? p == 0 : p + 1 == parts) {
                     expand(slot_w ^ 1);
                     load_w(s + 2);
                 }
