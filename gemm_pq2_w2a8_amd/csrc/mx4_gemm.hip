@@ -184,7 +184,7 @@ __device__ __forceinline__ void end_share(const Mx4Args &a, const MxPlan &p, con
         finish<L::WN, L::WM, GATED>(a, acc, first_column<L, GATED>(s.tn) + (GATED ? 8 : 16) * L::WN * wn, m + (lane & 15), a.N, lane);
         return;
     }
-    if (m < a.M) store_share<L::WN, L::WM, L::T>(p, s.item, wave * kWave + lane, acc);
+    if (m < a.M) store_share<L::WN, L::WM, L::T>(p, s.item, wave * kWave + lane, L::WM, acc);
 }
 
 // The split tiles' sums and their end: a block for every two instruction tiles of a
@@ -200,7 +200,7 @@ __global__ __launch_bounds__(L::T) void mx4_sum_kernel(Mx4Args a, MxPlan p) {
     const int64_t m = (int64_t)tm * L::BM + 16 * WM * wm;
     if (m >= a.M) return;
     v4f32 acc[NI][WM];
-    sum_shares<NI, L::WN, WM, L::T>(p, index, NI * cut, tid, acc);
+    sum_shares<L::WN, WM, L::T>(p, index, NI * cut, 0, tid, acc);
     const int64_t n = first_column<L, GATED>(tn) + (GATED ? 8 : 16) * (L::WN * wn + NI * cut);
     finish<NI, WM, GATED>(a, acc, n, m + (lane & 15), a.N, lane);
 }

@@ -20,7 +20,6 @@ namespace pq2 {
 namespace {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef short v4s __attribute__((ext_vector_type(4)));
 
 constexpr int kStep = 64;             // n of a stage: two matrix instructions
 
@@ -119,8 +118,8 @@ __device__ __forceinline__ void round_values(void *x, int64_t at, float (&v)[V])
 
 // What multiplies the weights: d's parts, for a gated block from dh, g and u, whose
 // dgu it writes too (dgu may be gu). V columns a thread: eight where rows of F
-// columns keep 16-byte addresses (2048 x 17408 bfloat16 116 us one by one, TODO by
-// eight); the columns behind d's last, up to a whole stage, are zeros. A block is
+// columns keep 16-byte addresses (2048 x 17408 bfloat16 116 us one by one, 55 by
+// eight, 6.5 TB/s); the columns behind d's last, up to a whole stage, are zeros. A block is
 // 2^span threads wide, the others of its 256 take rows below.
 template <int FMT, bool GATED, int V>
 __global__ __launch_bounds__(256) void grad_rows_kernel(const void *dy, const void *gu, void *dgu,
@@ -172,85 +171,107 @@ __global__ __launch_bounds__(256) void grad_rows_kernel(const void *dy, const vo
 
 // ---------------------------------------------------------------- product
 //
-// A block owns BN columns of dx x BM tokens, NWK x NWM waves of WK x WM
-// instruction tiles. A stage is 64 n of one part of d: d's tile and the weights
-// as bfloat16, rows n of BN values, in two LDS slots each. Both come through
-// registers, loaded a stage before they are stored: a thread expands 32 values
-// under one scale (sixteen conversions) while others multiply. (Buffer -> LDS
-// copies do not go with the transposing LDS reads: the compiler waits for every
-// copy in flight before such a read; 4096 x 5120 x 17408 in 1009 us instead of
-// TODO.) The instruction wants, for a column k, eight consecutive n: the
-// transposing read takes them out of four rows at a time. The 32-byte segment seg
-// of row n lies at place seg ^ turn(n), so that the four (and eight) rows of such a
-// read are in different banks.
+// A block owns BN columns of dx x BM tokens, a wave 32 of the columns (one block of
+// scales) and all tokens, so that no two waves expand the same weights. A stage is
+// 64 n of one part of d, in two LDS slots: d's tile, and the weights' codes and
+// scales (as float32) as they are, rows n of BN codes. All come through registers,
+// loaded a stage before they are stored. The instruction wants, for a column k,
+// eight consecutive n: the transposing read gives a lane eight rows' bytes of one
+// place, which are two columns, 2 r and 2 r + 1, of each row; a conversion makes
+// the two bfloat16 values of a byte under its row's scale, a permutation of two
+// conversions a pair of n of one column. So an instruction tile holds the 16 even
+// columns of a block and the next one the odd, and a lane's results are eight
+// columns in a row. The 16-byte unit u of row n lies at place(u, n), so that the 16
+// rows that half a wave reads at a time are in different banks.
 // A step is one instruction's 32 n, two a stage. What a step multiplies was read
-// from LDS during the step before, tokens into the other of two register sets,
-// weights rolling, each tile's registers taking the next step's as soon as its
+// from LDS during the step before: weights into the other of two register sets,
+// tokens rolling, each tile's registers taking the next step's as soon as its
 // products are issued. In the first step of a stage the next stage's tile is
 // stored and the one after requested; a barrier in the second shows it to all.
-// TODO figures
-template <int WK_, int WM_, int NWK_, int NWM_>
+// 4096 x 5120 x 17408 bfloat16 581 us with 256 x 256 tiles (1.26 PFLOP/s; a library
+// product of bfloat16 matrices 1.44); 128 x 34816 x 5120 82 with 128 x 64. Every
+// other instruction shares the SIMD's issue with the matrix instructions: the loop of
+// waves of 64 columns x half the tokens, with parts left out, took 358 us for those
+// alone, 99 more with the conversions, 31 with the reads of d, 40 with the stores to
+// LDS, 73 with the requests, 17 with their latency, 619 in all. From there scales as
+// float32 instead of bytes (no shifts: 608) and the waves of 32 columns (half the
+// conversions, twice the reads of d: 581). Before it, weights expanded to bfloat16 in
+// LDS once a block and read transposed from there: 616 and 92 us, LDS and conversions;
+// and buffer -> LDS copies, which the compiler waits for before a transposing read:
+// 1009 us instead of 708.
+template <int WM_, int W_>
 struct GradTile {
-    static constexpr int WK = WK_, WM = WM_, NWK = NWK_, NWM = NWM_;
-    static constexpr int W = NWK * NWM, T = kWave * W;
-    static constexpr int BN = 16 * WK * NWK, BM = 16 * WM * NWM;
+    static constexpr int WM = WM_, W = W_, T = kWave * W;
+    static constexpr int BN = 32 * W, BM = 16 * WM;
     static constexpr int kD = BM * 128;                  // bytes of a tile of d
-    static constexpr int kWide = kStep * BN * 2;
-    static constexpr int kLdsBytes = 2 * (kD + kWide);
+    static constexpr int kRow = BN / 2;          // bytes of a row n of codes
+    static constexpr int kScales = 4 * kStep + 32;            // bytes of a block's scales, one for each n
+    static constexpr int kSlot = kStep * kRow + W * kScales;
+    static constexpr int kLdsBytes = 2 * (kD + kSlot);
     static constexpr int kRows = BM / 8 / W;             // 16-byte pieces of d's tile a thread moves
-    static constexpr int kUnits = BN / 32;               // blocks of scales in a row of the tile
     static constexpr bool kTwo = W == 8;                 // two waves a SIMD (wide)
     static constexpr int kBlocks = kTwo ? 1 : 3;         // a compute unit holds
-    static constexpr int kRun = kTwo ? 1770 : 640, kMore = kTwo ? 80 : 540,
-                         kEnds = kTwo ? 5000 : 2500;               // plan_tiles's times
-    static_assert(kRows * W * 8 == BM && kStep * kUnits == T, "a thread expands one block");
+    static constexpr int kRun = kTwo ? 1470 : 565, kMore = kTwo ? 180 : 400,
+                         kEnds = kTwo ? 5000 : 2500;     // plan_tiles's times
+    static constexpr int kNJ = WM / 4;                    // instruction tiles of tokens a block sums
+    static_assert(kRows * W * 8 == BM && kStep * W == T && kSlot % 16 == 0, "a thread moves one block");
+
+    // where unit u of row n of the codes lies in the row
+    static __device__ __forceinline__ int place(int u, int n) { return u ^ (W == 8 ? (n >> 1) & 7 : (n >> 2) & 3); }
 };
 
-__device__ __forceinline__ int grad_turn(int n) { return (n & 3) | (((n >> 3) & 1) << 2); }
 __device__ __forceinline__ int grad_swizzle(int row) { return row & 6; }
 
-__device__ __forceinline__ uint32_t expand2(uint32_t word, float scale, int byte) {
-    switch (byte) {
-        case 0: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, scale, 0));
-        case 1: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, scale, 1));
-        case 2: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, scale, 2));
-        default: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, scale, 3));
-    }
+// Eight codes of one place 2 c, 2 c + 1 of eight rows (byte j: row j's pair), under
+// the rows' scales (byte j: row j's): the column of the even places and of the odd.
+// The conversion takes its scale's exponent bits alone.
+template <int J>
+__device__ __forceinline__ uint32_t expand2(v2u codes, const v4f32 (&scales)[2]) {
+    const float scale = scales[J / 4][J % 4];
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[J / 4], scale, J % 4));
 }
 
-// Sixteen columns of four rows, transposed: lane i of 16 gives the address of
-// four columns of row i / 4 and gets column i of all four rows.
-__device__ __forceinline__ v4s read_turned(const uint8_t *p) {
-    typedef __attribute__((address_space(3))) v4s lds_v4s;
-    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)p);
+template <int J>
+__device__ __forceinline__ void expand4(v2u codes, const v4f32 (&scales)[2], v4u &even, v4u &odd) {
+    const uint32_t a = expand2<2 * J>(codes, scales), b = expand2<2 * J + 1>(codes, scales);
+    even[J] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+    odd[J] = __builtin_amdgcn_perm(b, a, 0x07060302u);
 }
 
-// Four results of one row of dx from column k on, which is a multiple of four.
-__device__ __forceinline__ void store_dx(void *dx, int format, int64_t at, v4f32 v, bool wide) {
-    if (wide && format == kF32) {
-        *reinterpret_cast<v4f32 *>(static_cast<float *>(dx) + at) = v;
-    } else if (wide) {
-        *reinterpret_cast<v2u *>(static_cast<uint16_t *>(dx) + at) =
-            v2u{pack16(format, v[0], v[1]), pack16(format, v[2], v[3])};
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) store_fmt(dx, format, at + e, v[e]);
-    }
+// Sixteen bytes of eight rows, transposed: lane i of 16 gives the address of eight
+// bytes of row i / 2 and gets byte i of all eight rows.
+__device__ __forceinline__ v2u read_turned(const uint8_t *p) {
+    typedef int v2i __attribute__((ext_vector_type(2)));
+    typedef __attribute__((address_space(3))) v2i lds_v2i;
+    return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i *)p));
 }
 
-// acc[i][j]: four columns from k + 16 i + 4 (lane / 16) on of token m + 16 j.
-template <int NI, int WM>
-__device__ __forceinline__ void finish_dx(const v4f32 (&acc)[NI][WM], void *dx, int format, int64_t k, int64_t m,
+// acc[0][j], acc[1][j]: the even and the odd ones of eight columns from
+// k + 8 (lane / 16) on, token m + 16 j.
+template <int NJ>
+__device__ __forceinline__ void finish_dx(const v4f32 (&acc)[2][NJ], void *dx, int format, int64_t k, int64_t m,
                                           int64_t M, int64_t K, int lane) {
-    const bool wide = (reinterpret_cast<uintptr_t>(dx) & (format == kF32 ? 15 : 7)) == 0;
+    const bool wide = (reinterpret_cast<uintptr_t>(dx) & 15) == 0;
 #pragma unroll
-    for (int j = 0; j < WM; ++j) {
+    for (int j = 0; j < NJ; ++j) {
         const int64_t t = m + 16 * j;
         if (t >= M) continue;
+        const int64_t c = k + 8 * (lane >> 4), at = t * K + c;
+        if (c >= K) continue;                        // K is a multiple of 32
+        const v4f32 e = acc[0][j], o = acc[1][j];
+        if (wide && format == kF32) {
+            *reinterpret_cast<v4f32 *>(static_cast<float *>(dx) + at) = v4f32{e[0], o[0], e[1], o[1]};
+            *reinterpret_cast<v4f32 *>(static_cast<float *>(dx) + at + 4) = v4f32{e[2], o[2], e[3], o[3]};
+        } else if (wide) {
+            *reinterpret_cast<v4u *>(static_cast<uint16_t *>(dx) + at) =
+                v4u{pack16(format, e[0], o[0]), pack16(format, e[1], o[1]), pack16(format, e[2], o[2]),
+                    pack16(format, e[3], o[3])};
+        } else {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int64_t c = k + 16 * i + 4 * (lane >> 4);
-            if (c < K) store_dx(dx, format, t * K + c, acc[i][j], wide);     // K is a multiple of four
+            for (int x = 0; x < 4; ++x) {
+                store_fmt(dx, format, at + 2 * x, e[x]);
+                store_fmt(dx, format, at + 2 * x + 1, o[x]);
+            }
         }
     }
 }
@@ -264,42 +285,38 @@ struct GradOut {
 // The end of a block's work: the tile's results, or a split tile's sums.
 template <class L>
 __device__ __forceinline__ void end_grad(const GradOut &o, const MxPlan &p, const MxShare &s,
-                                         const v4f32 (&acc)[L::WK][L::WM], int wave, int lane) {
-    const int wk = wave % L::NWK, wm = wave / L::NWK;
-    const int64_t m = (int64_t)s.tm * L::BM + 16 * L::WM * wm;
+                                         const v4f32 (&acc)[2][L::WM], int wave, int lane) {
+    const int64_t m = (int64_t)s.tm * L::BM;
     if (!s.split)
-        finish_dx<L::WK, L::WM>(acc, o.dx, o.format, (int64_t)s.tn * L::BN + 16 * L::WK * wk, m + (lane & 15), o.M,
-                                o.K, lane);
-    else if (m < o.M)
-        store_share<L::WK, L::WM, L::T>(p, s.item, wave * kWave + lane, acc);
+        finish_dx(acc, o.dx, o.format, (int64_t)s.tn * L::BN + 32 * wave, m + (lane & 15), o.M, o.K, lane);
+    else
+        store_share<2, L::WM, L::T>(p, s.item, wave * kWave + lane, (int)(o.M - m < L::BM ? (o.M - m + 15) / 16 : L::WM),
+                                    acc);
 }
 
 template <class L>
 __global__ __launch_bounds__(L::T) void grad_sum_kernel(GradOut o, MxPlan p) {
-    constexpr int NI = 1, kCuts = L::WK / NI;
+    constexpr int NJ = L::kNJ, kCuts = L::WM / NJ;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
-    const int index = (int)blockIdx.x / kCuts, cut = (int)blockIdx.x % kCuts;
-    const int wk = wave % L::NWK, wm = wave / L::NWK;
+    const int index = (int)blockIdx.x / kCuts, j0 = (int)blockIdx.x % kCuts * NJ;
     int tn, tm;
     tile_at(p, p.full + index, tn, tm);
-    const int64_t m = (int64_t)tm * L::BM + 16 * L::WM * wm;
+    const int64_t m = (int64_t)tm * L::BM + 16 * j0;
     if (m >= o.M) return;
-    v4f32 acc[NI][L::WM];
-    sum_shares<NI, L::WK, L::WM, L::T>(p, index, NI * cut, tid, acc);
-    finish_dx<NI, L::WM>(acc, o.dx, o.format, (int64_t)tn * L::BN + 16 * (L::WK * wk + NI * cut), m + (lane & 15), o.M,
-                         o.K, lane);
+    v4f32 acc[2][NJ];
+    sum_shares<2, L::WM, L::T>(p, index, 0, j0, tid, acc);
+    finish_dx(acc, o.dx, o.format, (int64_t)tn * L::BN + 32 * wave, m + (lane & 15), o.M, o.K, lane);
 }
 
 template <class L>
 __global__ __launch_bounds__(L::T) __attribute__((amdgpu_waves_per_eu(2)))
 void grad_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__restrict__ ws, GradOut o, MxPlan plan) {
-    constexpr int WK = L::WK, WM = L::WM, W = L::W, NR = L::kRows;
+    constexpr int WM = L::WM, W = L::W, NR = L::kRows;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    uint8_t *const wide0 = smem + 2 * L::kD;
+    uint8_t *const codes0 = smem + 2 * L::kD;
     const int tid = threadIdx.x;
     const int lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wk = wave % L::NWK, wm = wave / L::NWK;
     const int r = lane & 15, lg = lane >> 4;
     const MxShare share = share_of(plan);
     if (!share.live) return;
@@ -335,8 +352,8 @@ void grad_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__res
         for (int i = 0; i < NR; ++i)
             *reinterpret_cast<v4u *>(smem + slot * L::kD + (i * W + wave) * 1024 + 16 * lane) = held[i];
     };
-    // weights: the thread expands block unit_w of row row_w of a stage
-    const int kb = (int)(K / 2), row_w = tid / L::kUnits, unit_w = tid % L::kUnits;
+    // weights: the thread moves block unit_w of row row_w of a stage, and its scale
+    const int kb = (int)(K / 2), row_w = tid / W, unit_w = tid % W;
     const bool live_w = 32 * unit_w < cols;
     v4u codes;
     uint32_t byte;
@@ -353,79 +370,76 @@ void grad_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__res
             make_rsrc(ws + first * sb + k0 / kMxBlock, rows ? (int64_t)(rows - 1) * sb + cols / kMxBlock : 0);
         byte = __builtin_amdgcn_raw_buffer_load_b8(rss, live ? row_w * sb + unit_w : kCopyOob, 0, 0);
     };
-    // 16-byte piece q of the block goes to place q ^ turn of its 64 bytes in the
-    // row; the lanes write their pieces in the order q ^ order, so that eight of
-    // them fill 128 bytes at a time (in one order 32 clocks a store, so 14)
-    const int order = (unit_w >> 1) & 3, turn_w = grad_turn(row_w);
-    const uint32_t to_wide = row_w * (2 * L::BN) + 64 * (unit_w ^ (turn_w >> 1)) + 16 * (order ^ (2 * (turn_w & 1)));
-    auto expand = [&](int slot) __attribute__((always_inline)) {
-        const float scale = mx_scale(byte & 0xffu);
-        const bool odd = order & 1, high = order & 2;
-        const uint32_t c0 = odd ? codes[1] : codes[0], c1 = odd ? codes[0] : codes[1];
-        const uint32_t c2 = odd ? codes[3] : codes[2], c3 = odd ? codes[2] : codes[3];
-        const v4u c = {high ? c2 : c0, high ? c3 : c1, high ? c0 : c2, high ? c1 : c3};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            v4u v;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = expand2(c[q], scale, j);
-            *reinterpret_cast<v4u *>(wide0 + slot * L::kWide + (to_wide ^ (16 * q))) = v;
-        }
+    const uint32_t to_codes = row_w * L::kRow + 16 * L::place(unit_w, row_w);
+    const uint32_t to_scale = kStep * L::kRow + unit_w * L::kScales + 4 * row_w;
+    auto store_w = [&](int slot) __attribute__((always_inline)) {
+        *reinterpret_cast<v4u *>(codes0 + slot * L::kSlot + to_codes) = codes;
+        *reinterpret_cast<uint32_t *>(codes0 + slot * L::kSlot + to_scale) = byte << 23;
     };
 
-    v4f32 acc[WK][WM];
+    v4f32 acc[2][WM];
 #pragma unroll
-    for (int i = 0; i < WK; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < WM; ++j) acc[i][j] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
-    v8bf fw[WK], fd[2][WM];
-    // weights: segment WK wk + i of row 8 lg + r / 4 of a step, and of the row four
-    // on; WK wk + i and i differ in bits that turn() leaves alone or by an XOR too
-    const int row_t = 8 * lg + (r >> 2);
-    const uint32_t turned = 32 * ((WK * wk) ^ grad_turn(row_t)) + 8 * (r & 3) + 2 * L::BN * row_t;
-    auto read_w = [&](int slot, int half, int i) __attribute__((always_inline)) {
-        const uint8_t *p = wide0 + (turned ^ (32 * i)) + slot * L::kWide + half * (64 * L::BN);
-        const v4s lo = read_turned(p), hi = read_turned(p + 8 * L::BN);
-        fw[i] = __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    v4u fw[2][2];                                    // of a step, and of the next
+    v8bf fd[WM];
+    // weights: rows 8 lg .. of a step, columns of block `wave`
+    v2u raw;
+    v4f32 scales[2];
+    const int row_t = 8 * lg + (r >> 1);
+    const uint8_t *const at_w = codes0 + row_t * L::kRow + 16 * L::place(wave, row_t) + 8 * (r & 1);
+    const uint8_t *const at_s = codes0 + kStep * L::kRow + wave * L::kScales + 32 * lg;
+    auto read_w = [&](int slot, int half) __attribute__((always_inline)) {
+        raw = read_turned(at_w + slot * L::kSlot + half * (32 * L::kRow));
+        scales[0] = *reinterpret_cast<const v4f32 *>(at_s + slot * L::kSlot + 128 * half);
+        scales[1] = *reinterpret_cast<const v4f32 *>(at_s + slot * L::kSlot + 128 * half + 16);
     };
-    const uint8_t *const at_d0 = smem + 128 * (16 * WM * wm + r) + 16 * (lg ^ grad_swizzle(r));
-    const uint8_t *const at_d1 = smem + 128 * (16 * WM * wm + r) + 16 * ((4 + lg) ^ grad_swizzle(r));
+    auto expand = [&](int half) __attribute__((always_inline)) {
+        expand4<0>(raw, scales, fw[half][0], fw[half][1]);
+        expand4<1>(raw, scales, fw[half][0], fw[half][1]);
+        expand4<2>(raw, scales, fw[half][0], fw[half][1]);
+        expand4<3>(raw, scales, fw[half][0], fw[half][1]);
+    };
+    const uint8_t *const at_d0 = smem + 128 * r + 16 * (lg ^ grad_swizzle(r));
+    const uint8_t *const at_d1 = smem + 128 * r + 16 * ((4 + lg) ^ grad_swizzle(r));
     auto read_d = [&](int slot, int half, int j) __attribute__((always_inline)) {
-        fd[half][j] = *reinterpret_cast<const v8bf *>((half ? at_d1 : at_d0) + slot * L::kD + 2048 * j);
+        fd[j] = *reinterpret_cast<const v8bf *>((half ? at_d1 : at_d0) + slot * L::kD + 2048 * j);
     };
 
     load_d(s0, 0);
     load_w(s0);
     store_d(0);
-    expand(s0 & 1);
+    store_w(s0 & 1);
     int ahead_s = parts > 1 ? s0 : s0 + 1, ahead_p = parts > 1 ? 1 : 0;          // the tile that is held
     load_d(ahead_s, ahead_p);
     load_w(s0 + 1);
     ring_barrier();
-#pragma unroll
-    for (int i = 0; i < WK; ++i) read_w(s0 & 1, 0, i);
+    read_w(s0 & 1, 0);
 #pragma unroll
     for (int j = 0; j < WM; ++j) read_d(0, 0, j);
+    expand(0);
 
-    constexpr int kLead = WK / 4;                    // column tiles multiplied before the barrier
+    constexpr int kLead = WM / 4;                 // token tiles multiplied before the barrier
     int s = s0, p = 0;
     for (int t = 0; s < s1; ++t) {
         const int slot = t & 1, slot_w = s & 1;
-        auto products = [&](int half, int i) __attribute__((always_inline)) {
+        const bool turn = p + 1 == parts;            // the next tile is of the next stage
+        auto products = [&](int half, int j) __attribute__((always_inline)) {
 #pragma unroll
-            for (int j = 0; j < WM; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[i], fd[half][j], acc[i][j], 0, 0, 0);
+            for (int i = 0; i < 2; ++i)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, fw[half][i]), fd[j],
+                                                                    acc[i][j], 0, 0, 0);
         };
         // first step
+        read_w(slot_w, 1);
 #pragma unroll
-        for (int j = 0; j < WM; ++j) read_d(slot, 1, j);
-#pragma unroll
-        for (int i = 0; i < WK; ++i) {
-            products(0, i);
-            read_w(slot_w, 1, i);
-            // wide: the two waves of a SIMD, wave and wave + W / 2, not at once (684 -> 645
-            // us at 2048 x 34816 x 5120). Small: a block has one wave on each
-            if (i == 0 ? !L::kTwo || wave < W / 2 : L::kTwo && i == WK / 2 && wave >= W / 2) {
+        for (int j = 0; j < WM; ++j) {
+            products(0, j);
+            read_d(slot, 1, j);
+            // wide: the two waves of a SIMD, wave and wave + W / 2, not at once. Small: a
+            // block has one wave on each
+            if (j == 0 ? !L::kTwo || wave < W / 2 : L::kTwo && j == WM / 2 && wave >= W / 2) {
                 __builtin_amdgcn_sched_barrier(0);
                 store_d(slot ^ 1);
                 ++ahead_p;
@@ -434,31 +448,28 @@ void grad_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__res
                     ++ahead_s;
                 }
                 load_d(ahead_s, ahead_p);
-                // in a stage's first tile or in its last, as measured: wide 616 us at 4096 x
-                // 5120 x 17408 (628 in the last), small 116 at 128 x 5120 x 17408 float32 (134)
-                if (L::kTwo ? p == 0 : p + 1 == parts) {
-                    expand(slot_w ^ 1);
+                if (turn) {
+                    store_w(slot_w ^ 1);
                     load_w(s + 2);
                 }
             }
         }
+        expand(1);
         __builtin_amdgcn_sched_barrier(0);
         // second step
 #pragma unroll
-        for (int i = 0; i < kLead; ++i) products(1, i);
+        for (int j = 0; j < kLead; ++j) products(1, j);
         __builtin_amdgcn_sched_barrier(0);
         ring_barrier();                              // the next tile is there, this one is read
-        const bool turn = p + 1 == parts;
-        const int next_w = (turn ? s + 1 : s) & 1;
+        read_w((turn ? s + 1 : s) & 1, 0);
 #pragma unroll
-        for (int j = 0; j < WM; ++j) read_d(slot ^ 1, 0, j);
+        for (int j = 0; j < kLead; ++j) read_d(slot ^ 1, 0, j);
 #pragma unroll
-        for (int i = 0; i < kLead; ++i) read_w(next_w, 0, i);
-#pragma unroll
-        for (int i = kLead; i < WK; ++i) {
-            products(1, i);
-            read_w(next_w, 0, i);
+        for (int j = kLead; j < WM; ++j) {
+            products(1, j);
+            read_d(slot ^ 1, 0, j);
         }
+        expand(0);
         __builtin_amdgcn_sched_barrier(0);
         s += turn;
         p = turn ? 0 : p + 1;
@@ -466,14 +477,13 @@ void grad_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__res
     end_grad<L>(o, plan, share, acc, wave, lane);
 }
 
-// A launch holds fewer than 2^32 threads: the kernels go round again.
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // Whether d is read where it lies: bfloat16 rows of whole 16-byte units.
 bool in_place(int64_t N, int format) { return format == kBf16 && N % 8 == 0; }
 
-typedef GradTile<8, 4, 2, 4> GradWide;     // 256 x 256
-typedef GradTile<4, 2, 2, 2> GradSmall;    // 128 x 64
+typedef GradTile<16, 8> GradWide;     // 256 x 256
+typedef GradTile<4, 4> GradSmall;    // 128 x 64
 
 // The tile for a shape: the least of plan_tiles's counts.
 bool choose_wide(int64_t M, int64_t N, int64_t K, int parts, size_t bytes, MxPlan &plan) {
@@ -491,7 +501,7 @@ hipError_t run_grad(const GradRows &d, const Mx4GradArgs &a, MxPlan p, void *wor
     const hipError_t e = hipGetLastError();
     const int rest = p.tiles_n * p.tiles_m - p.full;
     if (e != hipSuccess || rest == 0) return e;
-    hipLaunchKernelGGL(grad_sum_kernel<L>, dim3((unsigned)(rest * L::WK)), dim3(L::T), 0, stream, o, p);
+    hipLaunchKernelGGL(grad_sum_kernel<L>, dim3((unsigned)(rest * (L::WM / L::kNJ))), dim3(L::T), 0, stream, o, p);
     return hipGetLastError();
 }
 

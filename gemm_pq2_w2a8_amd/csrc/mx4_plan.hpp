@@ -52,26 +52,27 @@ __device__ __forceinline__ MxShare share_of(const MxPlan &p) {
     return s;
 }
 
-// A share's sums, acc[I][J] of a block of T threads.
+// A share's sums, acc[I][J] of a block of T threads, as far as j < live.
 template <int I, int J, int T>
-__device__ __forceinline__ void store_share(const MxPlan &p, int item, int tid, const v4f32 (&acc)[I][J]) {
+__device__ __forceinline__ void store_share(const MxPlan &p, int item, int tid, int live, const v4f32 (&acc)[I][J]) {
     float *const to = p.part + (int64_t)item * (I * J * T * 4) + 4 * tid;
 #pragma unroll
     for (int i = 0; i < I; ++i)
 #pragma unroll
-        for (int j = 0; j < J; ++j) *reinterpret_cast<v4f32 *>(to + (i * J + j) * (4 * T)) = acc[i][j];
+        for (int j = 0; j < J; ++j)
+            if (j < live) *reinterpret_cast<v4f32 *>(to + (i * J + j) * (4 * T)) = acc[i][j];
 }
 
-// Rows i0 .. i0 + NI - 1 of split tile `index`, its shares added in order, four
-// requested at a time.
-template <int NI, int I, int J, int T>
-__device__ __forceinline__ void sum_shares(const MxPlan &p, int index, int i0, int tid, v4f32 (&acc)[NI][J]) {
+// acc[i0 .. i0 + NI - 1][j0 .. j0 + NJ - 1] of split tile `index`, its shares
+// added in order, four requested at a time.
+template <int I, int J, int T, int NI, int NJ>
+__device__ __forceinline__ void sum_shares(const MxPlan &p, int index, int i0, int j0, int tid, v4f32 (&acc)[NI][NJ]) {
     const float *const from = p.part + (int64_t)index * p.ways * (I * J * T * 4) + 4 * tid;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const float *const at = from + ((i0 + i) * J + j) * (4 * T);
+        for (int j = 0; j < NJ; ++j) {
+            const float *const at = from + ((i0 + i) * J + j0 + j) * (4 * T);
             v4f32 sum = *reinterpret_cast<const v4f32 *>(at);
             for (int way = 1; way < p.ways; way += 4) {
                 v4f32 v[4];
