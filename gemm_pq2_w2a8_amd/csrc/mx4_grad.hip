@@ -188,14 +188,15 @@ __global__ __launch_bounds__(256) void grad_rows_kernel(const void *dy, const vo
 // tokens rolling, each tile's registers taking the next step's as soon as its
 // products are issued. In the first step of a stage the next stage's tile is
 // stored and the one after requested; a barrier in the second shows it to all.
-// 4096 x 5120 x 17408 bfloat16 581 us with 256 x 256 tiles (1.26 PFLOP/s; a library
-// product of bfloat16 matrices 1.44); 128 x 34816 x 5120 82 with 128 x 64. Every
+// 4096 x 5120 x 17408 bfloat16 573 us with 256 x 256 tiles (1.27 PFLOP/s; a library
+// product of bfloat16 matrices 1.44); 128 x 34816 x 5120 78 with 128 x 64. Every
 // other instruction shares the SIMD's issue with the matrix instructions: the loop of
 // waves of 64 columns x half the tokens, with parts left out, took 358 us for those
 // alone, 99 more with the conversions, 31 with the reads of d, 40 with the stores to
 // LDS, 73 with the requests, 17 with their latency, 619 in all. From there scales as
-// float32 instead of bytes (no shifts: 608) and the waves of 32 columns (half the
-// conversions, twice the reads of d: 581). Before it, weights expanded to bfloat16 in
+// float32 instead of bytes (no shifts: 608), the waves of 32 columns (half the
+// conversions, twice the reads of d: 591), addresses stepped instead of formed anew
+// (580) and products at a higher priority (573). Before it, weights expanded to bfloat16 in
 // LDS once a block and read transposed from there: 616 and 92 us, LDS and conversions;
 // and buffer -> LDS copies, which the compiler waits for before a transposing read:
 // 1009 us instead of 708.
@@ -204,14 +205,14 @@ struct GradTile {
     static constexpr int WM = WM_, W = W_, T = kWave * W;
     static constexpr int BN = 32 * W, BM = 16 * WM;
     static constexpr int kD = BM * 128;                  // bytes of a tile of d
-    static constexpr int kRow = BN / 2;          // bytes of a row n of codes
-    static constexpr int kScales = 4 * kStep + 32;            // bytes of a block's scales, one for each n
+    static constexpr int kRow = BN / 2;                  // bytes of a row n of codes
+    static constexpr int kScales = 4 * kStep + 32;    // bytes of a block's scales, one for each n
     static constexpr int kSlot = kStep * kRow + W * kScales;
     static constexpr int kLdsBytes = 2 * (kD + kSlot);
     static constexpr int kRows = BM / 8 / W;             // 16-byte pieces of d's tile a thread moves
     static constexpr bool kTwo = W == 8;                 // two waves a SIMD (wide)
     static constexpr int kBlocks = kTwo ? 1 : 3;         // a compute unit holds
-    static constexpr int kRun = kTwo ? 1470 : 565, kMore = kTwo ? 180 : 400,
+    static constexpr int kRun = kTwo ? 1450 : 500, kMore = kTwo ? 170 : 380,
                          kEnds = kTwo ? 5000 : 2500;     // plan_tiles's times
     static constexpr int kNJ = WM / 4;                    // instruction tiles of tokens a block sums
     static_assert(kRows * W * 8 == BM && kStep * W == T && kSlot % 16 == 0, "a thread moves one block");
@@ -339,8 +340,11 @@ void grad_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__res
     const int off = sub * row_bytes + 16 * unit;
     const uint16_t *const base_d = d.d + (m0 + 8 * wave) * d.cols;
     v4u held[NR];                                    // the tile of d after the next
+    const uint16_t *next_d = base_d + (int64_t)s0 * kStep;       // the tile that is loaded next
+    const int64_t turn_d = kStep - (parts - 1) * d.plane;
     auto load_d = [&](int s, int p) __attribute__((always_inline)) {
-        const uint16_t *from = base_d + p * d.plane + (int64_t)s * kStep;
+        const uint16_t *from = next_d;
+        next_d += p + 1 == parts ? turn_d : d.plane;
         const int at = s < s1 && (int64_t)s * kStep + 8 * unit < d.n ? off : kCopyOob;
 #pragma unroll
         for (int i = 0; i < NR; ++i)
@@ -357,17 +361,19 @@ void grad_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__res
     const bool live_w = 32 * unit_w < cols;
     v4u codes;
     uint32_t byte;
+    const uint8_t *next_w = w + (int64_t)s0 * kStep * kb + k0 / 2;
+    const uint8_t *next_s = ws + (int64_t)s0 * kStep * (kb / 16) + k0 / kMxBlock;
     auto load_w = [&](int s) __attribute__((always_inline)) {
         const int64_t n0 = (int64_t)s * kStep;
         const int rows = s < s1 ? (int)(N - n0 < kStep ? N - n0 : kStep) : 0;
         const bool live = live_w && row_w < rows;
-        const int64_t first = rows ? n0 : 0;
-        const __amdgpu_buffer_rsrc_t rs = make_rsrc(w + first * kb + k0 / 2, rows ? (int64_t)(rows - 1) * kb + cols / 2 : 0);
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(next_w, rows * kb);
         codes = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(
             rs, live ? row_w * kb + 16 * unit_w : kCopyOob, 0, 0));
         const int sb = kb / 16;
-        const __amdgpu_buffer_rsrc_t rss =
-            make_rsrc(ws + first * sb + k0 / kMxBlock, rows ? (int64_t)(rows - 1) * sb + cols / kMxBlock : 0);
+        const __amdgpu_buffer_rsrc_t rss = make_rsrc(next_s, rows * sb);
+        next_w += kStep * kb;
+        next_s += kStep * sb;
         byte = __builtin_amdgcn_raw_buffer_load_b8(rss, live ? row_w * sb + unit_w : kCopyOob, 0, 0);
     };
     const uint32_t to_codes = row_w * L::kRow + 16 * L::place(unit_w, row_w);
@@ -435,7 +441,9 @@ void grad_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__res
         read_w(slot_w, 1);
 #pragma unroll
         for (int j = 0; j < WM; ++j) {
+            __builtin_amdgcn_s_setprio(1);           // this wave's products before the other's rest
             products(0, j);
+            __builtin_amdgcn_s_setprio(0);
             read_d(slot, 1, j);
             // wide: the two waves of a SIMD, wave and wave + W / 2, not at once. Small: a
             // block has one wave on each
@@ -466,7 +474,9 @@ void grad_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__res
         for (int j = 0; j < kLead; ++j) read_d(slot ^ 1, 0, j);
 #pragma unroll
         for (int j = kLead; j < WM; ++j) {
+            __builtin_amdgcn_s_setprio(1);
             products(1, j);
+            __builtin_amdgcn_s_setprio(0);
             read_d(slot ^ 1, 0, j);
         }
         expand(0);
