@@ -35,18 +35,21 @@ struct MxShare {
     int q0, q1;                       // runs of this block
 };
 
-// Whole tiles come first; each XCD takes a contiguous run of either kind.
+// Whole tiles come first; each XCD takes a contiguous run of either kind, of shares
+// in the order of the runs, so that its tiles at a time are multiplied over the same
+// columns.
 __device__ __forceinline__ MxShare share_of(const MxPlan &p) {
     MxShare s;
     const int whole = (p.full + 7) / 8 * 8;
     s.split = (int)blockIdx.x >= whole;
     const int b = s.split ? blockIdx.x - whole : blockIdx.x;
     const int count = s.split ? (p.tiles_n * p.tiles_m - p.full) * p.ways : p.full;
-    s.item = (b & 7) * ((count + 7) / 8) + (b >> 3);
-    s.live = s.item < count;
+    const int at = (b & 7) * ((count + 7) / 8) + (b >> 3);
+    s.live = at < count;
     if (!s.live) return s;
-    const int ways = s.split ? p.ways : 1, way = s.split ? s.item % p.ways : 0;
-    tile_at(p, s.split ? p.full + s.item / p.ways : s.item, s.tn, s.tm);
+    const int ways = s.split ? p.ways : 1, tiles = count / ways, way = at / tiles, t = at - way * tiles;
+    s.item = t * ways + way;
+    tile_at(p, s.split ? p.full + t : t, s.tn, s.tm);
     s.q0 = __builtin_amdgcn_readfirstlane((int)((uint32_t)p.runs * way / ways));
     s.q1 = __builtin_amdgcn_readfirstlane((int)((uint32_t)p.runs * (way + 1) / ways));
     return s;

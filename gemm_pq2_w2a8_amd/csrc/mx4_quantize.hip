@@ -10,7 +10,8 @@
 // of a block exchange their largest value in the VALU (quad permutes). The
 // largest is taken over bit patterns, whose order as integers is that of the
 // magnitudes with infinities and NaN on top, so that one compare finds both.
-// Bound by HBM; for a few rows by the launch.
+// Bound by HBM: 4096 x 17408 bfloat16 42 us (4.3 TB/s), back 27 (from the caches, what
+// was just written). One row of 5120: 1.6 us each, a launch.
 #include "mx4_device.hpp"
 #include "mx4_launch.hpp"
 
