@@ -535,8 +535,9 @@ hipError_t run_rows(const Mx4GradArgs &a, void *dgu, uint16_t *out, int64_t cols
     if (a.gu)
         return eight ? launch_rows<FMT, true, 8>(a, dgu, out, cols, stream)
                      : launch_rows<FMT, true, 1>(a, dgu, out, cols, stream);
-    return eight ? launch_rows<FMT, false, 8>(a, dgu, out, cols, stream)
-                 : launch_rows<FMT, false, 1>(a, dgu, out, cols, stream);
+    if constexpr (FMT != kBf16)                      // such rows of bfloat16 are read in place
+        if (eight) return launch_rows<FMT, false, 8>(a, dgu, out, cols, stream);
+    return launch_rows<FMT, false, 1>(a, dgu, out, cols, stream);
 }
 
 }  // namespace

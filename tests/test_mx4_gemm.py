@@ -164,7 +164,9 @@ def test_gemm_exact(M, N, K):
 @pytest.mark.parametrize("M,N,K,gated", [
     (33, 5120, 17408, False), (100, 1000, 8192, False), (130, 5120, 17408, False), (500, 5120, 17408, False),
     (1000, 5120, 6144, False), (1000, 17408, 1152, False), (4096, 4352, 8192, False), (2000, 8704, 5120, False),
-    (40, 2048, 17408, True), (300, 8704, 5120, True), (1030, 2176, 8192, True), (4000, 2200, 5120, True)])
+    (40, 2048, 17408, True), (300, 8704, 5120, True), (1030, 2176, 8192, True), (4000, 2200, 5120, True),
+    (256, 5120, 17408, True), (300, 2560, 17408, True), (1024, 1024, 17408, True), (2048, 8704, 5120, True),
+    (2048, 8704, 1152, True), (1000, 8704, 5120, True)])
 def test_plans_agree(M, N, K, gated):
     """Every tile, whole and split along K in any workspace: with all scales alike
     nothing is rounded, so the results are the same bits; some rows against
