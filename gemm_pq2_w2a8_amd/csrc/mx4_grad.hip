@@ -211,10 +211,10 @@ struct GradTile {
     static constexpr int kLdsBytes = 2 * (kD + kSlot);
     static constexpr int kRows = BM / 8 / W;             // 16-byte pieces of d's tile a thread moves
     static constexpr bool kTwo = W == 8;                 // two waves a SIMD (wide)
-    static constexpr int kBlocks = kTwo ? 1 : 3;         // a compute unit holds
-    static constexpr int kRun = kTwo ? 1450 : 500, kMore = kTwo ? 170 : 380,
+    static constexpr int kBlocks = kTwo ? 1 : WM == 4 ? 3 : 5;    // a compute unit holds
+    static constexpr int kRun = kTwo ? 1450 : WM == 4 ? 490 : 440, kMore = kTwo ? 170 : WM == 4 ? 390 : 900,
                          kEnds = kTwo ? 5000 : 2500;     // plan_tiles's times
-    static constexpr int kNJ = WM / 4;                    // instruction tiles of tokens a block sums
+    static constexpr int kNJ = WM < 4 ? 1 : WM / 4;     // instruction tiles of tokens a block sums
     static_assert(kRows * W * 8 == BM && kStep * W == T && kSlot % 16 == 0, "a thread moves one block");
 
     // where unit u of row n of the codes lies in the row
@@ -494,13 +494,20 @@ bool in_place(int64_t N, int format) { return format == kBf16 && N % 8 == 0; }
 
 typedef GradTile<16, 8> GradWide;     // 256 x 256
 typedef GradTile<4, 4> GradSmall;    // 128 x 64
+typedef GradTile<2, 4> GradFew;      // 128 x 32
 
-// The tile for a shape: the least of plan_tiles's counts.
-bool choose_wide(int64_t M, int64_t N, int64_t K, int parts, size_t bytes, MxPlan &plan) {
+// f(a tile's type, its plan) for a shape's tile: the small one's or the wide one's,
+// the less of plan_tiles's counts; where 32 tokens are all, the one that holds no
+// more, five blocks a unit instead of three (16 x 5120 x 17408 float32 38 us instead of
+// 50; bfloat16 16 x 34816 x 5120 36 instead of 42 with weights in the caches, 47 instead
+// of 48 without; 64 x 5120 x 17408, two tiles down, 33 instead of 29).
+template <class F>
+auto with_tile(int64_t M, int64_t N, int64_t K, int parts, size_t bytes, F f) {
     const int64_t stages = (N + kStep - 1) / kStep;
-    const MxCost s = plan_tiles<GradSmall>(M, K, stages, bytes, parts), w = plan_tiles<GradWide>(M, K, stages, bytes, parts);
-    plan = w.ns <= s.ns ? w.plan : s.plan;
-    return w.ns <= s.ns;
+    if (M <= GradFew::BM) return f(GradFew(), plan_tiles<GradFew>(M, K, stages, bytes, parts).plan);
+    const MxCost small = plan_tiles<GradSmall>(M, K, stages, bytes, parts),
+                 wide = plan_tiles<GradWide>(M, K, stages, bytes, parts);
+    return wide.ns <= small.ns ? f(GradWide(), wide.plan) : f(GradSmall(), small.plan);
 }
 
 template <class L>
@@ -549,9 +556,8 @@ size_t mx4_grad_least_bytes(int64_t M, int64_t N, int format, bool gated, bool k
 
 size_t mx4_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int format, bool gated,
                                 bool keeps_dgu) {
-    MxPlan p;
-    const bool wide = choose_wide(M, N, K, parts_of(format), SIZE_MAX, p);
-    return mx4_grad_least_bytes(M, N, format, gated, keeps_dgu) + (wide ? part_bytes<GradWide>(p) : part_bytes<GradSmall>(p));
+    return mx4_grad_least_bytes(M, N, format, gated, keeps_dgu) +
+           with_tile(M, N, K, parts_of(format), SIZE_MAX, [](auto tile, const MxPlan &p) { return part_bytes<decltype(tile)>(p); });
 }
 
 hipError_t launch_mx4_grad(const Mx4GradArgs &a, void *work, size_t work_bytes, hipStream_t stream) {
@@ -580,10 +586,9 @@ hipError_t launch_mx4_grad(const Mx4GradArgs &a, void *work, size_t work_bytes, 
                               : run_rows<kF16>(a, a.dgu, rows, d.cols, stream);
     }
     if (e != hipSuccess) return e;
-    MxPlan p;
-    const bool wide = choose_wide(a.M, a.N, a.K, d.parts, work_bytes - least, p);
-    void *const sums = p.ways > 1 ? static_cast<uint8_t *>(work) + least : nullptr;
-    return wide ? run_grad<GradWide>(d, a, p, sums, stream) : run_grad<GradSmall>(d, a, p, sums, stream);
+    return with_tile(a.M, a.N, a.K, d.parts, work_bytes - least, [&](auto tile, const MxPlan &p) {
+        return run_grad<decltype(tile)>(d, a, p, p.ways > 1 ? static_cast<uint8_t *>(work) + least : nullptr, stream);
+    });
 }
 
 }  // namespace pq2

@@ -144,7 +144,7 @@ def test_gemm_grad_exact(M, N, K, ty):
 @pytest.mark.gpu
 @pytest.mark.parametrize("ty", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("M,N,K", [(1, 17408, 1024), (33, 5120, 17408), (300, 5120, 6144), (1000, 2048, 17408),
-                                   (2048, 2048, 8704), (4000, 1000, 5120)])
+                                   (2048, 2048, 8704), (4000, 1000, 5120), (32, 34816, 1024), (17, 1000, 17408)])
 def test_plans_agree(M, N, K, ty):
     """Both tiles, whole and split along N in any workspace: small integers, no
     rounding but the output's, so the same bits; some rows against float64."""
