@@ -255,9 +255,10 @@ def _format(x: torch.Tensor, name: str) -> int:
 
 
 def _mk(x: torch.Tensor) -> Tuple[int, int]:
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("expected a 2-D tensor")
-    return int(x.shape[0]), int(x.shape[1])
+    return shape[0], shape[1]
 
 
 def pq2_quantize_act(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, t: torch.Tensor,
