@@ -122,7 +122,10 @@ __device__ __forceinline__ void gate_act_slope(float g, float &a, float &d) {
     } else {
         const float s = logistic(gelu_inner(g));
         a = g * s;
-        d = s + a * (1.0f - s) * (1.5957691216057308f * (1.0f + 0.134145f * g * g));
+        // from 20 on s is 0 or 1 and the second term 0; g's square would make it NaN
+        // once infinite (max and min drop a NaN of g, which s has)
+        const float c = fminf(fmaxf(g, -20.0f), 20.0f);
+        d = s + c * s * (1.0f - s) * (1.5957691216057308f * (1.0f + 0.134145f * c * c));
     }
 }
 
