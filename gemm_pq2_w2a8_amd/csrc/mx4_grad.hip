@@ -116,6 +116,13 @@ __device__ __forceinline__ void round_values(void *x, int64_t at, float (&v)[V])
     }
 }
 
+// v u s with a slope s (at most 1.13): where the first product overflows although its
+// factors are finite, both exceed 1, and with s near 0 the whole may still be finite.
+__device__ __forceinline__ float times_slope(float v, float u, float s) {
+    const float p = v * u;
+    return fabsf(p) == INFINITY && fabsf(v) != INFINITY ? v * (u * s) : p * s;
+}
+
 // What multiplies the weights: d's parts, for a gated block from dh, g and u, whose
 // dgu it writes too (dgu may be gu). V columns a thread: eight where rows of F
 // columns keep 16-byte addresses (2048 x 17408 bfloat16 116 us one by one, 55 by
@@ -147,7 +154,7 @@ __global__ __launch_bounds__(256) void grad_rows_kernel(const void *dy, const vo
                 for (int e = 0; e < V; ++e) {
                     float a, s;
                     gate_act_slope<kind.value>(g[e], a, s);
-                    dg[e] = v[e] * u[e] * s;
+                    dg[e] = times_slope(v[e], u[e], s);
                     du[e] = v[e] * a;
                 }
             };

@@ -7,6 +7,8 @@ integer or zero, nothing is rounded and results are compared for equality."""
 import pytest
 import torch
 
+from oracle import mx4
+
 pq2 = pytest.importorskip("gemm_pq2_w2a8_amd")
 
 import test_mx4_grad as grad  # noqa: E402
@@ -37,4 +39,27 @@ def test_slopes_of_gates_whose_square_is_infinite(ty, act):
     assert torch.equal(dgu[0, :F].float(), torch.where(g > 0, t, 0.0))
     assert torch.equal(dgu[0, F:], torch.where(g > 0, g * t, torch.zeros_like(g)))
     assert torch.isfinite(dx).all()
+    grad.check(dx, *grad.product(dgu, grad.decoded(*w), ty), ty)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act,g", [("silu", -50.0), ("gelu", -10.0), ("gelu_tanh", -5.5)])
+@pytest.mark.parametrize("ty", ["bf16", "f32"])
+def test_slopes_near_zero_of_large_gradients(ty, act, g):
+    """dh u is infinite in float32, times the slope it is not: the activation's
+    relative (10 + 3 max(|z|, g^2)) 2^-23 of test_mx4_grad.py, |z| <= 21 and g^2 <=
+    100 but for silu, which has no g^2, on a slope of two terms of which one is the
+    other's g-fold: below 2^-13 in all. Slopes that are 0 give zeros."""
+    F, big = 64, 1e20
+    gates = torch.tensor([g, -1e3, -1e10, g]).repeat(F // 4).to(TYPES[ty]).cuda()
+    dh = torch.full((2, F), big, dtype=TYPES[ty], device="cuda")
+    dh[1] = -dh[0]
+    gu = torch.cat([gates, torch.full_like(gates, big)]).repeat(2, 1)
+    w = grad.weights(2 * F, 128, 1)
+    dx, dgu = gated_grad(dh, gu, act, w)
+    slope = torch.from_numpy(mx4.act(act, gates.double().cpu().numpy())[1]).cuda()
+    want = dh.double() * gu[:, F:].double() * slope
+    assert (dgu[:, :F][:, gates < -100] == 0).all()
+    off = (dgu[:, :F].double() - want).abs()
+    assert (off <= (2.0 ** -13 + grad.HALF[ty]) * want.abs()).all()
     grad.check(dx, *grad.product(dgu, grad.decoded(*w), ty), ty)
