@@ -5,7 +5,8 @@
 //   gated:  du = dh act(g),  dg = dh u act'(g),  d = (dg | du), n over 2 F
 //
 // The sum runs along n, across the weights' blocks of scales, so the weights
-// are expanded to bfloat16, in which every one of them is exact, and multiplied
+// are expanded to bfloat16, in which every one of them is exact (subnormal ones
+// too; those beyond its range lend d a factor, see split_scale), and multiplied
 // by bfloat16 matrix instructions with float32 sums. d enters without a
 // rounding of its own: bfloat16 as it is, float16 and float32 split into two
 // and three bfloat16 parts that add up to it exactly (truncated, so that no
@@ -215,7 +216,8 @@ struct GradTile {
     static constexpr int kRow = BN / 2;                  // bytes of a row n of codes
     static constexpr int kScales = 4 * kStep + 32;    // bytes of a block's scales, one for each n
     static constexpr int kSlot = kStep * kRow + W * kScales;
-    static constexpr int kLdsBytes = 2 * (kD + kSlot);
+    static constexpr int kOver = 2 * (kD + kSlot);       // whether the block met a scale beyond 2^125
+    static constexpr int kLdsBytes = kOver + 16;
     static constexpr int kRows = BM / 8 / W;             // 16-byte pieces of d's tile a thread moves
     static constexpr bool kTwo = W == 8;                 // two waves a SIMD (wide)
     static constexpr int kBlocks = kTwo ? 1 : WM == 4 ? 3 : 5;    // a compute unit holds
@@ -244,6 +246,44 @@ __device__ __forceinline__ void expand4(v2u codes, const v4f32 (&scales)[2], v4u
     const uint32_t a = expand2<2 * J>(codes, scales), b = expand2<2 * J + 1>(codes, scales);
     even[J] = __builtin_amdgcn_perm(b, a, 0x05040100u);
     odd[J] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+}
+
+// Scales beyond 2^125 make weights that bfloat16 does not hold. A wave's weights of a
+// row n are one block, so such a row can be expanded under 2^125 and the rest of its
+// scale, 2 or 4, multiply the row's values of d. The exponent of that rest lies in the
+// low bits of the scale, which the conversions do not read. 255 (NaN) stays.
+constexpr uint32_t kTopByte = 252;
+__device__ __forceinline__ bool is_over(uint32_t byte) { return byte - (kTopByte + 1) < 2u; }
+__device__ __forceinline__ uint32_t split_scale(uint32_t byte) {
+    return is_over(byte) ? kTopByte << 23 | (byte - kTopByte) : byte << 23;
+}
+
+// The exponents of the rests of eight rows' scales, two bits each.
+__device__ __forceinline__ uint32_t rests_of(const v4f32 (&scales)[2]) {
+    uint32_t all = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) all |= (bits_of(scales[i / 4][i % 4]) & 3u) << (2 * i);
+    return all;
+}
+
+// Eight values of d by their rows' rests. A finite one that overflows becomes the
+// largest finite one: by a weight of 2^124 or more it is infinite all the same, by 0
+// it is 0.
+__device__ __forceinline__ v8bf lifted(v8bf d, uint32_t rests) {
+    v4u w = __builtin_bit_cast(v4u, d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t out = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float x = as_float(h ? w[i] & 0xffff0000u : w[i] << 16);
+            uint32_t b = bits_of(ldexpf(x, (int)(rests >> (2 * (2 * i + h)) & 3u)));
+            if ((b & 0x7fffffffu) == 0x7f800000u && fabsf(x) != INFINITY) b = (b & 0x80000000u) | 0x7f7f0000u;
+            out |= h ? b & 0xffff0000u : b >> 16;
+        }
+        w[i] = out;
+    }
+    return __builtin_bit_cast(v8bf, w);
 }
 
 // Sixteen bytes of eight rows, transposed: lane i of 16 gives the address of eight
@@ -328,6 +368,8 @@ void grad_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__res
     const int r = lane & 15, lg = lane >> 4;
     const MxShare share = share_of(plan);
     if (!share.live) return;
+    int *const met = reinterpret_cast<int *>(smem + L::kOver);
+    if (tid == 0) *met = 0;
     const int64_t M = o.M, N = o.N, K = o.K, m0 = (int64_t)share.tm * L::BM;
     const int k0 = share.tn * L::BN, s0 = share.q0, s1 = share.q1;
     const int parts = d.parts;
@@ -368,6 +410,7 @@ void grad_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__res
     const bool live_w = 32 * unit_w < cols;
     v4u codes;
     uint32_t byte;
+    bool over = false;                               // a scale of the thread's was
     const uint8_t *next_w = w + (int64_t)s0 * kStep * kb + k0 / 2;
     const uint8_t *next_s = ws + (int64_t)s0 * kStep * (kb / 16) + k0 / kMxBlock;
     auto load_w = [&](int s) __attribute__((always_inline)) {
@@ -388,6 +431,7 @@ void grad_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__res
     auto store_w = [&](int slot) __attribute__((always_inline)) {
         *reinterpret_cast<v4u *>(codes0 + slot * L::kSlot + to_codes) = codes;
         *reinterpret_cast<uint32_t *>(codes0 + slot * L::kSlot + to_scale) = byte << 23;
+        over |= is_over(byte);
     };
 
     v4f32 acc[2][WM];
@@ -490,6 +534,50 @@ void grad_kernel(GradRows d, const uint8_t *__restrict__ w, const uint8_t *__res
         __builtin_amdgcn_sched_barrier(0);
         s += turn;
         p = turn ? 0 : p + 1;
+    }
+    // A scale beyond 2^125, which the quantiser does not write: the whole sum again, one
+    // tile at a time, with the rests on d. The loop above only notes that there was one
+    // (4096 x 5120 x 17408 594 -> 599 us; lifting d in that loop, in a branch, spilled 64
+    // of its registers).
+    if (__any(over) && lane == 0) *met = 1;          // cleared before the first barrier
+    ring_barrier();
+    if (__builtin_amdgcn_readfirstlane(*met)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < WM; ++j) acc[i][j] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+        next_d = base_d + (int64_t)s0 * kStep;
+        next_w = w + (int64_t)s0 * kStep * kb + k0 / 2;
+        next_s = ws + (int64_t)s0 * kStep * (kb / 16) + k0 / kMxBlock;
+        for (s = s0; s < s1; ++s) {
+            load_w(s);
+            for (p = 0; p < parts; ++p) {
+                load_d(s, p);
+                ring_barrier();                      // the last tile is read
+                store_d(0);
+                if (p == 0) {
+                    *reinterpret_cast<v4u *>(codes0 + to_codes) = codes;
+                    *reinterpret_cast<uint32_t *>(codes0 + to_scale) = split_scale(byte);
+                }
+                ring_barrier();
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    read_w(0, half);
+                    expand(half);
+                    const uint32_t rests = rests_of(scales);
+#pragma unroll
+                    for (int j = 0; j < WM; ++j) {
+                        read_d(0, half, j);
+                        fd[j] = lifted(fd[j], rests);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                __builtin_bit_cast(v8bf, fw[half][i]), fd[j], acc[i][j], 0, 0, 0);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+            }
+        }
     }
     end_grad<L>(o, plan, share, acc, wave, lane);
 }

@@ -4,6 +4,7 @@ of two or an expanded weight leaves float32 although the result does not.
 Bounds are those of test_mx4_grad.py; where everything is a power of two, a small
 integer or zero, nothing is rounded and results are compared for equality."""
 
+import numpy as np
 import pytest
 import torch
 
@@ -63,3 +64,40 @@ def test_slopes_near_zero_of_large_gradients(ty, act, g):
     off = (dgu[:, :F].double() - want).abs()
     assert (off <= (2.0 ** -13 + grad.HALF[ty]) * want.abs()).all()
     grad.check(dx, *grad.product(dgu, grad.decoded(*w), ty), ty)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ty", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(5, 64, 128), (33, 200, 256), (64, 5120, 256), (130, 1000, 512), (3100, 264, 4096),
+                                   (2050, 100, 7040)])
+def test_gradients_under_scales_of_every_size(M, N, K, ty):
+    """Scale bytes 0, 1, 252, 253 and 254, in one row of the weights each. Their
+    weights meet gradients that are 0, that take the product back among small
+    integers, that are small integers themselves (products in and beyond float32's
+    range), 2^127 (2^15 in float16) or infinite; nothing is rounded but the output."""
+    ends = (0, 1, 252, 253, 254)
+    codes, scales = grad.weights(N, K, 1, flat=True)
+    g = torch.Generator(device="cuda").manual_seed(N)
+    dy = torch.randint(-4, 5, (M, N), device="cuda", generator=g).double()
+    kind = torch.arange(M, device="cuda") % 5
+    dy[kind >= 2] = 0
+    for i, byte in enumerate(ends):
+        n = (N - 1) * i // 4
+        own = torch.arange(K // 32, device="cuda") % 5 == i
+        codes[n, ~own.repeat_interleave(16)] = 0
+        scales[n, own] = byte
+        v = torch.randint(1, 5, (M,), device="cuda", generator=g).double()
+        v[torch.rand(M, device="cuda", generator=g) < 0.5] *= -1
+        back = 0.0 if ty == "f16" else 2.0 ** (120 if byte < 2 else 127 - byte)
+        most = 2.0 ** (15 if ty == "f16" else 127)
+        size = torch.tensor([0.0, back, 1.0, most, torch.inf], dtype=torch.float64, device="cuda")[kind]
+        dy[:, n] = torch.where(size >= most, size * v.sign(), size * v)
+    dy = dy.to(TYPES[ty])
+    dx = torch.full((M, K), 7.0, dtype=TYPES[ty], device="cuda")
+    pq2.pq2_mx4_gemm_grad(dy, codes, scales, dx)
+    # powers of two from the host: the device's power function is one step off at 2^125
+    powers = torch.from_numpy(np.ldexp(1.0, scales.cpu().numpy().astype(np.int32) - 127)).cuda()
+    values = grad.decoded(codes, torch.full_like(scales, 127)) * powers.repeat_interleave(32, 1)
+    want = (dy.double() @ values).float().to(TYPES[ty])
+    assert ((dx == want) | (dx.isnan() & want.isnan())).all()
+    assert torch.isfinite(want[kind < 2]).all() and torch.isfinite(dx[kind < 2]).all()
