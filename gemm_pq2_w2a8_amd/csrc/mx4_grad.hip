@@ -10,7 +10,8 @@
 // by bfloat16 matrix instructions with float32 sums. d enters without a
 // rounding of its own: bfloat16 as it is, float16 and float32 split into two
 // and three bfloat16 parts that add up to it exactly (truncated, so that no
-// part overflows), which run through the same loop as two or three passes over
+// part overflows; of a float32 below 2^-110 the bits below bfloat16's last, 2^-133,
+// are lost), which run through the same loop as two or three passes over
 // d's tiles beside one expansion of the weights.
 #include <type_traits>
 

@@ -437,8 +437,9 @@ pq2_status pq2_mx4_gated(const uint8_t *a, const uint8_t *ascale, const uint8_t 
  * The gradient of pq2_mx4_gemm's input, dx[m][k] = sum_n dy[m][n] w[n][k], with
  * respect to the values that a's codes stand for (a quantiser in front passes
  * it on unchanged). The weights are frozen: they have no gradient. Weights are
- * exact under every scale byte, dy enters the products unrounded, sums are
- * float32 in a fixed order, dx is rounded once.
+ * exact under every scale byte, dy enters the products unrounded (but for
+ * float32 values below 2^-110, which are cut off at bfloat16's last bit, 2^-133),
+ * sums are float32 in a fixed order, dx is rounded once.
  *   dy, dx   [M][N], 16-byte aligned, and [M][K], both of `format`;
  *   workspace  16-byte aligned; pq2_mx4_grad_workspace_bytes(M, N, K, format)
  *            bytes run the fastest plan. Without partial sums the least is none

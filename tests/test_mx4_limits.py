@@ -101,3 +101,32 @@ def test_gradients_under_scales_of_every_size(M, N, K, ty):
     want = (dy.double() @ values).float().to(TYPES[ty])
     assert ((dx == want) | (dx.isnan() & want.isnan())).all()
     assert torch.isfinite(want[kind < 2]).all() and torch.isfinite(dx[kind < 2]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("byte", [127, 252])
+@pytest.mark.parametrize("ty", ["bf16", "f16", "f32"])
+def test_the_smallest_gradients(ty, byte):
+    """One weight a column, 1 or 2^125: dx is dy itself, subnormals too. Of float32
+    below 2^-110 (the three parts' last bit there: 2^(-110 - 23) = 2^-133) what lies
+    below 2^-133 is cut off, and nothing else."""
+    N = K = 128
+    codes = torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda")
+    for n in range(N):
+        codes[n, n // 2] = 2 << (4 * (n % 2))            # 1.0
+    scales = torch.full((N, K // 32), byte, dtype=torch.uint8, device="cuda")
+    g = torch.Generator().manual_seed(4)
+    sign, frac, power = (torch.randint(0, n, (500, N), generator=g) for n in (2, 1 << 23, 24))
+    if ty == "f32":
+        dy = (frac | power << 23).to(torch.int32).view(torch.float32)
+    else:
+        dy = (frac & 0x3ff if ty == "f16" else frac & 0x7f | power << 7).to(torch.int16).view(TYPES[ty])
+    dy = torch.where(sign == 1, -dy, dy)
+    dx = torch.empty(500, K, dtype=TYPES[ty], device="cuda")
+    pq2.pq2_mx4_gemm_grad(dy.cuda(), codes, scales, dx)
+    want = dy.double()
+    if ty == "f32":
+        cut = torch.trunc(want * 2.0 ** 133) * 2.0 ** -133
+        assert (cut == want)[want.abs() >= 2.0 ** -110].all() and (cut != want).any()
+        want = cut
+    assert torch.equal(dx.cpu(), (want * 2.0 ** (byte - 127)).to(TYPES[ty]))
