@@ -583,7 +583,7 @@ void mx4_wide_kernel(Mx4Args a, MxPlan plan) {
 
 // ---------------------------------------------------------------- few tokens
 //
-// Up to 16 TT tokens a block: bound by the weights' bytes. A block takes `rows`
+// Up to 16 TT tokens in all: bound by the weights' bytes. A block takes `rows`
 // weight rows (gated: that many of gate and of up), a multiple of four chosen so
 // that the blocks fill the compute units evenly, and its waves share the runs of
 // 512 along K: their sums meet in LDS and are added in the order of K. A wave
@@ -601,7 +601,7 @@ void mx4_wide_kernel(Mx4Args a, MxPlan plan) {
 // start and end of the blocks count as much.
 struct MxThin {
     int rows;                         // of a block
-    int tokens4;                      // copies that hold a block's tokens, four each
+    int tokens4;                      // copies that hold the tokens, four each
 };
 
 template <int NI, int TT, bool GATED>
@@ -612,13 +612,13 @@ __global__ __launch_bounds__(1024) void mx4_thin_kernel(Mx4Args a, MxThin plan) 
     const int waves = blockDim.x >> 6;
     const int r = lane & 15, lg = lane >> 4;
     constexpr int kHalves = GATED ? 2 : 1;
-    const int64_t n0 = (int64_t)blockIdx.x * plan.rows, m0 = (int64_t)blockIdx.y * (16 * TT);
+    const int64_t n0 = (int64_t)blockIdx.x * plan.rows;
     const int kb = (int)(a.K / 2), sb = (int)(a.K / kMxBlock);
     const int steps = (int)(a.K / 128), runs = (steps + 3) / 4;
     const int q0 = __builtin_amdgcn_readfirstlane((int)((uint32_t)runs * wave / waves));
     const int q1 = __builtin_amdgcn_readfirstlane((int)((uint32_t)runs * (wave + 1) / waves));
     const int rows_n = (int)(a.N - n0 < plan.rows ? a.N - n0 : plan.rows);
-    const int rows_m = (int)(a.M - m0 < 16 * TT ? a.M - m0 : 16 * TT);
+    const int rows_m = (int)a.M;
     uint8_t *const mine = smem + wave * 256 * (kHalves * plan.rows + 4 * plan.tokens4);
     uint8_t *const mine_x = mine + 256 * kHalves * plan.rows;
 
@@ -661,7 +661,7 @@ __global__ __launch_bounds__(1024) void mx4_thin_kernel(Mx4Args a, MxThin plan) 
 #pragma unroll
         for (int h = 0; h < kHalves; ++h)
             copies(a.w + (n0 + h * a.N) * kb, rows_n, plan.rows / 4, mine + 256 * h * plan.rows, q);
-        copies(a.a + m0 * kb, rows_m, plan.tokens4, mine_x, q);
+        copies(a.a, rows_m, plan.tokens4, mine_x, q);
         v4u sw[NI], sx[TT];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
@@ -670,7 +670,7 @@ __global__ __launch_bounds__(1024) void mx4_thin_kernel(Mx4Args a, MxThin plan) 
             sw[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(
                 rs, row < rows_n ? row * sb + 16 * q : kCopyOob, 0, 0));
         }
-        const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.as + m0 * sb, (int64_t)rows_m * sb);
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.as, (int64_t)rows_m * sb);
 #pragma unroll
         for (int j = 0; j < TT; ++j)
             sx[j] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(
@@ -724,7 +724,7 @@ __global__ __launch_bounds__(1024) void mx4_thin_kernel(Mx4Args a, MxThin plan) 
         for (int o = 1; o < waves; ++o)
 #pragma unroll
             for (int i = 0; i < kEach; ++i) v[i][0] += sums[((o * NI + i0 + i) * TT + j) * kWave + lane];
-        finish<kEach, 1, GATED>(a, v, n0 + 16 * i0, m0 + 16 * j + r, n0 + rows_n, lane);
+        finish<kEach, 1, GATED>(a, v, n0 + 16 * i0, 16 * j + r, n0 + rows_n, lane);
     }
 }
 
@@ -756,21 +756,21 @@ hipError_t run_tiles(const Mx4Args &a, bool gated, const MxPlan &p, void *work, 
 
 template <int NI, int TT, bool GATED>
 hipError_t launch_thin(const Mx4Args &a, int rows, hipStream_t stream) {
-    const int64_t blocks = (a.N + rows - 1) / rows, tokens = (a.M + 16 * TT - 1) / (16 * TT);
+    const int64_t blocks = (a.N + rows - 1) / rows;
     MxThin plan;
     plan.rows = rows;
-    plan.tokens4 = (int)((a.M < 16 * TT ? a.M : 16 * TT) + 3) / 4;
+    plan.tokens4 = (int)(a.M + 3) / 4;
     // as many waves as LDS holds (two blocks a unit unless each has its own),
     // the runs dealt evenly
     const int64_t bytes = 256 * ((GATED ? 2 : 1) * rows + 4 * plan.tokens4);
     const int64_t sums = NI * TT * 1024, piece = bytes > sums ? bytes : sums;
     const int64_t runs = (a.K + 511) / 512;
-    int64_t most = (blocks * tokens > 256 ? 80 * 1024 : 160 * 1024) / piece;
+    int64_t most = (blocks > 256 ? 80 * 1024 : 160 * 1024) / piece;
     most = most > 16 ? 16 : most;
     const int64_t each = (runs + most - 1) / most;
     const int waves = (int)((runs + each - 1) / each);
-    hipLaunchKernelGGL((mx4_thin_kernel<NI, TT, GATED>), dim3((unsigned)blocks, (unsigned)tokens),
-                       dim3((unsigned)(kWave * waves)), (size_t)(waves * piece), stream, a, plan);
+    hipLaunchKernelGGL((mx4_thin_kernel<NI, TT, GATED>), dim3((unsigned)blocks), dim3((unsigned)(kWave * waves)),
+                       (size_t)(waves * piece), stream, a, plan);
     return hipGetLastError();
 }
 
