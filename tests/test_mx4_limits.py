@@ -17,6 +17,16 @@ import test_mx4_grad as grad  # noqa: E402
 TYPES, ACTS = grad.TYPES, grad.ACTS
 
 
+def test_workspace_query_at_the_width_limits():
+    """A gated block's rows are both halves: the width a product still takes, and
+    splits, is refused for it and taken at half."""
+    f, K = pq2.lib.pq2_mx4_workspace_bytes, 1 << 14
+    for rows in (1 << 20) + 128, (1 << 20) + 64:
+        assert f(64, rows, K, 0) > 0 and f(64, rows, K, 1) == 0
+        assert f(64, rows // 2, K, 1) == f(64, rows, K, 0)
+    assert f(64, (1 << 21) + 1, K, 0) == 0
+
+
 def gated_grad(dh, gu, act, w):
     F = dh.shape[1]
     dx = torch.full((len(dh), 2 * w[0].shape[1]), 7.0, dtype=dh.dtype, device="cuda")
