@@ -634,7 +634,7 @@ hipError_t launch_rows(const Mx4GradArgs &a, void *dgu, uint16_t *out, int64_t c
 
 template <int FMT>
 hipError_t run_rows(const Mx4GradArgs &a, void *dgu, uint16_t *out, int64_t cols, hipStream_t stream) {
-    const bool eight = (a.gu ? a.N / 2 : a.N) % 8 == 0;     // bases are 16-byte aligned, cols whole stages
+    const bool eight = (a.gu ? a.N / 2 : a.N) % 8 == 0;     // then bases are 16-byte aligned; cols are whole stages
     if (a.gu)
         return eight ? launch_rows<FMT, true, 8>(a, dgu, out, cols, stream)
                      : launch_rows<FMT, true, 1>(a, dgu, out, cols, stream);

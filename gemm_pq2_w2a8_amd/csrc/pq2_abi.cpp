@@ -45,6 +45,10 @@ pq2_status check_mx4(int64_t M, int64_t N, int64_t K, bool gated) {
     return PQ2_OK;
 }
 
+// Alignment of an array of a format: its elements', and where the kernels take rows of
+// `cols` eight columns at a time, 16 bytes.
+uintptr_t rows_align(int64_t cols, int format) { return cols % 8 == 0 ? 16 : format == PQ2_ACT_F32 ? 4 : 2; }
+
 bool finite32(float v) { return v - v == 0.0f; }
 
 pq2_status from_hip(hipError_t e) { return e == hipSuccess ? PQ2_OK : PQ2_ERR_HIP; }
@@ -475,7 +479,7 @@ pq2_status pq2_mx4_gemm_grad(const void *dy, const uint8_t *w, const uint8_t *ws
     const pq2_status st = check_mx4(M, N, K, false);
     if (st != PQ2_OK) return st;
     if (!known_format(format)) return PQ2_ERR_ARG;
-    if (!aligned(dy, 16) || !aligned(w, 16) || !aligned(wscale, 4) ||
+    if (!aligned(dy, rows_align(N, format)) || !aligned(w, 16) || !aligned(wscale, 4) ||
         !aligned(dx, format == PQ2_ACT_F32 ? 4 : 2) || !aligned(workspace, 16))
         return PQ2_ERR_ALIGN;
     const size_t bytes = workspace ? workspace_bytes : 0;
@@ -500,8 +504,10 @@ pq2_status pq2_mx4_gated_grad(const void *dh, const void *gu, int act, const uin
     if (st != PQ2_OK) return st;
     if (!known_format(format) || act < PQ2_GATE_SILU || act > PQ2_GATE_GELU_TANH)
         return PQ2_ERR_ARG;
-    if (!aligned(dh, 16) || !aligned(gu, 16) || !aligned(dgu, 16) || !aligned(w, 16) ||
-        !aligned(wscale, 4) || !aligned(dx, format == PQ2_ACT_F32 ? 4 : 2) || !aligned(workspace, 16))
+    // (bfloat16 dgu is read in place, by eight of its 2 F columns)
+    if (!aligned(dh, rows_align(F, format)) || !aligned(gu, rows_align(F, format)) ||
+        !aligned(dgu, rows_align(2 * F, format)) || !aligned(w, 16) || !aligned(wscale, 4) ||
+        !aligned(dx, format == PQ2_ACT_F32 ? 4 : 2) || !aligned(workspace, 16))
         return PQ2_ERR_ALIGN;
     const size_t bytes = workspace ? workspace_bytes : 0;
     if (bytes < pq2::mx4_grad_least_bytes(M, 2 * F, format, true, dgu != nullptr))

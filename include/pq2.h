@@ -440,7 +440,9 @@ pq2_status pq2_mx4_gated(const uint8_t *a, const uint8_t *ascale, const uint8_t 
  * exact under every scale byte, dy enters the products unrounded (but for
  * float32 values below 2^-110, which are cut off at bfloat16's last bit, 2^-133),
  * sums are float32 in a fixed order, dx is rounded once.
- *   dy, dx   [M][N], 16-byte aligned, and [M][K], both of `format`;
+ *   dy, dx   [M][N] and [M][K], both of `format`; dy 16-byte aligned where N is a
+ *            multiple of 8, else as its elements (rows of an odd width may start
+ *            anywhere), dx as its elements;
  *   workspace  16-byte aligned; pq2_mx4_grad_workspace_bytes(M, N, K, format)
  *            bytes run the fastest plan. Without partial sums the least is none
  *            for PQ2_ACT_BF16 with N a multiple of 8; else dy's bfloat16 parts
@@ -459,8 +461,9 @@ pq2_status pq2_mx4_gemm_grad(const void *dy, const uint8_t *w, const uint8_t *ws
  *   dg = dh * u * act'(g),   du = dh * act(g),   dx = dg Wg + du Wu.
  * dg and du are rounded to `format`, where a projection's adapter reads them,
  * and multiply the weights as rounded.
- *   dh, gu, dgu  [M][F], [M][2F], [M][2F], 16-byte aligned; dx [M][K]; all of
- *            `format`. dgu may be gu itself, or NULL (then the workspace holds
+ *   dh, gu, dgu, dx  [M][F], [M][2F], [M][2F], [M][K], all of `format`: dh and gu
+ *            16-byte aligned where F is a multiple of 8, dgu where 2F is, else as
+ *            their elements, like dx. dgu may be gu itself, or NULL (then the workspace holds
  *            it where the products read it in place);
  *   workspace  pq2_mx4_gated_grad_workspace_bytes(M, F, K, format, dgu != NULL)
  *            bytes run the fastest plan; the least is that of pq2_mx4_gemm_grad

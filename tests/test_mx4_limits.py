@@ -140,3 +140,57 @@ def test_the_smallest_gradients(ty, byte):
         assert (cut == want)[want.abs() >= 2.0 ** -110].all() and (cut != want).any()
         want = cut
     assert torch.equal(dx.cpu(), (want * 2.0 ** (byte - 127)).to(TYPES[ty]))
+
+
+@pytest.mark.parametrize("kw,want", [
+    # rows of 13 columns: the elements' alignment (then the workspace is too small)
+    (dict(dy=grad.P + 4, fmt=0, N=13), grad.ERR_SCRATCH), (dict(dy=grad.P + 2, fmt=1, N=13), grad.ERR_SCRATCH),
+    (dict(dy=grad.P + 2, fmt=2, N=13), grad.ERR_SCRATCH), (dict(dy=grad.P + 2, fmt=0, N=13), grad.ERR_ALIGN),
+    (dict(dy=grad.P + 1, fmt=1, N=13), grad.ERR_ALIGN), (dict(dy=grad.P + 4, fmt=0, N=16), grad.ERR_ALIGN),
+])
+def test_alignment_of_odd_rows(kw, want):
+    assert grad.gemm_grad(size=0, **kw) == want
+    assert grad.gated_grad(size=0, **kw) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(gu=grad.P + 4, N=13), grad.ERR_SCRATCH), (dict(gu=grad.P + 2, N=13), grad.ERR_ALIGN),
+    (dict(dgu=grad.P + 4, N=13), grad.ERR_SCRATCH), (dict(dgu=grad.P + 2, N=13), grad.ERR_ALIGN),
+    # 12 columns, and 24 of both halves
+    (dict(dy=grad.P + 4, gu=grad.P + 4, N=12), grad.ERR_SCRATCH), (dict(dgu=grad.P + 4, N=12), grad.ERR_ALIGN),
+])
+def test_alignment_of_odd_rows_of_the_gated_block(kw, want):
+    assert grad.gated_grad(fmt=0, size=0, **kw) == want
+
+
+def off_by_one(t):
+    """The same rows, one element past an aligned address."""
+    buf = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+    buf[1:] = t.flatten()
+    return buf[1:].view(t.shape)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ty", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(1, 7, 128), (33, 100, 256), (130, 1411, 384), (3100, 260, 4096)])
+def test_gradients_of_odd_rows_from_any_element(M, N, K, ty):
+    w, dy = grad.weights(N, K, 1), grad.randn(M, N, ty, 1)
+    dx, other = (torch.full((M, K), 7.0, dtype=TYPES[ty], device="cuda") for _ in range(2))
+    pq2.pq2_mx4_gemm_grad(dy, *w, dx)
+    pq2.pq2_mx4_gemm_grad(off_by_one(dy), *w, other)
+    assert torch.equal(dx, other)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ty", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M,F,K", [(1, 7, 128), (33, 100, 256), (130, 1411, 384)])
+def test_gated_gradients_of_odd_rows_from_any_element(M, F, K, ty):
+    w, dh, gu = grad.weights(2 * F, K, 1), grad.randn(M, F, ty, 1), grad.randn(M, 2 * F, ty, 2)
+    dx, dgu = gated_grad(dh, gu, "silu", w)
+    other = torch.full_like(dx, 7.0)
+    pq2.pq2_mx4_gated_grad(off_by_one(dh), off_by_one(gu), *w, other)
+    assert torch.equal(dx, other)
+    if F % 4:
+        odd = off_by_one(gu)                             # and dgu in its place
+        pq2.pq2_mx4_gated_grad(dh, odd, *w, other, dgu=odd)
+        assert torch.equal(dx, other) and torch.equal(odd, dgu)
