@@ -608,7 +608,8 @@ def pq2_mx4_gated_grad(dh: torch.Tensor, gu: torch.Tensor, w: torch.Tensor, wsca
                        workspace="auto", stream=None) -> None:
     """Backward pass of pq2_mx4_gated: from dh [M][F] and the gu [M][2F] it
     stored, dgu [M][2F] = (dh u act'(g) | dh act(g)) and dx [M][K] = dgu w; all of
-    dh's type. dgu may be gu itself, or None (not returned). workspace as for
+    dh's type, to which dgu is rounded before it multiplies w. dgu may be gu itself,
+    or None (not returned, dx the same). workspace as for
     pq2_mx4_gemm_grad, sized by mx4_gated_grad_workspace_bytes."""
     kind = _gate_act(act)
     fmt = _format(dh, "dh")

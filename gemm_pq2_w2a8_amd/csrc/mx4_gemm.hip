@@ -816,9 +816,11 @@ MxKind choose_tile(int64_t M, int64_t N, int64_t K, bool gated, size_t bytes, Mx
     return kind;
 }
 
-// Up to 16 tokens, and up to 32 where 64 x 64 tiles are few: a gated block of 17408
-// columns takes 24.0 us this way at 32 tokens and 21 in tiles, 5120 x 17408 13.5
-// and 20.
+// Up to 16 tokens, and up to 32 where 64 x 64 tiles are fewer than two a compute
+// unit. Both ways at 17 and 32 tokens, 1411 to 65536 rows and K of 896, 5120 and 17408
+// (us at 32): 5120 x 17408 13.8 this way and 18.1 in tiles, 17408 x 5120 15.6 and 16.6,
+// 24576 x 17408 61.5 and 55.7, 34816 x 5120 23.5 and 21.7 (gated 29.4 and 31.6), 65536 x
+// 17408 143 and 128; the rule takes the faster one or one within 17 %.
 bool takes_thin(int64_t M, int64_t N, bool gated) {
     return M <= 16 || (M <= 32 && (gated ? 2 * N : N) < 64 * 512);
 }

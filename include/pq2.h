@@ -460,7 +460,7 @@ pq2_status pq2_mx4_gemm_grad(const void *dy, const uint8_t *w, const uint8_t *ws
  * The gated block's backward pass, from the g and u that pq2_mx4_gated stored:
  *   dg = dh * u * act'(g),   du = dh * act(g),   dx = dg Wg + du Wu.
  * dg and du are rounded to `format`, where a projection's adapter reads them,
- * and multiply the weights as rounded.
+ * and multiply the weights as rounded, with or without dgu.
  *   dh, gu, dgu, dx  [M][F], [M][2F], [M][2F], [M][K], all of `format`: dh and gu
  *            16-byte aligned where F is a multiple of 8, dgu where 2F is, else as
  *            their elements, like dx. dgu may be gu itself, or NULL (then the workspace holds
