@@ -386,8 +386,8 @@ __global__ __launch_bounds__(L::T) void mx4_tile_kernel(Mx4Args a, MxPlan plan) 
 // follow.
 // Each copy has a resource of its own, the eight rows that it fills as far as
 // they exist, so that one lane offset serves all of them.
-// 4096 x 5120 x 17408 185 us (3.9 PFLOP/s) and 11 of sums; gated 2048 x 17408 x 5120
-// 212 us (3.4), 280 with g and u written. With 128 x 128 tiles 276 and 310. The same
+// 4096 x 5120 x 17408 185 to 194 us by the clock (3.9 PFLOP/s) and 11 of sums; gated
+// 2048 x 17408 x 5120 212 us (3.4), 280 with g and u written. With 128 x 128 tiles 276 and 310. The same
 // loop without its copies reaches 4.9, matrix instructions alone on random operands
 // 6.2 to 6.9 (the clock falls to 1.7 GHz; 8.6 on constant ones): the copies' share of
 // the issue and the clock bound it. An epilogue overlaps nothing, a unit has one block.
@@ -803,9 +803,10 @@ typedef MxTile<4, 1, 1, 4> MxSmall;    // 64 x 64
 typedef MxTile<4, 4, 2, 2> MxMid;      // 128 x 128
 
 // The tile for a shape: the least of plan_tiles's counts. (Measured at 33 to 4096
-// tokens, N x K 5120 x 17408, 17408 x 5120, 6144 x 5120, 17408 x 1024 and 1411 x
-// 896, each tile in 1 to 16 ways: the count takes the fastest or one within a
-// tenth of it.)
+// tokens, N x K 5120 x 17408, 17408 x 5120, plain and gated, 6144 x 5120, 17408 x 1024
+// and 1411 x 896, each tile in 1 to 16 ways: what the count takes is within 8 % of the
+// fastest but at 1024 x 5120 x 17408, 74.5 us whole in 128 x 128 where 256 x 256 in two
+// ways takes 64.7.)
 enum class MxKind { kSmall, kMid, kWide };
 MxKind choose_tile(int64_t M, int64_t N, int64_t K, bool gated, size_t bytes, MxPlan &plan) {
     const int64_t rows = gated ? 2 * N : N, runs = (K + 511) / 512;

@@ -201,8 +201,9 @@ __global__ __launch_bounds__(256) void grad_rows_kernel(const void *dy, const vo
 // tokens rolling, each tile's registers taking the next step's as soon as its
 // products are issued. In the first step of a stage the next stage's tile is
 // stored and the one after requested; a barrier in the second shows it to all.
-// 4096 x 5120 x 17408 bfloat16 573 us with 256 x 256 tiles (1.27 PFLOP/s; a library
-// product of bfloat16 matrices 1.44); 128 x 34816 x 5120 78 with 128 x 64. Every
+// 4096 x 5120 x 17408 bfloat16 576 to 600 us by the clock with 256 x 256 tiles (1.2 to
+// 1.27 PFLOP/s; a library product of bfloat16 matrices 1.37 to 1.44); 128 x 34816 x 5120
+// 82 with 128 x 64. Every
 // other instruction shares the SIMD's issue with the matrix instructions: the loop of
 // waves of 64 columns x half the tokens, with parts left out, took 358 us for those
 // alone, 99 more with the conversions, 31 with the reads of d, 40 with the stores to
